@@ -12,10 +12,15 @@ from __future__ import annotations
 __all__ = [
     "gdn_chunk_fwd", "gdn_build_chunk_indices", "gdn_workspace_size",
     "gdn_read_status", "gdn_status_string", "GdnError", "load_library",
+    "gdn_attn_front", "gdn_attn_prefill", "gdn_attn_decode", "gdn_attn_workspace_size",
+    "rope_table",
 ]
 
 
 def __getattr__(name):
+    if name == "rope_table":
+        from .rope import rope_table
+        return rope_table
     if name in __all__:
         from . import binding
         return getattr(binding, name)

@@ -26,16 +26,20 @@ GDN_FLAG_WORKSPACE_GUARDS = 8
 GDN_NUM_STAGE_EVENTS = 5
 DEV_STATUS_BITS = {1: "bad cu_seqlens", 2: "chunk overflow", 4: "bad chunk table",
                    8: "on-chip wait timed out", 16: "non-finite state or output",
-                   32: "index out of range (GDN_DEBUG build)"}
+                   32: "index out of range (GDN_DEBUG build)", 64: "bad page table",
+                   128: "bad length or position"}
 GDN_DEV_DEBUG_INDEX = 32
 
-# Every entry point include/gdn.h declares.
+# Every entry point include/gdn.h and include/gdn_attn.h declare.
 EXPORTED = ("gdn_check_desc", "gdn_nt_max", "gdn_workspace_size", "gdn_build_chunk_indices",
             "gdn_chunk_fwd", "gdn_read_status", "gdn_status_string", "gdn_chunk_fwd_noalloc",
             "gdn_noalloc_read_status", "gdn_test_scan_timeout", "gdn_workspace_regions",
             "gdn_debug_build", "gdn_test_debug_poison",
-            "gdn_recurrent_fwd", "gdn_conv_front", "gdn_bwd_workspace_size", "gdn_chunk_bwd")
+            "gdn_recurrent_fwd", "gdn_conv_front", "gdn_bwd_workspace_size", "gdn_chunk_bwd",
+            "gdn_attn_check_desc", "gdn_attn_workspace_size", "gdn_attn_front",
+            "gdn_attn_prefill", "gdn_attn_decode")
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
+GDN_ATTN_ROPE_INTERLEAVED = 1
 
 
 class GdnError(RuntimeError):
@@ -53,6 +57,17 @@ class GdnDesc(ctypes.Structure):
                 ("flags", ctypes.c_uint32), ("l2norm_eps", ctypes.c_float),
                 ("workspace", ctypes.c_void_p), ("workspace_bytes", ctypes.c_size_t),
                 ("stage_events", ctypes.c_void_p)]
+
+
+class GdnAttnDesc(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("N", ctypes.c_int32), ("H", ctypes.c_int32),
+                ("Hk", ctypes.c_int32), ("D", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("n_pages", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("rot_dim", ctypes.c_int32), ("max_pos", ctypes.c_int32),
+                ("in_dtype", ctypes.c_int32), ("out_dtype", ctypes.c_int32),
+                ("flags", ctypes.c_uint32), ("norm_eps", ctypes.c_float),
+                ("status", ctypes.c_void_p), ("workspace", ctypes.c_void_p),
+                ("workspace_bytes", ctypes.c_size_t)]
 
 
 _lock = threading.Lock()
@@ -103,6 +118,18 @@ def load_library(path: str = LIB_PATH):
         lib.gdn_chunk_bwd.argtypes = [P(GdnDesc), vp, vp, vp, vp, vp, ctypes.c_float, vp, vp,
                                       vp, vp, vp, vp, vp, vp, vp, vp, vp, vp]
         lib.gdn_chunk_bwd.restype = ctypes.c_int
+        lib.gdn_attn_check_desc.argtypes = [P(GdnAttnDesc)]
+        lib.gdn_attn_check_desc.restype = ctypes.c_int
+        lib.gdn_attn_workspace_size.argtypes = [P(GdnAttnDesc)]
+        lib.gdn_attn_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_attn_front.argtypes = [P(GdnAttnDesc)] + [vp] * 13
+        lib.gdn_attn_front.restype = ctypes.c_int
+        lib.gdn_attn_prefill.argtypes = [P(GdnAttnDesc), vp, vp, vp, vp, ctypes.c_float, vp, vp,
+                                         vp]
+        lib.gdn_attn_prefill.restype = ctypes.c_int
+        lib.gdn_attn_decode.argtypes = [P(GdnAttnDesc), vp, vp, vp, vp, vp, i32, ctypes.c_float,
+                                        vp, vp, vp]
+        lib.gdn_attn_decode.restype = ctypes.c_int
         lib.gdn_read_status.argtypes = [P(GdnDesc), vp, vp]
         lib.gdn_read_status.restype = ctypes.c_int
         lib.gdn_status_string.argtypes = [ctypes.c_int]
@@ -459,3 +486,181 @@ def gdn_workspace_regions(desc: GdnDesc):
     if n < 0:
         raise GdnError(n, "gdn_workspace_regions")
     return [(int(b[i]), int(e[i])) for i in range(n)]
+
+
+# ---------------------------------------------------------------- softmax attention
+_DTYPE_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+
+
+def make_attn_desc(T: int, N: int, H: int, Hk: int, D: int, in_dtype: torch.dtype = torch.bfloat16,
+                   out_dtype: Optional[torch.dtype] = None, page_size: int = 0, n_pages: int = 0,
+                   max_pages: int = 0, rot_dim: int = 0, max_pos: int = 0, flags: int = 0,
+                   norm_eps: float = 0.0) -> GdnAttnDesc:
+    return GdnAttnDesc(T, N, H, Hk, D, page_size, n_pages, max_pages, rot_dim, max_pos,
+                       _dtype_code(in_dtype), _dtype_code(out_dtype or in_dtype), flags, norm_eps,
+                       None, None, 0)
+
+
+def gdn_attn_check_desc(desc: GdnAttnDesc) -> int:
+    return load_library().gdn_attn_check_desc(ctypes.byref(desc))
+
+
+def gdn_attn_workspace_size(desc: GdnAttnDesc) -> int:
+    return int(load_library().gdn_attn_workspace_size(ctypes.byref(desc)))
+
+
+def _addr(t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype] = None,
+          shape: Optional[tuple] = None) -> Optional[int]:
+    """Device address of an optional contiguous CUDA tensor of this dtype and shape."""
+    if t is None:
+        return None
+    if not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if shape is not None and t.shape != shape:
+        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _num_seqs(cu_seqlens: Optional[torch.Tensor]) -> int:
+    if cu_seqlens is None:
+        return 1
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
+        raise ValueError("cu_seqlens must have shape [N + 1] with N >= 1")
+    return cu_seqlens.shape[0] - 1
+
+
+def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
+                   q_weight: Optional[torch.Tensor] = None,
+                   k_weight: Optional[torch.Tensor] = None, norm_eps: float = 0.0,
+                   rope: Optional[torch.Tensor] = None, interleaved: bool = False,
+                   cu_seqlens: Optional[torch.Tensor] = None,
+                   kv_lens: Optional[torch.Tensor] = None,
+                   page_table: Optional[torch.Tensor] = None,
+                   k_cache: Optional[torch.Tensor] = None, v_cache: Optional[torch.Tensor] = None,
+                   output_kv: bool = True, out_dtype: Optional[torch.dtype] = None,
+                   q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
+                   v: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
+                   stream=None):
+    """Front end of an attention layer through the C ABI.
+
+    x [T, (H + 2 Hk) * D] (fp32 or bf16), channels q | k | v. Per head of q and k: RMS norm
+    with q_weight / k_weight (fp32 [D]; None leaves that norm out), then the rotation of the
+    first rope.shape[1] elements by the rows of `rope` (fp32 [max_pos, rot], see
+    rope.rope_table) at the token's position. With page_table [N, max_pages] int32, k_cache
+    and v_cache [n_pages, Hk, page_size, D], k and v are appended to the cache; kv_lens [N]
+    int32 are the cache's lengths after that (None: the tokens are the sequence's first).
+    Returns (q [T, H, D], k, v [T, Hk, D]), the last two None when output_kv is false.
+    `status`, if given, is one int32 on the device that receives the device status word.
+    """
+    T = x.shape[0]
+    dev = x.device
+    N = _num_seqs(cu_seqlens)
+    if out_dtype is None:
+        out_dtype = k_cache.dtype if k_cache is not None else q.dtype if q is not None else x.dtype
+    if x.dtype not in _DTYPE_CODES or out_dtype not in _DTYPE_CODES:
+        raise TypeError(f"unsupported dtype {x.dtype} -> {out_dtype}")
+    if q is None:
+        q = torch.empty((T, H, D), dtype=out_dtype, device=dev)
+    if output_kv:
+        if k is None:
+            k = torch.empty((T, Hk, D), dtype=out_dtype, device=dev)
+        if v is None:
+            v = torch.empty((T, Hk, D), dtype=out_dtype, device=dev)
+    else:
+        k = v = None
+    max_pos, rot = (0, 0) if rope is None else rope.shape
+    n_pages = page = max_pages = 0
+    if k_cache is not None:
+        if k_cache.dim() != 4 or page_table is None or page_table.dim() != 2:
+            raise ValueError("the cache needs k_cache, v_cache [n_pages, Hk, page_size, D] and "
+                             "page_table [N, max_pages]")
+        n_pages, page, max_pages = k_cache.shape[0], k_cache.shape[2], page_table.shape[1]
+    desc = GdnAttnDesc(T, N, H, Hk, D, page, n_pages, max_pages, rot, max_pos,
+                       _DTYPE_CODES[x.dtype], _DTYPE_CODES[out_dtype],
+                       GDN_ATTN_ROPE_INTERLEAVED if interleaved else 0, norm_eps,
+                       _addr(status, "status", torch.int32), None, 0)
+    cache_shape = (n_pages, Hk, page, D)
+    rc = load_library().gdn_attn_front(
+        ctypes.byref(desc), _addr(x, "x", None, (T, (H + 2 * Hk) * D)),
+        _addr(q_weight, "q_weight", torch.float32, (D,)),
+        _addr(k_weight, "k_weight", torch.float32, (D,)), _addr(rope, "rope", torch.float32),
+        _addr(cu_seqlens, "cu_seqlens", torch.int32), _addr(kv_lens, "kv_lens", torch.int32, (N,)),
+        _addr(page_table, "page_table", torch.int32, (N, max_pages)),
+        _addr(q, "q", out_dtype, (T, H, D)), _addr(k, "k", out_dtype, (T, Hk, D)),
+        _addr(v, "v", out_dtype, (T, Hk, D)), _addr(k_cache, "k_cache", out_dtype, cache_shape),
+        _addr(v_cache, "v_cache", out_dtype, cache_shape), _stream_handle(stream))
+    if rc != 0:
+        raise GdnError(rc, "gdn_attn_front")
+    return q, k, v
+
+
+def gdn_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
+                     cu_seqlens: Optional[torch.Tensor] = None, scale: Optional[float] = None,
+                     out_dtype: Optional[torch.dtype] = None, out: Optional[torch.Tensor] = None,
+                     return_lse: bool = False, lse: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None):
+    """Causal attention of packed prompts through the C ABI: q [T, H, D], k, v [T, Hk, D]
+    bf16, D = 128 or 64, H a multiple of Hk; cu_seqlens int32 [N + 1] or None (one
+    sequence). Returns out [T, H, D], or (out, lse) with lse fp32 [T, H] when return_lse."""
+    T, H, D = q.shape
+    Hk = k.shape[1]
+    N = _num_seqs(cu_seqlens)
+    if out is None:
+        out = torch.empty((T, H, D), dtype=out_dtype or q.dtype, device=q.device)
+    if return_lse and lse is None:
+        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
+    desc = GdnAttnDesc(T, N, H, Hk, D, 0, 0, 0, 0, 0, _dtype_code(q.dtype), _dtype_code(out.dtype),
+                       0, 0.0, _addr(status, "status", torch.int32), None, 0)
+    rc = load_library().gdn_attn_prefill(
+        ctypes.byref(desc), _addr(q, "q"), _addr(k, "k", q.dtype, (T, Hk, D)),
+        _addr(v, "v", q.dtype, (T, Hk, D)), _addr(cu_seqlens, "cu_seqlens", torch.int32),
+        0.0 if scale is None else scale, _addr(out, "out", out_dtype, (T, H, D)),
+        _addr(lse, "lse", torch.float32, (T, H)), _stream_handle(stream))
+    if rc != 0:
+        raise GdnError(rc, "gdn_attn_prefill")
+    return (out, lse) if return_lse else out
+
+
+def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    page_table: torch.Tensor, kv_lens: torch.Tensor, shared_len: int = 0,
+                    scale: Optional[float] = None, out_dtype: Optional[torch.dtype] = None,
+                    out: Optional[torch.Tensor] = None, return_lse: bool = False,
+                    lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                    status: Optional[torch.Tensor] = None, stream=None):
+    """Decode attention over the paged cache through the C ABI: q [N, H, D] (one token a
+    sequence) or [N, n_q, H, D] bf16; k_cache, v_cache [n_pages, Hk, page_size, D] bf16;
+    page_table int32 [N, max_pages]; kv_lens int32 [N], the call's tokens included. The first
+    shared_len tokens (a multiple of page_size) are the same pages for every sequence and are
+    read once for all. `workspace` (uint8, gdn_attn_workspace_size bytes) is allocated when
+    not given. Returns out with q's shape, or (out, lse) when return_lse."""
+    N, H, D = q.shape[0], q.shape[-2], q.shape[-1]
+    nq = 1 if q.dim() == 3 else q.shape[1]
+    n_pages, Hk, page, _ = k_cache.shape
+    if out is None:
+        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
+    if return_lse and lse is None:
+        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
+    desc = GdnAttnDesc(N * nq, N, H, Hk, D, page, n_pages, page_table.shape[1], 0, 0,
+                       _dtype_code(q.dtype), _dtype_code(out.dtype), 0, 0.0,
+                       _addr(status, "status", torch.int32), None, 0)
+    lib = load_library()
+    if workspace is None:
+        n = lib.gdn_attn_workspace_size(ctypes.byref(desc))
+        if n == 0:
+            raise GdnError(lib.gdn_attn_check_desc(ctypes.byref(desc)), "gdn_attn_decode")
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    desc.workspace = _addr(workspace, "workspace")
+    desc.workspace_bytes = workspace.numel() * workspace.element_size()
+    cache_shape = (n_pages, Hk, page, D)
+    rc = lib.gdn_attn_decode(
+        ctypes.byref(desc), _addr(q, "q"), _addr(k_cache, "k_cache", q.dtype, cache_shape),
+        _addr(v_cache, "v_cache", q.dtype, cache_shape),
+        _addr(page_table, "page_table", torch.int32, (N, page_table.shape[1])),
+        _addr(kv_lens, "kv_lens", torch.int32, (N,)), shared_len, 0.0 if scale is None else scale,
+        _addr(out, "out", out_dtype, q.shape), _addr(lse, "lse", torch.float32, q.shape[:-1]),
+        _stream_handle(stream))
+    if rc != 0:
+        raise GdnError(rc, "gdn_attn_decode")
+    return (out, lse) if return_lse else out

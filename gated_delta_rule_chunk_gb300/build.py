@@ -42,7 +42,8 @@ def _sources():
 
 def _deps():
     return _sources() + sorted(glob.glob(os.path.join(CSRC, "*.cuh"))) + [
-        os.path.join(PKG, "..", "include", "gdn.h"), os.path.abspath(__file__)]
+        os.path.join(PKG, "..", "include", "gdn.h"),
+        os.path.join(PKG, "..", "include", "gdn_attn.h"), os.path.abspath(__file__)]
 
 
 def up_to_date(lib: str = LIB) -> bool:

@@ -84,9 +84,13 @@ typedef enum gdn_dev_status {
   GDN_DEV_NONFINITE = 16,         /* a state or output of the bf16 tensor-core path came out
                                      non-finite: an fp16 operand (state, decayed v_new) left
                                      the fp16 range, or the inputs held inf/NaN */
-  GDN_DEV_DEBUG_INDEX = 32        /* (GDN_DEBUG builds only) an index that addresses global
+  GDN_DEV_DEBUG_INDEX = 32,       /* (GDN_DEBUG builds only) an index that addresses global
                                      memory in the chunk-table, intra or scan kernel was out of
                                      its range: that access was skipped or redirected */
+  GDN_DEV_BAD_PAGE_TABLE = 64,    /* (gdn_attn.h) a page outside the cache: not written, read
+                                     as zeros */
+  GDN_DEV_BAD_LENGTH = 128        /* (gdn_attn.h) a length or position outside the page table
+                                     or the rotary table: clamped, or not appended */
 } gdn_dev_status;
 
 enum {

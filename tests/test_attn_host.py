@@ -1,0 +1,214 @@
+"""Attention operators on the host: refusals (every call fails before any CUDA call, so no
+GPU is needed), the rotary table, and pins of the oracle."""
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_chunk_gb300 import binding as B
+from gated_delta_rule_chunk_gb300.build import build
+from gated_delta_rule_chunk_gb300.rope import rope_frequencies, rope_table
+from oracle import attention as A
+
+
+@pytest.fixture(scope="module")
+def lib():
+    build()
+    return B.load_library()
+
+
+def desc(**kw):
+    base = dict(T=8, N=4, H=8, Hk=2, D=128, page_size=16, n_pages=9, max_pages=5, rot_dim=64,
+                max_pos=80)
+    base.update(kw)
+    return B.make_attn_desc(**base)
+
+
+@pytest.mark.parametrize("kw, want", [
+    ({}, 0), (dict(D=64), 0), (dict(T=0), 0), (dict(page_size=0), 0), (dict(rot_dim=0), 0),
+    (dict(page_size=256), 0), (dict(in_dtype=torch.float32), 0),
+    (dict(T=-1), -2), (dict(N=0), -2), (dict(H=0), -2), (dict(Hk=0), -2), (dict(H=9), -2),
+    (dict(n_pages=-1), -2), (dict(max_pages=-1), -2), (dict(rot_dim=-16), -2),
+    (dict(rot_dim=144), -2), (dict(max_pos=-1), -2), (dict(page_size=-16), -2),
+    (dict(max_pages=1 << 27), -2), (dict(T=1 << 30), -2),
+    (dict(D=96), -3), (dict(D=256, rot_dim=0), -3), (dict(rot_dim=24), -3), (dict(page_size=48), -3),
+    (dict(page_size=8), -3), (dict(page_size=512), -3), (dict(H=130, Hk=2), -3), (dict(flags=2), -3),
+])
+def test_check_desc(lib, kw, want):
+    assert B.gdn_attn_check_desc(desc(**kw)) == want
+    if want == 0 and desc(**kw).T:
+        assert B.gdn_attn_workspace_size(desc(**kw)) > 0
+    elif want:
+        assert B.gdn_attn_workspace_size(desc(**kw)) == 0
+
+
+def test_check_desc_null_and_dtype(lib):
+    assert lib.gdn_attn_check_desc(None) == -1
+    d = desc()
+    d.in_dtype = 5
+    assert B.gdn_attn_check_desc(d) == -3
+    assert B.gdn_attn_workspace_size(desc(T=9)) == 0  # not a multiple of N
+
+
+def call(fn, d, *args):
+    conv = [ctypes.c_void_p(a) if type(a) is int else a for a in args]
+    return fn(ctypes.byref(d), *conv)
+
+
+FRONT = dict(x=16, qw=16, kw=16, rope=16, cu=16, kv=16, table=16, q=16, k=16, v=16, kc=16, vc=16)
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(x=None), -1), (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1),
+    (dict(rope=None), -1), (dict(kc=None), -1), (dict(vc=None), -1), (dict(table=None), -1),
+    (dict(cu=None), -2), (dict(x=24), -4), (dict(qw=8), -4), (dict(rope=20), -4), (dict(q=18), -4),
+    (dict(kc=40), -4), (dict(cu=18), -4), (dict(kv=17), -4), (dict(table=19), -4),
+])
+def test_front_refuses(lib, change, want):
+    a = {**FRONT, **change}
+    assert call(lib.gdn_attn_front, desc(), *a.values(), None) == want
+
+
+def test_front_refuses_by_desc(lib):
+    assert call(lib.gdn_attn_front, desc(page_size=0), *FRONT.values(), None) == -2
+    assert call(lib.gdn_attn_front, desc(max_pos=0), *FRONT.values(), None) == -2
+    assert call(lib.gdn_attn_front, desc(D=32, rot_dim=0), *FRONT.values(), None) == -3
+    assert lib.gdn_attn_front(None, *[ctypes.c_void_p(16)] * 12, None) == -1
+
+
+@pytest.mark.parametrize("change, want", [
+    (dict(q=None), -1), (dict(k=None), -1), (dict(v=None), -1), (dict(out=None), -1),
+    (dict(cu=None), -2), (dict(q=8), -4), (dict(k=17), -4), (dict(v=24), -4), (dict(out=2), -4),
+    (dict(cu=2), -4), (dict(lse=2), -4),
+])
+def test_prefill_refuses(lib, change, want):
+    a = {**dict(q=16, k=16, v=16, cu=16, scale=0.0, out=16, lse=None), **change}
+    a["scale"] = ctypes.c_float(0)
+    assert call(lib.gdn_attn_prefill, desc(), *a.values(), None) == want
+
+
+def test_prefill_refuses_f32(lib):
+    p = ctypes.c_void_p(16)
+    d = desc(in_dtype=torch.float32)
+    assert lib.gdn_attn_prefill(ctypes.byref(d), p, p, p, p, 0.0, p, None, None) == -3
+
+
+@pytest.mark.parametrize("change, kw, want", [
+    (dict(q=None), {}, -1), (dict(kc=None), {}, -1), (dict(vc=None), {}, -1),
+    (dict(table=None), {}, -1), (dict(kv=None), {}, -1), (dict(out=None), {}, -1),
+    (dict(shared=8), {}, -2), (dict(shared=-16), {}, -2), (dict(shared=96), {}, -2),
+    ({}, dict(T=9), -2), ({}, dict(page_size=0), -2), ({}, dict(T=4 * 17), -3),
+    ({}, dict(in_dtype=torch.float32), -3),
+    (dict(q=8), {}, -4), (dict(kc=8), {}, -4), (dict(vc=8), {}, -4), (dict(table=2), {}, -4),
+    (dict(kv=2), {}, -4), (dict(out=8), {}, -4), (dict(lse=2), {}, -4),
+])
+def test_decode_refuses(lib, change, kw, want):
+    a = {**dict(q=16, kc=16, vc=16, table=16, kv=16, shared=0, scale=0, out=16, lse=None), **change}
+    d = desc(**kw)
+    d.workspace = 4096
+    d.workspace_bytes = 1 << 40
+    f = lambda x: None if x is None else ctypes.c_void_p(x)
+    assert lib.gdn_attn_decode(ctypes.byref(d), f(a["q"]), f(a["kc"]), f(a["vc"]), f(a["table"]),
+                               f(a["kv"]), a["shared"], 0.0, f(a["out"]), f(a["lse"]), None) == want
+
+
+def test_decode_refuses_workspace(lib):
+    p = ctypes.c_void_p(16)
+    d = desc()
+    run = lambda: lib.gdn_attn_decode(ctypes.byref(d), p, p, p, p, p, 0, 0.0, p, None, None)
+    assert run() == -1
+    d.workspace = 4096
+    d.workspace_bytes = B.gdn_attn_workspace_size(d) - 1
+    assert run() == -5
+    d.workspace = 4096 + 16
+    d.workspace_bytes = 1 << 40
+    assert run() == -4
+
+
+def test_binding_refuses_cpu_tensors_and_shapes():
+    x = torch.zeros(4, 6 * 128)
+    with pytest.raises(ValueError):
+        B.gdn_attn_front(x, 4, 1, 128)
+    with pytest.raises(ValueError):
+        B.gdn_attn_front(x, 4, 1, 128, cu_seqlens=torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        B.gdn_attn_front(x.half(), 4, 1, 128)
+    q = torch.zeros(4, 2, 64, dtype=torch.bfloat16)
+    with pytest.raises(ValueError):
+        B.gdn_attn_prefill(q, q, q)
+
+
+# ---------------------------------------------------------------- rotary table
+def test_rope_table_plain():
+    t = rope_table(50, 8, base=100.0, device="cpu")
+    assert t.shape == (50, 8) and t.dtype == torch.float32
+    for p in (0, 1, 49):
+        for i in range(4):
+            a = p * 100.0 ** (-2 * i / 8)
+            assert abs(t[p, i].item() - np.cos(a)) < 1e-7
+            assert abs(t[p, 4 + i].item() - np.sin(a)) < 1e-7
+
+
+def test_rope_scaling_rules():
+    f = rope_frequencies(64)
+    assert torch.allclose(rope_frequencies(64, linear=4.0), f / 4, rtol=1e-14)
+    n = rope_frequencies(64, ntk=8.0)
+    assert n[0] == f[0] and abs((f[-1] / n[-1]).item() - 8.0) < 1e-9
+    b = rope_frequencies(64, by_parts=(8.0, 4096, 1.0, 32.0))
+    turns = f * 4096 / (2 * np.pi)
+    assert torch.equal(b[turns > 32], f[turns > 32])
+    assert torch.allclose(b[turns < 1], f[turns < 1] / 8, rtol=1e-14)
+    mid = (turns > 1) & (turns < 32)
+    assert mid.any() and ((b[mid] > f[mid] / 8) & (b[mid] < f[mid])).all()
+    assert torch.equal(rope_table(9, 16, magnitude=1.5, device="cpu")[0, :8], torch.full((8,), 1.5))
+    with pytest.raises(ValueError):
+        rope_frequencies(7)
+    with pytest.raises(ValueError):
+        rope_frequencies(8, by_parts=(8.0, 4096, 2.0, 2.0))
+
+
+# ---------------------------------------------------------------- oracle pins
+def test_oracle_attention_closed_forms():
+    rng = np.random.default_rng(0)
+    v = rng.normal(size=(7, 4))
+    q = np.zeros((7, 4))  # equal scores: running means
+    out, _, lse = A.attend(q, rng.normal(size=(7, 4)), v, np.arange(7), 1.0)
+    np.testing.assert_allclose(out, np.cumsum(v, 0) / np.arange(1, 8)[:, None], rtol=1e-12)
+    np.testing.assert_allclose(lse, np.log(np.arange(1, 8)), rtol=1e-12)
+    k = np.eye(4) * 1e4  # one key takes all
+    out, _, _ = A.attend(np.eye(4), k, v[:4], np.full(4, 3), 1.0)
+    np.testing.assert_allclose(out, v[:4], rtol=1e-12)
+    out, _, lse = A.attend(q, k, v[:4], np.full(7, -1), 1.0)  # nothing seen
+    assert not out.any() and np.isneginf(lse).all()
+
+
+def test_oracle_decode_equals_prefill_last_row():
+    rng = np.random.default_rng(1)
+    L, H, Hk, D, page = 37, 4, 2, 8, 16
+    q, k, v = (rng.normal(size=(L, h, D)) for h in (H, Hk, Hk))
+    out, _, lse, _ = A.prefill(q, k, v)
+    table = np.array([[2, 0, 1]])
+    kc, vc = np.full((3, Hk, page, D), np.nan), np.full((3, Hk, page, D), np.nan)
+    for t in range(L):
+        kc[table[0, t // page], :, t % page], vc[table[0, t // page], :, t % page] = k[t], v[t]
+    for shared in (0, 16, 32):
+        o, _, l = A.decode(q[None, -3:], kc, vc, table, [L], shared)
+        np.testing.assert_allclose(o[0], out[-3:], rtol=1e-12)
+        np.testing.assert_allclose(l[0], lse[-3:], rtol=1e-12)
+
+
+def test_oracle_front_rotation_keeps_relative_position():
+    """q . k after rotation depends on the distance only, and each pair's norm is kept."""
+    rng = np.random.default_rng(2)
+    D, rot = 16, 8
+    x = rng.normal(size=(1, 3 * D))
+    for inter in (False, True):
+        table = rope_table(40, rot, base=50.0, device="cpu").double().numpy()
+        dots = []
+        for p in (3, 30):
+            q = A.front(x, 1, 1, D, rope=table, interleaved=inter, kv_lens=[p + 1])[0][0, 0]
+            k = A.front(x, 1, 1, D, rope=table, interleaved=inter, kv_lens=[p - 2])[1][0, 0]
+            dots.append(q @ k)
+            np.testing.assert_allclose(np.linalg.norm(q), np.linalg.norm(x[0, :D]), rtol=1e-6)
+        np.testing.assert_allclose(dots[0], dots[1], rtol=1e-5)

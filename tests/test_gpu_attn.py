@@ -1,0 +1,551 @@
+"""Attention operators through the C ABI against the fp64 oracle.
+
+Tolerances, derived before the first run:
+  - attention, fp32 output: each weight may be rounded to bf16 (relative 2^-8 at most), which
+    moves an output by at most 2^-8 sum_j w_ij |v_j|; scores (fp32 sums of D exact products)
+    and exp add less than 2^-11 of the same sum at these inputs. A bf16 output adds half a
+    unit in its last place, 2^-8 |o|. For one key the weight is 1 and exact.
+  - lse: fp32 throughout; D roundings of partial sums of q . k, at most 2^-24 * D * sum |q k|,
+    scaled; 1e-3 covers the largest score used here (sum |q k| scale < 600).
+  - front: fp32 arithmetic of about ten roundings, 2e-6 relative to the pair's size (a
+    rotation mixes both); a bf16 result adds 2^-8 of its own size.
+"""
+import numpy as np
+import pytest
+import torch
+
+from gated_delta_rule_chunk_gb300 import binding as B
+from gated_delta_rule_chunk_gb300.rope import rope_table
+from oracle import attention as A
+
+pytestmark = pytest.mark.gpu
+
+BF, F32 = torch.bfloat16, torch.float32
+REL = 2.0 ** -8 + 2.0 ** -11
+
+
+def randn(g, *shape, dtype=BF, mul=1.0):
+    return (torch.randn(*shape, generator=g, dtype=torch.float64) * mul).to(dtype)
+
+
+def np64(x):
+    return x.detach().double().cpu().numpy()
+
+
+def close_attention(out, lse, ref, mag, ref_lse, rows=None):
+    o = np64(out).reshape(ref.shape)
+    rows = np.ones(ref.shape[0], bool) if rows is None else rows
+    tol = REL * mag + (2.0 ** -8 * np.abs(ref) if out.dtype == BF else 0.0) + 1e-6
+    bad = ~(np.abs(o - ref) <= tol)
+    bad[~rows] = False
+    assert not bad.any(), (np.argwhere(bad)[:5], o[bad][:5], ref[bad][:5], tol[bad][:5])
+    if lse is not None:
+        got = np64(lse).reshape(ref_lse.shape)[rows]
+        want = ref_lse[rows]
+        assert np.array_equal(np.isneginf(got), np.isneginf(want))
+        fin = np.isfinite(want)
+        assert np.abs(got[fin] - want[fin]).max(initial=0.0) <= 1e-3
+
+
+# ---------------------------------------------------------------- prefill
+def run_prefill(lens, H, Hk, D, seed=0, lead=0, tail=0, mul=1.0, scale=None, out_dtype=F32,
+                spoil=None):
+    g = torch.Generator().manual_seed(seed)
+    T = lead + sum(lens) + tail
+    q, k, v = randn(g, T, H, D, mul=mul), randn(g, T, Hk, D, mul=mul), randn(g, T, Hk, D)
+    if spoil:
+        spoil(q, k, v)
+    cu = torch.tensor([lead] + lens).cumsum(0).to(torch.int32)
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    out = torch.full((T, H, D), 7.0, dtype=out_dtype, device="cuda")
+    lse = torch.full((T, H), 7.0, device="cuda")
+    B.gdn_attn_prefill(q.cuda(), k.cuda(), v.cuda(), cu.cuda(), scale=scale, out=out, return_lse=True,
+                       lse=lse, status=status)
+    assert status.item() == 0
+    return q, k, v, cu, out, lse
+
+
+def check_prefill(*a, **kw):
+    q, k, v, cu, out, lse = run_prefill(*a, **kw)
+    ref, mag, rl, inside = A.prefill(np64(q), np64(k), np64(v), cu.numpy(), kw.get("scale"))
+    close_attention(out, lse, ref, mag, rl, inside)
+    assert (out[torch.tensor(~inside)] == 7.0).all() and (lse[torch.tensor(~inside)] == 7.0).all()
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("L", [1, 2, 31, 63, 64, 65, 127, 128, 129, 255, 257, 400])
+def test_prefill_lengths(L, D):
+    check_prefill([L], 2, 1, D, seed=L)
+
+
+@pytest.mark.parametrize("H, Hk", [(1, 1), (3, 3), (3, 1), (5, 1), (6, 2), (7, 1), (8, 1), (16, 2),
+                                   (24, 2), (33, 1), (64, 1)])
+def test_prefill_groups(H, Hk):
+    check_prefill([70, 1, 150], H, Hk, 128, seed=H)
+
+
+@pytest.mark.parametrize("lens", [[0, 5, 0, 130, 1, 0], [300, 1, 1, 64], [128, 128], [1] * 70,
+                                  [3, 250, 17, 129, 66]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_prefill_packed(lens, D):
+    check_prefill(lens, 4, 2, D, seed=len(lens), lead=3, tail=9)
+
+
+@pytest.mark.parametrize("mul", [0.01, 4.0, 8.0])
+def test_prefill_score_ranges(mul):
+    """Nearly uniform weights, and weights of a few keys whose maximum grows along the row."""
+    check_prefill([385], 2, 1, 128, mul=mul, seed=3, out_dtype=F32)
+
+
+def test_prefill_growing_maximum():
+    """Every block of keys scores far above the one before: each running maximum is replaced."""
+    def spoil(q, k, v):
+        q[:] = 1.0
+        k[:] = (torch.arange(k.shape[0]) / 8).floor()[:, None, None].to(k.dtype) / 16
+    check_prefill([500], 2, 1, 128, spoil=spoil)
+
+    def falling(q, k, v):
+        q[:] = 1.0
+        k[:] = (-(torch.arange(k.shape[0]) / 8).floor())[:, None, None].to(k.dtype) / 16
+    check_prefill([500], 2, 1, 64, spoil=falling)
+
+
+def test_prefill_scale_and_bf16_output():
+    check_prefill([200], 4, 1, 128, scale=0.3, seed=5)
+    check_prefill([200], 4, 1, 64, seed=6, out_dtype=BF)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("what", ["nan", "inf", "lowest"])
+def test_prefill_unseen_values_have_no_influence(what, D):
+    """Keys and values from row 130 on, and the rows around the sequences, hold NaN, infinities
+    or the type's lowest value: rows before 130 come out as if they held zeros."""
+    bad = dict(nan=float("nan"), inf=float("inf"), lowest=torch.finfo(BF).min)[what]
+
+    def spoil(q, k, v):
+        for x in (k, v):
+            x[:2] = bad
+            x[2 + 130:2 + 200] = bad
+            x[-5:] = bad
+    lens = [200, 90]
+    q, k, v, cu, out, lse = run_prefill(lens, 4, 2, D, lead=2, tail=5, spoil=spoil)
+    kz, vz = np64(k), np64(v)
+    for x in (kz, vz):
+        x[2 + 130:2 + 200] = 0
+    ref, mag, rl, inside = A.prefill(np64(q), kz, vz, cu.numpy())
+    inside[2 + 130:2 + 200] = False
+    close_attention(out, lse, ref, mag, rl, inside)
+    if what == "nan":
+        assert torch.isnan(out[2 + 130:2 + 200]).all()  # NaN that is seen is not hidden
+
+
+def test_prefill_one_nan_value_reaches_only_the_rows_that_see_it():
+    def spoil(q, k, v):
+        v[77, 0, 5] = float("nan")
+    q, k, v, cu, out, lse = run_prefill([190], 2, 1, 128, spoil=spoil)
+    vz = np64(v)
+    vz[77, 0, 5] = 0
+    ref, mag, rl, _ = A.prefill(np64(q), np64(k), vz)
+    assert torch.isnan(out[77:, :, 5]).all()
+    keep = torch.ones(128, dtype=torch.bool)
+    keep[5] = False
+    close_attention(out[..., keep], lse, ref[..., keep.numpy()], mag[..., keep.numpy()], rl)
+    close_attention(out[:77], lse[:77], ref[:77], mag[:77], rl[:77])
+
+
+def test_prefill_malformed_cu_seqlens():
+    g = torch.Generator().manual_seed(1)
+    q, k, v = (randn(g, 300, h, 64).cuda() for h in (4, 2, 2))
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for cu in ([0, 200, 100, 260], [-5, 90, 999], [50, 40, 30, 290], [7, 400, 20]):
+        sane = torch.tensor(A.sane_bounds(cu, 300), dtype=torch.int32).cuda()
+        outs = []
+        for c in (torch.tensor(cu, dtype=torch.int32).cuda(), sane):
+            out = torch.zeros(300, 4, 64, dtype=BF, device="cuda")
+            B.gdn_attn_prefill(q, k, v, c, out=out, status=status)
+            outs.append((out, status.item()))
+        assert outs[0][1] == 1 and outs[1][1] == 0
+        assert torch.equal(outs[0][0], outs[1][0])
+
+
+def test_prefill_repeatable_other_stream_and_graph():
+    g = torch.Generator().manual_seed(2)
+    q, k, v = (randn(g, 700, h, 128).cuda() for h in (8, 2, 2))
+    cu = torch.tensor([0, 333, 700], dtype=torch.int32).cuda()
+    a = B.gdn_attn_prefill(q, k, v, cu)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    b = torch.empty_like(a)
+    B.gdn_attn_prefill(q, k, v, cu, out=b, stream=s)
+    s.synchronize()
+    assert torch.equal(a, b)
+    c = torch.zeros_like(a)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.gdn_attn_prefill(q, k, v, cu, out=c)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(a, c)
+    cu.copy_(torch.tensor([0, 100, 650], dtype=torch.int32))  # other lengths, same graph
+    graph.replay()
+    d = B.gdn_attn_prefill(q, k, v, cu, out=a.clone())
+    torch.cuda.synchronize()
+    assert torch.equal(c[:650], d[:650])
+
+
+def test_prefill_empty():
+    e = torch.empty(0, 4, 64, dtype=BF, device="cuda")
+    assert B.gdn_attn_prefill(e, e, e).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("H, Hk, D", [(16, 4, 128), (8, 8, 64)])
+def test_prefill_long(H, Hk, D):
+    """Many key tiles and many work items at once, against 64-bit products on the GPU."""
+    lens = [2500, 1, 1200, 777]
+    g = torch.Generator().manual_seed(9)
+    T = sum(lens)
+    q, k, v = (randn(g, T, h, D).cuda() for h in (H, Hk, Hk))
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    out, lse = B.gdn_attn_prefill(q, k, v, cu.cuda(), return_lse=True, out_dtype=F32)
+    for b, e in zip(cu[:-1].tolist(), cu[1:].tolist()):
+        kk, vv = (x[b:e].double().repeat_interleave(H // Hk, 1).transpose(0, 1) for x in (k, v))
+        s = (q[b:e].double().transpose(0, 1) @ kk.transpose(1, 2)) * D ** -0.5
+        s = s.masked_fill(torch.ones(e - b, e - b, device="cuda").triu(1).bool(), float("-inf"))
+        w = torch.softmax(s, -1)
+        ref, mag, rl = w @ vv, w @ vv.abs(), torch.logsumexp(s, -1)
+        d = (out[b:e].double().transpose(0, 1) - ref).abs() - (REL * mag + 1e-6)
+        assert d.max().item() <= 0
+        assert (lse[b:e].double().t() - rl).abs().max().item() <= 1e-3
+
+
+# ---------------------------------------------------------------- decode
+def make_cache(g, lens, Hk, D, page, shared=0, extra=3, fill=float("nan")):
+    """A paged cache in scattered page order whose unused rows hold `fill`; returns
+    (k_cache, v_cache, table, n_pages) on the CPU."""
+    own = [max(0, -(-n // page) - shared // page) for n in lens]
+    width = max(1, shared // page + max(own))
+    n_pages = shared // page + sum(own) + extra
+    perm = torch.randperm(n_pages, generator=g).tolist()
+    table = torch.full((len(lens), width), -7, dtype=torch.int32)  # unused entries: no page
+    first = [perm.pop() for _ in range(shared // page)]
+    kc, vc = (torch.full((n_pages, Hk, page, D), fill, dtype=BF) for _ in range(2))
+    for p in first:
+        kc[p], vc[p] = randn(g, Hk, page, D), randn(g, Hk, page, D)
+    for n, length in enumerate(lens):
+        table[n, :len(first)] = torch.tensor(first, dtype=torch.int32)
+        for j in range(len(first) * page, length, page):
+            p = perm.pop()
+            table[n, j // page] = p
+            c = min(page, length - j)
+            kc[p, :, :c], vc[p, :, :c] = randn(g, Hk, c, D), randn(g, Hk, c, D)
+    return kc, vc, table
+
+
+def check_decode(lens, H, Hk, D, page, nq=1, shared=0, seed=0, scale=None, out_dtype=F32, mul=1.0):
+    g = torch.Generator().manual_seed(seed)
+    kc, vc, table = make_cache(g, lens, Hk, D, page, shared)
+    N = len(lens)
+    q = randn(g, N, nq, H, D, mul=mul)
+    kv = torch.tensor(lens, dtype=torch.int32)
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    out, lse = B.gdn_attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), kv.cuda(), shared,
+                                 scale=scale, out_dtype=out_dtype, return_lse=True, status=status)
+    assert status.item() == 0
+    ref, mag, rl = A.decode(np64(q), np64(kc), np64(vc), table.numpy(), lens, shared, scale)
+    close_attention(out, lse, ref, mag, rl)
+    return q, kc, vc, table, kv, out
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_pages(page, D):
+    check_decode([1, page - 1, page, page + 1, 3 * page + 5, 300], 8, 2, D, page, seed=page)
+
+
+@pytest.mark.parametrize("H, Hk", [(1, 1), (3, 1), (4, 4), (7, 1), (16, 1), (17, 1), (40, 2), (64, 1)])
+def test_decode_groups(H, Hk):
+    check_decode([77, 130, 5], H, Hk, 128, 32, seed=H)
+
+
+@pytest.mark.parametrize("nq, G", [(2, 1), (3, 5), (4, 4), (8, 8), (64, 1), (9, 7), (5, 3)])
+def test_decode_several_tokens(nq, G):
+    check_decode([nq, nq + 1, 70, 200], 2 * G, 2, 64, 16, nq=nq, seed=nq)
+
+
+def test_decode_empty_sequences():
+    q, kc, vc, table, kv, out = check_decode([0, 40, 0, 1, 0], 4, 2, 128, 16)
+    assert (out[[0, 2, 4]] == 0).all()
+    check_decode([0], 2, 1, 64, 16)
+    check_decode([1, 3, 0], 2, 1, 64, 16, nq=4)  # rows before the sequence's start see nothing
+
+
+def test_decode_long_and_uneven():
+    """One long axis to split beside many short ones; and a single long sequence."""
+    check_decode([9000, 1, 2, 300, 17, 1025], 8, 2, 128, 64, seed=1)
+    check_decode([20011], 4, 1, 128, 16, seed=2)
+    check_decode([1 + 13 * i % 200 for i in range(97)], 4, 2, 64, 16, seed=3)
+
+
+@pytest.mark.parametrize("mul", [0.01, 6.0])
+def test_decode_score_ranges(mul):
+    check_decode([700, 50], 4, 2, 128, 16, mul=mul)
+
+
+def test_decode_scale_and_bf16_output():
+    check_decode([100, 33], 4, 2, 128, 16, scale=0.2)
+    check_decode([100, 33], 4, 2, 128, 16, out_dtype=BF)
+
+
+@pytest.mark.parametrize("shared, page", [(16, 16), (128, 16), (112, 16), (384, 128), (256, 256),
+                                          (1280, 64)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_shared_prefix(shared, page, D):
+    check_decode([shared + x for x in (1, 0, 40, 17, 300)], 8, 2, D, page, shared=shared, seed=shared)
+
+
+@pytest.mark.parametrize("N, H, Hk, nq", [(70, 8, 2, 1), (33, 5, 1, 3), (3, 64, 1, 1), (9, 21, 3, 8),
+                                          (1, 4, 1, 1), (130, 1, 1, 1)])
+def test_decode_shared_prefix_rows(N, H, Hk, nq):
+    """Row counts below, at and above a tile of rows, group sizes that do not divide it."""
+    check_decode([320 + 5 + 7 * i % 90 for i in range(N)], H, Hk, 64, 32, nq=nq, shared=320, seed=N)
+
+
+def test_decode_sequences_shorter_than_the_prefix():
+    check_decode([200, 64, 0, 1, 320, 319, 257], 4, 2, 128, 64, shared=320, seed=4)
+    check_decode([2, 64, 0, 1, 320, 65], 4, 2, 128, 64, nq=3, shared=320, seed=4)
+
+
+def test_decode_long_shared_prefix():
+    check_decode([8192 + 1 + i for i in range(20)], 16, 2, 128, 64, shared=8192, seed=5)
+
+
+def test_decode_shared_equals_unshared():
+    """The same batch with and without the hint, each within its tolerance of the oracle."""
+    for shared in (0, 512):
+        check_decode([512 + 3 * i for i in range(12)], 8, 2, 128, 32, shared=shared, seed=6)
+
+
+def test_decode_bad_pages_and_lengths():
+    g = torch.Generator().manual_seed(3)
+    kc, vc, table = make_cache(g, [100, 90], 2, 64, 16, fill=0.0)
+    table[0, 2], table[1, 0] = 10 ** 6, -3
+    q = randn(g, 2, 4, 64)
+    for lens, shared, want in (([100, 90], 0, 64), ([100, 90], 48, 64), ([100, 10 ** 9], 0, 64 | 128),
+                               ([-5, 90], 0, 64 | 128)):
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        out, lse = B.gdn_attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(),
+                                     torch.tensor(lens, dtype=torch.int32).cuda(), shared,
+                                     out_dtype=F32, return_lse=True, status=status)
+        assert status.item() == want
+        t = np.where(table.numpy() == -7, -1, table.numpy())
+        ref, mag, rl = A.decode(np64(q)[:, None], np64(kc), np64(vc), t, lens, shared)
+        close_attention(out, lse, ref, mag, rl)
+
+
+def test_decode_cache_past_32_bit_offsets():
+    """Pages whose element offsets pass 2^32."""
+    Hk, D, page, n_pages = 8, 128, 256, 18000
+    assert n_pages * Hk * page * D > 2 ** 32
+    g = torch.Generator().manual_seed(4)
+    kc, vc = (torch.empty(n_pages, Hk, page, D, dtype=BF, device="cuda") for _ in range(2))
+    table = torch.tensor([[17999, 3, 17500], [9000, 17998, 0]], dtype=torch.int32)
+    small = [randn(g, 6, Hk, page, D) for _ in range(2)]
+    flat = table.flatten().long().cuda()
+    for c, s in zip((kc, vc), small):
+        c[flat] = s.cuda()
+    q, lens = randn(g, 2, 1, 16, D), [600, 700]
+    local = np.arange(6).reshape(2, 3)
+    for shared in (0, 512):
+        t, loc = table.clone(), local.copy()
+        if shared:
+            t[1, :2], loc[1, :2] = t[0, :2], loc[0, :2]
+        out = B.gdn_attn_decode(q.cuda(), kc, vc, t.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(),
+                                shared, out_dtype=F32)
+        ref, mag, rl = A.decode(np64(q), np64(small[0]), np64(small[1]), loc, lens, shared)
+        close_attention(out, None, ref, mag, rl)
+
+
+def test_decode_repeatable_other_stream_and_graph():
+    g = torch.Generator().manual_seed(7)
+    lens = [900, 3, 400, 1500]
+    kc, vc, table = (x.cuda() for x in make_cache(g, [1600] * 4, 2, 128, 16, 256, fill=0.5))
+    q, kv = randn(g, 4, 8, 128).cuda(), torch.tensor(lens, dtype=torch.int32).cuda()
+    for shared in (0, 256):
+        a = B.gdn_attn_decode(q, kc, vc, table, kv, shared)
+        s = torch.cuda.Stream()
+        s.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(s):
+            b = B.gdn_attn_decode(q, kc, vc, table, kv, shared)
+        s.synchronize()
+        assert torch.equal(a, b)
+        c = torch.zeros_like(a)
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            B.gdn_attn_decode(q, kc, vc, table, kv, shared, out=c)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, c)
+        kv.copy_(torch.tensor([1600, 299, 0, 1], dtype=torch.int32))
+        graph.replay()
+        d = B.gdn_attn_decode(q, kc, vc, table, kv, shared)
+        torch.cuda.synchronize()
+        assert torch.equal(c, d)
+        kv.copy_(torch.tensor(lens, dtype=torch.int32))
+
+
+# ---------------------------------------------------------------- front
+def check_front(lens, H, Hk, D, rot, inter=False, x_dtype=BF, out_dtype=BF, page=16, past=None,
+                norm=True, cache=True, dense=True, seed=0, lead=0, tail=0, mul=2.0):
+    g = torch.Generator().manual_seed(seed)
+    N, T = len(lens), lead + sum(lens) + tail
+    x = randn(g, T, (H + 2 * Hk) * D, dtype=x_dtype, mul=mul)
+    qw, kw = (1 + randn(g, D, dtype=F32, mul=0.2) for _ in range(2)) if norm else (None, None)
+    cu = torch.tensor([lead] + lens).cumsum(0).to(torch.int32)
+    past = [0] * N if past is None else past
+    kv = torch.tensor([p + n for p, n in zip(past, lens)], dtype=torch.int32)
+    need = [-(-int(n) // page) for n in kv]
+    n_pages, width = sum(need) + 2, max(max(need), 1)
+    perm = torch.randperm(n_pages, generator=g).tolist()
+    table = torch.full((N, width), -1, dtype=torch.int32)
+    for n in range(N):
+        for j in range(need[n]):
+            table[n, j] = perm.pop()
+    kc, vc = (randn(g, n_pages, Hk, page, D, dtype=out_dtype) for _ in range(2))
+    rope = rope_table(int(kv.max()) + 1, rot, device="cpu") if rot else None
+    dev = lambda t: None if t is None else t.cuda()
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    kd, vd = (dev(kc), dev(vc)) if cache else (None, None)
+    bufs = [torch.full((T, h, D), 9.0, dtype=out_dtype, device="cuda") for h in (H, Hk, Hk)]
+    q, k, v = B.gdn_attn_front(dev(x), H, Hk, D, dev(qw), dev(kw), rope=dev(rope), interleaved=inter,
+                               cu_seqlens=dev(cu), kv_lens=dev(kv),
+                               page_table=dev(table) if cache else None, k_cache=kd, v_cache=vd,
+                               output_kv=dense, q=bufs[0], k=bufs[1], v=bufs[2],
+                               out_dtype=out_dtype, status=status)
+    assert status.item() == 0
+    ref = A.front(np64(x), H, Hk, D, None if qw is None else np64(qw), None if kw is None else np64(kw),
+                  1e-6, None if rope is None else np64(rope), inter, cu.numpy(), kv.numpy(),
+                  table.numpy(), np64(kc), np64(vc))
+    inside = ref[5]
+    assert (k is None) == (not dense)
+    pairs = [(q, ref[0]), (k, ref[1]), (v, ref[2])] if dense else [(q, ref[0])]
+    for got, want in pairs:
+        close_front(got[torch.tensor(inside)], want[inside], out_dtype)
+        assert (got[torch.tensor(~inside)] == 9.0).all()
+    if cache:
+        close_front(kd, ref[3], out_dtype)
+        close_front(vd, ref[4], out_dtype)
+
+
+def close_front(got, want, dtype):
+    g = np64(got)
+    size = np.abs(want).max(-1, keepdims=True) if want.size else np.abs(want)
+    tol = 2e-6 * size + (2.0 ** -8 * np.abs(want) if dtype == BF else 0.0)
+    assert (np.abs(g - want) <= tol).all(), np.abs(g - want).max()
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D, rot", [(64, 16), (64, 48), (64, 64), (128, 32), (128, 96), (128, 128),
+                                    (128, 0)])
+def test_front_rotary(D, rot, inter):
+    check_front([5, 1, 40], 6, 2, D, rot, inter, past=[7, 300, 0], seed=rot)
+
+
+@pytest.mark.parametrize("x_dtype, out_dtype", [(BF, BF), (BF, F32), (F32, BF), (F32, F32)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_front_types(D, x_dtype, out_dtype):
+    check_front([33, 2], 5, 1, D, 32, x_dtype=x_dtype, out_dtype=out_dtype, past=[3, 15])
+
+
+@pytest.mark.parametrize("norm, cache, dense", [(False, True, True), (True, False, True),
+                                                (True, True, False), (False, False, True)])
+def test_front_parts(norm, cache, dense):
+    check_front([20, 11], 4, 2, 128, 64, norm=norm, cache=cache, dense=dense)
+
+
+@pytest.mark.parametrize("lens, lead, tail", [([1], 0, 0), ([1] * 130, 0, 0), ([1, 0, 1, 0, 3], 0, 0),
+                                              ([0, 0, 7], 2, 5), ([0], 0, 4), ([2, 1, 1, 1], 1, 0)])
+def test_front_sequences(lens, lead, tail):
+    check_front(lens, 4, 2, 128, 64, past=[11 * i % 70 for i in range(len(lens))], lead=lead, tail=tail)
+
+
+@pytest.mark.parametrize("page", [16, 32, 64, 128, 256])
+def test_front_pages(page):
+    check_front([page + 3, 2 * page, 5], 3, 1, 64, 64, page=page, past=[page - 1, 0, 2 * page + 7])
+
+
+def test_front_many_rows():
+    """Enough rows for the several-heads-a-group form, a head count it does not divide."""
+    check_front([700, 501], 15, 3, 128, 64, seed=2)
+    check_front([700, 501], 15, 3, 64, 32, inter=True, x_dtype=F32, out_dtype=F32, seed=2)
+
+
+def test_front_small_and_zero_rows():
+    check_front([3], 2, 1, 128, 64, mul=1e-4)
+    check_front([3], 2, 1, 128, 64, mul=0.0)
+
+
+def test_front_without_lengths_and_bad_places():
+    g = torch.Generator().manual_seed(5)
+    x = randn(g, 40, 4 * 64).cuda()
+    rope = rope_table(16, 32)
+    kc, vc = (torch.zeros(3, 1, 16, 64, dtype=BF, device="cuda") for _ in range(2))
+    table = torch.tensor([[1, 99]], dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q, k, v = B.gdn_attn_front(x, 2, 1, 64, rope=rope, page_table=table, k_cache=kc, v_cache=vc,
+                               status=status)
+    assert status.item() == 64 | 128  # page 99; positions past both tables
+    assert torch.equal(kc[1, 0], k[:16, 0]) and torch.equal(vc[1, 0], v[:16, 0])
+    assert (kc[[0, 2]] == 0).all() and (vc[[0, 2]] == 0).all()
+    ref = A.front(np64(x), 2, 1, 64, rope=np64(rope))
+    close_front(q, ref[0], BF)  # positions past the table use its last row
+    kv = torch.tensor([20], dtype=torch.int32, device="cuda")  # 40 tokens, 20 of them before the start
+    B.gdn_attn_front(x, 2, 1, 64, rope=rope_table(64, 32), kv_lens=kv, page_table=table, k_cache=kc,
+                     v_cache=vc, status=status)
+    assert status.item() & 128
+    B.gdn_attn_front(x, 2, 1, 64, cu_seqlens=torch.tensor([0, 30, 20, 45], dtype=torch.int32).cuda(),
+                     status=status)
+    assert status.item() == 1
+
+
+def test_front_graph_and_stream():
+    g = torch.Generator().manual_seed(6)
+    x = randn(g, 64, 6 * 128).cuda()
+    rope = rope_table(64, 64)
+    a = B.gdn_attn_front(x, 4, 1, 128, rope=rope)
+    out = [torch.zeros_like(t) for t in a]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        B.gdn_attn_front(x, 4, 1, 128, rope=rope, q=out[0], k=out[1], v=out[2])
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(s, t) for s, t in zip(a, out))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    b = B.gdn_attn_front(x, 4, 1, 128, rope=rope, stream=s)
+    s.synchronize()
+    assert all(torch.equal(u, t) for u, t in zip(a, b))
+
+
+# ---------------------------------------------------------------- together
+def test_prompt_then_decode_equals_a_longer_prompt():
+    """front + prefill of a prompt, then front + decode of the next tokens, give the rows that
+    one longer prompt gives."""
+    g = torch.Generator().manual_seed(8)
+    H, Hk, D, L, more = 8, 2, 128, 150, 5
+    x = randn(g, L + more, (H + 2 * Hk) * D).cuda()
+    w = torch.ones(D, device="cuda")
+    rope = rope_table(256, 64)
+    q, k, v = B.gdn_attn_front(x, H, Hk, D, w, w, rope=rope)
+    want = np64(B.gdn_attn_prefill(q, k, v, out_dtype=F32))
+    table = torch.arange(16, dtype=torch.int32, device="cuda").flip(0)[None].contiguous()
+    kc, vc = (torch.zeros(16, Hk, 16, D, dtype=BF, device="cuda") for _ in range(2))
+    for b, e in ((0, L), (L, L + 1), (L + 1, L + more)):
+        kv = torch.tensor([e], dtype=torch.int32, device="cuda")
+        q1, k1, v1 = B.gdn_attn_front(x[b:e], H, Hk, D, w, w, rope=rope, kv_lens=kv, page_table=table,
+                                      k_cache=kc, v_cache=vc)
+        if b == 0:
+            got = B.gdn_attn_prefill(q1, k1, v1, out_dtype=F32)
+        else:
+            got = B.gdn_attn_decode(q1[None], kc, vc, table, kv, out_dtype=F32)[0]
+        # both sides round their weights to bf16: twice the oracle's tolerance, |v| < 6
+        assert np.abs(np64(got) - want[b:e]).max() <= 2 * REL * 6
