@@ -1,0 +1,618 @@
+// Attention of row tiles on the tensor cores (tcgen05), shared by the prompt kernel and the
+// decode kernel's common-prefix part.
+//
+// Mathematics, per row with scores s_j = q . k_j: with any reference r,
+//   o = sum_j 2^(c (s_j - r)) v_j / sum_j 2^(c (s_j - r)),   c = scale * log2(e),
+// so the keys are taken 128 at a time with the running maximum as r. r is replaced only when
+// the maximum has grown by more than kGrow (in powers of two): weights then stay below
+// 2^kGrow, far inside fp32 and bf16, and the accumulator is rescaled a few times a row
+// instead of once a tile. The weights are rounded to bf16 for the second product (an fp16
+// weight would need an fp16 V); the denominator sums them in fp32 before that rounding.
+//
+// A row tile is 128 rows = floor(128 / G) tokens x the G query heads of one key head, so a
+// key tile is read once for all heads of its group, and a causal tile's masked part is
+// smaller. A CTA works on two row tiles (A, B) at a time against the same key tiles:
+//   warps 0-3, 4-7  one thread per row of A, B: scores from TMEM, weights back to TMEM (over
+//                   the scores), running sums, the output
+//   warp 8          TMA loads: Q of both tiles, a ring of K and V tiles
+//   warp 9          issues every MMA: S = Q K^T (both operands in shared memory),
+//                   O += P V (P in TMEM). While A's rows are weighed, B's products run.
+//   warp 10         hands out the work items (persistent CTAs, one per SM)
+//   warps 12-15     V tiles with masked keys: rows past the sequence's end are zeroed, and
+//                   a value that is not finite is looked for, because a weight of 0 would
+//                   not remove it (0 * inf); the rows of such a tile pair are then computed
+//                   one by one without it (rare, so only correctness counts there).
+// TMEM: S_A, S_B [0, 256), O_A, O_B [256, 256 + 2 D).
+#pragma once
+
+#include <cuda.h>
+
+#include "attn_common.cuh"
+#include "umma.cuh"
+#include "warp_mma.cuh"
+
+namespace gdn {
+
+constexpr int kAttnThreads = 512;
+constexpr int kRows = 128;           // rows of a tile
+constexpr int kKeys = 128;           // keys of a tile
+constexpr int kAttnSeqs = 4096;      // sequences of one launch
+constexpr uint32_t kPolls = 1u << 22;
+constexpr float kGrow = 8.0f;
+
+struct AttnItem {
+  int base;        // first token (row of q) of the sequence
+  int len;         // its tokens
+  int tok;         // first token of tile A, from base
+  int hk;
+  int nA, nB;      // key tiles of A and B (nB = 0: no tile B)
+  int mask0;       // first key tile that some row sees only in part
+  int valid;
+};
+
+template <int D>
+struct AttnSmem {
+  static constexpr int kTile = 128 * D * 2;            // one Q, K or V tile
+  static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kQ = 0, kRing = 2 * kTile;
+  static constexpr int kBounds = kRing + kStages * kTile;      // sanitized cu_seqlens
+  static constexpr int kBars = kBounds + 4 * (kAttnSeqs + 4);
+  static constexpr int kBytes = kBars + 512 + 1024;            // + alignment of the tiles
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Two fp32 FMAs / adds in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, z, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mov.b64 z, {%6, %7};\n fma.rn.f32x2 w, x, y, z;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " add.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// D[tmem] += A[tmem] * B: A is M x 16 bf16, two to a 32-bit column.
+__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
+                                             uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};\n" ::"r"(taddr),
+      "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]),
+      "r"(v[8]), "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]),
+      "r"(v[15]), "r"(v[16]), "r"(v[17]), "r"(v[18]), "r"(v[19]), "r"(v[20]), "r"(v[21]),
+      "r"(v[22]), "r"(v[23]), "r"(v[24]), "r"(v[25]), "r"(v[26]), "r"(v[27]), "r"(v[28]),
+      "r"(v[29]), "r"(v[30]), "r"(v[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,"
+      "%13,%14,%15,%16};\n" ::"r"(taddr),
+      "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+      "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;\n" ::"n"(N));
+}
+
+// Barriers of the attention kernel (all in shared memory).
+template <int kStages>
+struct AttnBars {
+  // A V tile with masked keys completes v_raw and, once the V warps are done, v_fixed, in
+  // place of kv_full: so whoever waits on one of the three sees each of its phases.
+  uint64_t kv_full[kStages], kv_empty[kStages], v_raw[kStages], v_fixed[kStages];
+  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t item_full[2], item_empty[2];
+  AttnItem item[2];
+  uint32_t tmem;
+  int poison[4];  // item number + 1 of the last item in this place with an unsafe V tile
+};
+
+// A bounded wait: once one has run out, this thread waits for nothing any more.
+struct Waiter {
+  bool ok = true;
+  int32_t* status;
+  __device__ explicit Waiter(int32_t* s) : status(s) {}
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t phase) {
+    if (ok && !mbar_wait(bar, phase & 1u, kPolls)) {
+      ok = false;
+      set_status(status, GDN_DEV_TIMEOUT);
+    }
+  }
+};
+
+// The work items of a batch of prompts, the ones with most keys first: pair i of a sequence
+// is its tokens [i * span, (i + 1) * span); the pairs of all sequences are numbered by
+// falling i, so that those that start last are the shortest. Called by one warp.
+struct PromptItems {
+  const int* bounds;  // [N + 1] in shared memory
+  int N, span, Hk, total;  // total: items of all key heads
+  int most;                // pairs of the longest sequence
+
+  __device__ int pairs(int n) const { return (bounds[n + 1] - bounds[n] + span - 1) / span; }
+  // pairs numbered i or higher, over all sequences
+  __device__ int count(int i) const {
+    int c = 0;
+    for (int n = threadIdx.x & 31; n < N; n += 32) c += max(0, pairs(n) - i);
+    return __reduce_add_sync(0xffffffffu, c);
+  }
+  __device__ void init() {
+    int m = 0;
+    for (int n = threadIdx.x & 31; n < N; n += 32) m = max(m, pairs(n));
+    most = __reduce_max_sync(0xffffffffu, m);
+    total = count(0) * Hk;
+  }
+  __device__ AttnItem get(int idx, int nt) const {
+    AttnItem it{};
+    if (idx >= total) return it;
+    const int s = idx / Hk, lane = threadIdx.x & 31;
+    int lo = 0, hi = most - 1;  // the largest i with count(i) > s
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (count(m) > s) lo = m;
+      else hi = m - 1;
+    }
+    int r = s - count(lo + 1);  // the r-th sequence that has a pair lo
+    for (int n0 = 0; n0 < N; n0 += 32) {
+      const bool has = n0 + lane < N && pairs(n0 + lane) > lo;
+      const uint32_t mask = __ballot_sync(0xffffffffu, has);
+      const int c = __popc(mask);
+      if (r < c) {
+        const int n = n0 + __fns(mask, 0, r + 1);
+        it.base = bounds[n];
+        it.len = bounds[n + 1] - bounds[n];
+        break;
+      }
+      r -= c;
+    }
+    it.tok = lo * span;
+    it.hk = idx % Hk;
+    it.nA = (min(it.tok + nt, it.len) + kKeys - 1) / kKeys;
+    it.nB = it.tok + nt < it.len ? (min(it.tok + 2 * nt, it.len) + kKeys - 1) / kKeys : 0;
+    it.mask0 = (it.tok + 1) / kKeys;
+    it.valid = 1;
+    return it;
+  }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
+                   const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v) {
+  using S = AttnSmem<D>;
+  constexpr int kStages = S::kStages;
+  extern __shared__ char smem_raw[];
+  char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
+  int* bounds = reinterpret_cast<int*>(smem + S::kBounds);
+  auto& B = *reinterpret_cast<AttnBars<kStages>*>(smem + S::kBars);
+  static_assert(sizeof(AttnBars<kStages>) <= 512, "barrier area");
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int nt = kRows / p.G;  // tokens of a row tile
+
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&B.kv_full[i], 1);
+      mbar_init(&B.kv_empty[i], 1);
+      mbar_init(&B.v_raw[i], 1);
+      mbar_init(&B.v_fixed[i], 4);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&B.q_full[i], 1);
+      mbar_init(&B.q_empty[i], 1);
+      mbar_init(&B.s_full[i], 1);
+      mbar_init(&B.p_full[i], 4);
+      mbar_init(&B.o_full[i], 1);
+      mbar_init(&B.o_empty[i], 4);
+      mbar_init(&B.item_full[i], 1);
+      mbar_init(&B.item_empty[i], 14);  // load, MMA, 8 row warps, 4 V warps
+    }
+    for (int i = 0; i < 4; ++i) B.poison[i] = 0;
+    mbar_init_fence();
+  }
+  if (warp == 8) {
+    tmem_alloc(&B.tmem, 512);
+    tmem_relinquish();
+  }
+  if (warp == 10) {  // cu_seqlens, each entry clamped and raised to the largest before it
+    int carry = p.cu ? min(max(p.cu[0], 0), p.T) : 0;
+    bool bad = p.cu && p.cu[0] != carry;
+    if (lane == 0) bounds[0] = carry;
+    for (int n0 = 1; n0 <= p.N; n0 += 32) {
+      const int n = n0 + lane;
+      const int raw = n <= p.N ? (p.cu ? p.cu[n] : p.T) : 0;
+      int e = n <= p.N ? min(max(raw, 0), p.T) : 0;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, e, o);
+        if (lane >= o) e = max(e, x);
+      }
+      e = max(e, carry);
+      if (n <= p.N) {
+        bounds[n] = e;
+        bad |= raw != e;
+      }
+      carry = __shfl_sync(0xffffffffu, e, 31);
+    }
+    if (bad && blockIdx.x == 0) set_status(p.status, GDN_DEV_BAD_CU_SEQLENS);
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B.tmem;
+  Waiter wait(p.status);
+
+  // ------------------------------------------------------------------ rows
+  if (warp < 8) {
+    regs_inc<192>();
+    const int X = warp >> 2, row = threadIdx.x & 127;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const uint32_t tS = tmem + lanes + X * 128, tO = tmem + lanes + 256 + X * D;
+    const float c = p.scale * 1.44269504088896340736f;
+    const int rt = row / p.G, rh = row - rt * p.G;  // token and head of this row in the tile
+    uint32_t steps = 0, tiles = 0;
+    for (uint32_t k = 0;; ++k) {
+      wait(&B.item_full[k & 1], k >> 1);
+      const AttnItem it = B.item[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
+      if (!it.valid || !wait.ok) break;
+      const int n = X ? it.nB : it.nA;
+      if (n == 0) continue;
+      const int tok = it.tok + X * nt + rt;
+      const bool real = rt < nt && tok < it.len;
+      const int lim = min(tok, it.len - 1) + 1;  // keys this row sees
+      float ref = -INFINITY, l = 0.f;            // reference of the weights, their sum
+      for (int j = 0; j < n; ++j, ++steps) {
+        wait(&B.s_full[X], steps);
+        tc_fence_after();
+        float s[128];
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          tmem_ld32(tS + 32 * q, *reinterpret_cast<float(*)[32]>(&s[32 * q]));
+        tmem_ld_wait();
+        const int seen = lim - j * kKeys;
+        if (__any_sync(0xffffffffu, seen < kKeys)) {
+#pragma unroll
+          for (int i = 0; i < 128; ++i) s[i] = i < seen ? s[i] : -INFINITY;
+        }
+        float m4[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+        for (int i = 4; i < 128; i += 4) {
+          m4[0] = fmaxf(m4[0], s[i]);
+          m4[1] = fmaxf(m4[1], s[i + 1]);
+          m4[2] = fmaxf(m4[2], s[i + 2]);
+          m4[3] = fmaxf(m4[3], s[i + 3]);
+        }
+        const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
+        // A new reference where the maximum outgrew the old one (always in the first tile
+        // that holds a key). S being complete, the product of the tile before is too.
+        const bool grown = m > ref && (m - ref) * c > kGrow;
+        if (__any_sync(0xffffffffu, grown)) {
+          const float f = grown ? ex2((ref - m) * c) : 1.f;  // 0 from -inf
+          if (grown) ref = m;
+          l *= f;
+          if (j > 0) {
+#pragma unroll 1
+            for (int q = 0; q < D; q += 16) {
+              float o[16];
+              tmem_ld16(tO + q, o);
+              tmem_ld_wait();
+#pragma unroll
+              for (int i = 0; i < 16; ++i) o[i] *= f;
+              tmem_st16(tO + q, o);
+            }
+          }
+        }
+        const float nr = ref == -INFINITY ? 0.f : -ref * c;
+        const float2 c2 = make_float2(c, c), r2 = make_float2(nr, nr);
+        float2 l0 = make_float2(l, 0.f), l1 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+          uint32_t w[32];
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) {
+            const int e = 64 * q + 2 * i;
+            float2 a = fma2(make_float2(s[e], s[e + 1]), c2, r2);
+            float2 b = fma2(make_float2(s[e + 2], s[e + 3]), c2, r2);
+            a.x = ex2(a.x); a.y = ex2(a.y); b.x = ex2(b.x); b.y = ex2(b.y);
+            l0 = add2(l0, a);
+            l1 = add2(l1, b);
+            w[i] = pack_bf16(a.x, a.y);
+            w[i + 1] = pack_bf16(b.x, b.y);
+          }
+          tmem_st32u(tS + 32 * q, w);
+        }
+        l = (l0.x + l0.y) + (l1.x + l1.y);
+        tmem_st_wait();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.p_full[X]);
+      }
+      wait(&B.o_full[X], tiles);
+      ++tiles;
+      tc_fence_after();
+      const size_t at = (size_t)(it.base + tok) * p.H + it.hk * p.G + rh;
+      const bool poison = *reinterpret_cast<volatile int*>(&B.poison[k & 3]) == (int)k + 1;
+      const float r = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+#pragma unroll
+      for (int q = 0; q < D; q += 32) {
+        float o[32];
+        tmem_ld32(tO + q, o);
+        tmem_ld_wait();
+        if (real && !poison) {
+          if (p.out_bf16) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at * D + q);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              dst[i] = make_uint4(pack_bf16(o[8 * i] * r, o[8 * i + 1] * r),
+                                  pack_bf16(o[8 * i + 2] * r, o[8 * i + 3] * r),
+                                  pack_bf16(o[8 * i + 4] * r, o[8 * i + 5] * r),
+                                  pack_bf16(o[8 * i + 6] * r, o[8 * i + 7] * r));
+          } else {
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D + q);
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              dst[i] = make_float4(o[4 * i] * r, o[4 * i + 1] * r, o[4 * i + 2] * r,
+                                   o[4 * i + 3] * r);
+          }
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.o_empty[X]);
+      if (real && p.lse)
+        p.lse[at] = l == 0.f ? -INFINITY : ref * p.scale + logf(l);
+      if (poison) {  // this warp's rows one by one, from global memory
+        for (int i = 0; i < 32; ++i) {
+          const int rr = (warp & 3) * 32 + i, ti = rr / p.G, t = it.tok + X * nt + ti;
+          if (ti >= nt || t >= it.len) continue;
+          const size_t to = (size_t)(it.base + t) * p.H + it.hk * p.G + (rr - ti * p.G);
+          const size_t kv = ((size_t)it.base * p.Hk + it.hk) * D, step = (size_t)p.Hk * D;
+          float o[D / 32], lse;
+          attn_row<D>(p.q + to * D, t + 1, p.scale,
+                      [&](int j) { return p.k + kv + j * step; },
+                      [&](int j) { return p.v + kv + j * step; }, o, lse);
+          store_row<D>(p.out, p.out_bf16, to, o);
+        }
+      }
+    }
+  } else if (warp < 12) {
+    regs_dec<88>();
+    // ---------------------------------------------------------------- loads
+    if (warp == 8 && lane == 0) {
+      uint32_t slot = 0, loads[2] = {0, 0};
+      uint32_t kv_uses = 0, raw_uses = 0, is_raw = 0;  // per stage: uses (mod 2), the last one
+      for (uint32_t k = 0;; ++k) {
+        wait(&B.item_full[k & 1], k >> 1);
+        const AttnItem it = B.item[k & 1];
+        mbar_arrive(&B.item_empty[k & 1]);
+        if (!it.valid || !wait.ok) break;
+        const int n = max(it.nA, it.nB);
+        auto load_q = [&](int X) {
+          if (X && it.nB == 0) return;
+          wait(&B.q_empty[X], loads[X] + 1);
+          ++loads[X];
+          mbar_expect_tx(&B.q_full[X], (uint32_t)(nt * p.G * D * 2));
+          for (int d = 0; d < D; d += 64)
+            tma_load_3d(smem + S::kQ + X * S::kTile + d * 256, &tm_q, d, it.hk * p.G,
+                        it.base + it.tok + X * nt, &B.q_full[X]);
+        };
+        auto load_kv = [&](const CUtensorMap* tm, int j, bool raw) {
+          const int st = slot % kStages;
+          wait(&B.kv_empty[st], slot / kStages + 1);
+          ++slot;
+          uint64_t* bar = raw ? &B.v_raw[st] : &B.kv_full[st];
+          (raw ? raw_uses : kv_uses) ^= 1u << st;
+          is_raw = (is_raw & ~(1u << st)) | ((uint32_t)raw << st);
+          mbar_expect_tx(bar, S::kTile);
+          for (int d = 0; d < D; d += 64)
+            tma_load_3d(smem + S::kRing + st * S::kTile + d * 256, tm, d, it.hk,
+                        it.base + j * kKeys, bar);
+        };
+        load_q(0);
+        load_kv(&tm_k, 0, false);
+        load_q(1);
+        load_kv(&tm_v, 0, it.mask0 == 0);
+        for (int j = 1; j < n; ++j) {
+          load_kv(&tm_k, j, false);
+          load_kv(&tm_v, j, j >= it.mask0);
+        }
+      }
+      if (!wait.ok) {  // copies in flight end before the CTA does
+        for (uint32_t i = 0; i < kStages && i < slot; ++i) {
+          if ((is_raw >> i) & 1) mbar_wait(&B.v_raw[i], ((raw_uses >> i) & 1) ^ 1, kPolls);
+          else mbar_wait(&B.kv_full[i], ((kv_uses >> i) & 1) ^ 1, kPolls);
+        }
+        for (int X = 0; X < 2; ++X)
+          if (loads[X]) mbar_wait(&B.q_full[X], (loads[X] - 1) & 1, kPolls);
+      }
+    }
+    // ---------------------------------------------------------------- products
+    if (warp == 9 && lane == 0) {
+      constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
+      constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
+      const uint64_t dQ = sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024);
+      const uint64_t dK = sdesc_sw128(smem_addr(smem + S::kRing), 16, 1024);
+      const uint64_t dV = sdesc_sw128(smem_addr(smem + S::kRing), 16384, 1024);
+      uint32_t base = 0;                          // ring place of the item's K_0
+      // parities to wait for, a bit per barrier
+      uint32_t kvs = 0, fixes = 0, qs = 0, ps = 0, os = 3;
+      auto scores = [&](int X, uint32_t place, bool load, bool first, bool last) {
+        const uint32_t st = place % kStages;
+        if (first) {
+          wait(&B.q_full[X], qs >> X);
+          qs ^= 1u << X;
+        }
+        if (load) {
+          wait(&B.kv_full[st], kvs >> st);
+          kvs ^= 1u << st;
+        }
+        tc_fence_after();
+        const uint64_t a = dQ + X * (S::kTile >> 4), b = dK + st * (S::kTile >> 4);
+#pragma unroll
+        for (int d = 0; d < D; d += 16) {
+          const uint32_t off = ((d >> 6) * 16384 + (d & 63) * 2) >> 4;
+          umma_bf16(tmem + X * 128, a + off, b + off, kIdS, d > 0);
+        }
+        umma_commit(&B.s_full[X]);
+        if (last) umma_commit(&B.q_empty[X]);
+      };
+      wait(&B.item_full[0], 0);
+      int nx[2] = {B.item[0].nA, B.item[0].nB}, mask0 = B.item[0].mask0;
+      bool valid = B.item[0].valid && wait.ok;
+      mbar_arrive(&B.item_empty[0]);
+      if (valid) {
+        scores(0, 0, true, true, nx[0] == 1);
+        if (nx[1]) scores(1, 0, false, true, nx[1] == 1);
+        umma_commit(&B.kv_empty[0]);
+      }
+      for (uint32_t k = 1; valid; ++k) {
+        const int n = max(nx[0], nx[1]);
+        int next[2] = {0, 0}, next0 = 0;
+        for (int j = 0; j < n; ++j) {
+          const bool end = j == n - 1;
+          if (end) {
+            wait(&B.item_full[k & 1], k >> 1);
+            valid = B.item[k & 1].valid && wait.ok;
+            if (valid) {
+              next[0] = B.item[k & 1].nA;
+              next[1] = B.item[k & 1].nB;
+              next0 = B.item[k & 1].mask0;
+            }
+            mbar_arrive(&B.item_empty[k & 1]);
+          }
+          const uint32_t vp = base + 2 * j + 1, vst = vp % kStages;
+          if (j >= mask0) {
+            wait(&B.v_fixed[vst], fixes >> vst);
+            fixes ^= 1u << vst;
+          } else {
+            wait(&B.kv_full[vst], kvs >> vst);
+            kvs ^= 1u << vst;
+          }
+          bool load = true;  // the next K tile is still to be waited for
+#pragma unroll 1
+          for (int X = 0; X < 2; ++X) {
+            const int nX = X ? nx[1] : nx[0], nextX = X ? next[1] : next[0];
+            if (j < nX) {
+              wait(&B.p_full[X], ps >> X);
+              ps ^= 1u << X;
+              if (j == 0) {
+                wait(&B.o_empty[X], os >> X);
+                os ^= 1u << X;
+              }
+              tc_fence_after();
+              const uint64_t b = dV + vst * (S::kTile >> 4);
+#pragma unroll
+              for (int t = 0; t < kKeys; t += 16)
+                umma_bf16_ts(tmem + 256 + X * D, tmem + X * 128 + (t >> 1), b + t * 8, kIdO,
+                             j > 0 || t > 0);
+              if (j == nX - 1) umma_commit(&B.o_full[X]);
+            }
+            const bool more = j + 1 < nX;
+            if (more || (end && nextX)) {
+              scores(X, base + 2 * (j + 1), load, !more, more ? j + 2 == nX : nextX == 1);
+              load = false;
+            }
+          }
+          umma_commit(&B.kv_empty[vst]);
+          if (!end || valid) umma_commit(&B.kv_empty[(vp + 1) % kStages]);
+        }
+        base += 2 * n;
+        nx[0] = next[0];
+        nx[1] = next[1];
+        mask0 = next0;
+      }
+    }
+    // ---------------------------------------------------------------- work items
+    if (warp == 10) {
+      PromptItems items{bounds, p.N, 2 * nt, p.Hk, 0, 0};
+      items.init();
+      const int grid = (int)gridDim.x, b = (int)blockIdx.x;
+      for (uint32_t k = 0;; ++k) {
+        // every other round dealt backwards, which evens out the falling sizes
+        const int64_t idx = (int64_t)k * grid + ((k & 1) ? grid - 1 - b : b);
+        const AttnItem it = items.get((int)min(idx, (int64_t)items.total), nt);
+        wait(&B.item_empty[k & 1], (k >> 1) + 1);
+        if (lane == 0) {
+          B.item[k & 1] = it;
+          mbar_arrive(&B.item_full[k & 1]);
+        }
+        __syncwarp();
+        // a round dealt backwards may skip this CTA in the last, partial round only
+        if (!it.valid || !wait.ok) break;
+      }
+    }
+    __syncwarp();
+  } else {
+    regs_dec<40>();
+    // ---------------------------------------------------------------- V tiles with masked keys
+    const int tid = threadIdx.x - 12 * 32;
+    uint32_t base = 0, raws = 0;
+    for (uint32_t k = 0;; ++k) {
+      wait(&B.item_full[k & 1], k >> 1);
+      const AttnItem it = B.item[k & 1];
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
+      if (!it.valid || !wait.ok) break;
+      const int n = max(it.nA, it.nB);
+      for (int j = it.mask0; j < n; ++j) {
+        const uint32_t st = (base + 2 * j + 1) % kStages;
+        wait(&B.v_raw[st], raws >> st);
+        raws ^= 1u << st;
+        char* tile = smem + S::kRing + st * S::kTile;
+        const int rows = it.len - j * kKeys;  // of this tile inside the sequence
+        bool found = false;
+#pragma unroll 4
+        for (int i = tid; i < S::kTile / 16; i += 128) {
+          uint4* v = reinterpret_cast<uint4*>(tile) + i;
+          if (((i >> 3) & 127) >= rows) {
+            *v = make_uint4(0, 0, 0, 0);
+          } else {
+            const uint4 x = *v;  // a bf16 exponent of all ones, in either half
+            const uint32_t e = ((x.x & 0x7F807F80u) + 0x00800080u) |
+                               ((x.y & 0x7F807F80u) + 0x00800080u) |
+                               ((x.z & 0x7F807F80u) + 0x00800080u) |
+                               ((x.w & 0x7F807F80u) + 0x00800080u);
+            found |= (e & 0x80008000u) != 0;
+          }
+        }
+        if (found) *reinterpret_cast<volatile int*>(&B.poison[k & 3]) = (int)k + 1;
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.v_fixed[st]);
+      }
+      base += 2 * n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+}  // namespace gdn

@@ -307,6 +307,12 @@ bool encode_rows_tmap(void* tmap, const void* base, int rows, int heads, int D);
 // Plain 2-D tensor map over a row-major [rows, cols] bf16 or fp32 matrix (no swizzle).
 bool encode_2d_tmap(void* tmap, const void* base, bool bf16, int cols, int rows, int box_cols,
                     int box_rows);
+// Tensor map over a bf16 tensor of `rank` <= 5 dimensions (innermost first; strides in bytes
+// from the second on) with the 128-byte swizzle, zeros outside.
+bool encode_bf16_tmap(void* tmap, const void* base, int rank, const uint64_t* dims,
+                      const uint64_t* strides, const uint32_t* box);
+// SMs of the current device (152 where it cannot be asked, as on a host without one).
+int num_sms();
 // Same over an fp32 state [rows, 128]: box 32 rows x 32 elements, 128-byte swizzle.
 bool encode_state_tmap(void* tmap, const float* base, int rows);
 
