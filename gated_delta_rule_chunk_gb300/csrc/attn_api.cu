@@ -64,7 +64,7 @@ int gdn_attn_check_desc(const gdn_attn_desc* desc) { return check_impl(desc); }
 
 size_t gdn_attn_workspace_size(const gdn_attn_desc* desc) {
   if (check_impl(desc) != GDN_OK || desc->T % desc->N != 0) return 0;
-  return 256;
+  return attn_decode_workspace(desc->T, desc->N, desc->H, desc->Hk, desc->D);
 }
 
 int gdn_attn_front(const gdn_attn_desc* desc, const void* x, const float* q_weight,
@@ -139,6 +139,9 @@ int gdn_attn_decode(const gdn_attn_desc* desc, const void* q, const void* k_cach
       shared_len > d.max_pages * d.page_size)
     return GDN_ERR_BAD_SHAPE;
   if ((int64_t)(d.T / d.N) * (d.H / d.Hk) > 64) return GDN_ERR_UNSUPPORTED;
+  // 64-key units of all pairs are counted in 31 bits
+  if ((int64_t)d.N * d.Hk * ((int64_t)d.max_pages * d.page_size / 64 + 1) >= ((int64_t)1 << 31))
+    return GDN_ERR_BAD_SHAPE;
   const void* ptrs16[] = {q, k_cache, v_cache, out};
   for (const void* p : ptrs16)
     if (!aligned(p, 16)) return GDN_ERR_MISALIGNED;
@@ -149,10 +152,10 @@ int gdn_attn_decode(const gdn_attn_desc* desc, const void* q, const void* k_cach
   AttnParams p = attn_params(d, q, k_cache, v_cache, scale, out, lse);
   p.nq = d.T / d.N;
   p.page = d.page_size; p.page_shift = log2_of(d.page_size);
-  p.n_pages = d.n_pages; p.max_pages = d.max_pages; p.shared = shared_len;
+  p.n_pages = d.n_pages; p.max_pages = d.max_pages; p.common = shared_len;
   p.table = page_table; p.kv_lens = kv_lens;
   if (!clear_status(d.status, stream)) return GDN_ERR_LAUNCH_FAILED;
-  if (!launch_attn_decode(p, stream)) return GDN_ERR_LAUNCH_FAILED;
+  if (!launch_attn_decode(p, d.workspace, stream)) return GDN_ERR_LAUNCH_FAILED;
   return cudaPeekAtLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH_FAILED;
 }
 

@@ -30,7 +30,9 @@ struct AttnFrontParams {
 struct AttnParams {
   int T, N, H, Hk, G, D;              // G = H / Hk
   int nq;                             // decode: tokens of each sequence
-  int page, page_shift, n_pages, max_pages, shared;  // shared: tokens of the common prefix
+  int page, page_shift, n_pages, max_pages;
+  int common;                         // decode: tokens whose pages are those of sequence 0
+  int shared;                         // those of them that the prefix kernel takes (all or 0)
   const __nv_bfloat16* q;
   const __nv_bfloat16* k;             // [T, Hk, D] or the cache
   const __nv_bfloat16* v;
@@ -46,7 +48,16 @@ struct AttnParams {
 
 bool launch_attn_front(const AttnFrontParams& p, cudaStream_t s);
 bool launch_attn_prefill(const AttnParams& p, cudaStream_t s);
-bool launch_attn_decode(const AttnParams& p, cudaStream_t s);
+bool launch_attn_decode(const AttnParams& p, void* workspace, cudaStream_t s);
+size_t attn_decode_workspace(int T, int N, int H, int Hk, int D);
+
+// Decode: the keys of sequence n, and those that its new token i sees.
+__device__ __forceinline__ int seq_len(const AttnParams& p, int n) {
+  return min(max(p.kv_lens[n], 0), p.max_pages << p.page_shift);
+}
+__device__ __forceinline__ int keys_seen(const AttnParams& p, int n, int i) {
+  return max(seq_len(p, n) - p.nq + i + 1, 0);
+}
 
 // Attention of one query row by one warp, in fp32 throughout: keys 32 at a time, one per
 // lane for the scores, then the lanes own D / 32 output columns each. kp(j) and vp(j) give

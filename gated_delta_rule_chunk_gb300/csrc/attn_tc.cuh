@@ -41,18 +41,31 @@ constexpr uint32_t kPolls = 1u << 22;
 constexpr float kGrow = 8.0f;
 
 struct AttnItem {
-  int base;        // first token (row of q) of the sequence
+  int base;        // first token (row of q) of the sequence (prefix: 0)
   int len;         // its tokens
   int tok;         // first token of tile A, from base
   int hk;
+  int kv0;         // first key tile (prompts: 0)
   int nA, nB;      // key tiles of A and B (nB = 0: no tile B)
   int mask0;       // first key tile that some row sees only in part
   int valid;
 };
 
-template <int D>
+// The common prefix's part of a decode step: per split of its keys, the rows' unnormalised
+// sums [splits][T][H][D], and their reference (in powers of two) and denominator.
+struct PrefixParts {
+  float* o;
+  float2* ml;
+  int splits, tiles;  // tiles: key tiles of the prefix
+};
+
+template <int D, bool kPrefix>
 struct AttnSmem {
   static constexpr int kTile = 128 * D * 2;            // one Q, K or V tile
+  // K and V tiles: 64-element halves of 128 rows each; a tile gathered from pages instead has
+  // both halves of every 8 rows together, so that a page is one box of any height.
+  static constexpr int kGroup = kPrefix ? D * 16 : 1024;    // bytes from 8 rows to the next
+  static constexpr int kHalf = kPrefix ? 1024 : 128 * 128;  // ... from a half to the other
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kQ = 0, kRing = 2 * kTile;
   static constexpr int kBounds = kRing + kStages * kTile;      // sanitized cu_seqlens
@@ -108,6 +121,14 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const float (&v)[16]) 
       "%13,%14,%15,%16};\n" ::"r"(taddr),
       "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
       "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15])
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, int y, int z, int w,
+                                            uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];\n" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
 }
 template <int N>
@@ -199,12 +220,41 @@ struct PromptItems {
   }
 };
 
-template <int D>
+// The work items of a common prefix: (pair of row tiles, key head, split of the keys).
+struct PrefixItems {
+  const AttnParams& p;
+  const PrefixParts& x;
+  int span, total;
+
+  __device__ PrefixItems(const AttnParams& p_, const PrefixParts& x_, int span_)
+      : p(p_), x(x_), span(span_) {
+    total = (p.T + span - 1) / span * p.Hk * x.splits;
+  }
+  __device__ AttnItem get(int idx, int nt) const {
+    AttnItem it{};
+    if (idx >= total) return it;
+    const int z = idx % x.splits, at = idx / x.splits, lane = threadIdx.x & 31;
+    it.len = p.T;
+    it.tok = at / p.Hk * span;
+    it.hk = at % p.Hk;
+    it.kv0 = (int)((int64_t)z * x.tiles / x.splits);
+    it.nA = (int)((int64_t)(z + 1) * x.tiles / x.splits) - it.kv0;
+    it.nB = it.tok + nt < it.len ? it.nA : 0;
+    int lim = p.shared;  // keys that every row of the pair sees
+    for (int t = it.tok + lane; t < min(it.tok + span, it.len); t += 32)
+      lim = min(lim, keys_seen(p, t / p.nq, t % p.nq));
+    it.mask0 = max(__reduce_min_sync(0xffffffffu, lim) / kKeys - it.kv0, 0);
+    it.valid = 1;
+    return it;
+  }
+};
+
+template <int D, bool kPrefix>
 __global__ void __launch_bounds__(kAttnThreads, 1)
-attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
-                   const __grid_constant__ CUtensorMap tm_k,
-                   const __grid_constant__ CUtensorMap tm_v) {
-  using S = AttnSmem<D>;
+attn_tc_kernel(const AttnParams p, const PrefixParts parts,
+               const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+               const __grid_constant__ CUtensorMap tm_v) {
+  using S = AttnSmem<D, kPrefix>;
   constexpr int kStages = S::kStages;
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
@@ -213,6 +263,7 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
   static_assert(sizeof(AttnBars<kStages>) <= 512, "barrier area");
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int nt = kRows / p.G;  // tokens of a row tile
+  if (kPrefix) pdl_release();  // the decode kernel needs nothing from here
 
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -238,7 +289,7 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
     tmem_alloc(&B.tmem, 512);
     tmem_relinquish();
   }
-  if (warp == 10) {  // cu_seqlens, each entry clamped and raised to the largest before it
+  if (!kPrefix && warp == 10) {  // cu_seqlens, each entry clamped and raised to the largest before it
     int carry = p.cu ? min(max(p.cu[0], 0), p.T) : 0;
     bool bad = p.cu && p.cu[0] != carry;
     if (lane == 0) bounds[0] = carry;
@@ -285,7 +336,10 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
       if (n == 0) continue;
       const int tok = it.tok + X * nt + rt;
       const bool real = rt < nt && tok < it.len;
-      const int lim = min(tok, it.len - 1) + 1;  // keys this row sees
+      const int last = min(tok, it.len - 1);
+      // keys this row sees, from the item's first
+      const int lim = kPrefix ? min(keys_seen(p, last / p.nq, last % p.nq), p.shared) - it.kv0 * kKeys
+                              : last + 1;
       float ref = -INFINITY, l = 0.f;            // reference of the weights, their sum
       for (int j = 0; j < n; ++j, ++steps) {
         wait(&B.s_full[X], steps);
@@ -356,17 +410,24 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
       wait(&B.o_full[X], tiles);
       ++tiles;
       tc_fence_after();
-      const size_t at = (size_t)(it.base + tok) * p.H + it.hk * p.G + rh;
+      size_t at = (size_t)(it.base + tok) * p.H + it.hk * p.G + rh;
+      size_t split = 0;
+      if constexpr (kPrefix) {
+        split = (size_t)(((int64_t)it.kv0 * parts.splits + parts.tiles - 1) / parts.tiles);
+        at += split * p.T * p.H;
+      }
       const bool poison = *reinterpret_cast<volatile int*>(&B.poison[k & 3]) == (int)k + 1;
-      const float r = l == 0.f ? 0.f : 1.f / l;  // NaN stays NaN
+      // prefix: as they are, for the merge with the other splits; NaN stays NaN
+      const float r = kPrefix ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      void* out = kPrefix ? parts.o : p.out;
 #pragma unroll
       for (int q = 0; q < D; q += 32) {
         float o[32];
         tmem_ld32(tO + q, o);
         tmem_ld_wait();
         if (real && !poison) {
-          if (p.out_bf16) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.out) + at * D + q);
+          if (!kPrefix && p.out_bf16) {
+            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at * D + q);
 #pragma unroll
             for (int i = 0; i < 4; ++i)
               dst[i] = make_uint4(pack_bf16(o[8 * i] * r, o[8 * i + 1] * r),
@@ -374,7 +435,7 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
                                   pack_bf16(o[8 * i + 4] * r, o[8 * i + 5] * r),
                                   pack_bf16(o[8 * i + 6] * r, o[8 * i + 7] * r));
           } else {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D + q);
+            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at * D + q);
 #pragma unroll
             for (int i = 0; i < 8; ++i)
               dst[i] = make_float4(o[4 * i] * r, o[4 * i + 1] * r, o[4 * i + 2] * r,
@@ -385,43 +446,71 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.o_empty[X]);
-      if (real && p.lse)
-        p.lse[at] = l == 0.f ? -INFINITY : ref * p.scale + logf(l);
+      if constexpr (kPrefix) {
+        if (real && !poison) parts.ml[at] = make_float2(ref * c, l);
+      } else {
+        if (real && p.lse) p.lse[at] = l == 0.f ? -INFINITY : ref * p.scale + logf(l);
+      }
       if (poison) {  // this warp's rows one by one, from global memory
         for (int i = 0; i < 32; ++i) {
           const int rr = (warp & 3) * 32 + i, ti = rr / p.G, t = it.tok + X * nt + ti;
           if (ti >= nt || t >= it.len) continue;
           const size_t to = (size_t)(it.base + t) * p.H + it.hk * p.G + (rr - ti * p.G);
-          const size_t kv = ((size_t)it.base * p.Hk + it.hk) * D, step = (size_t)p.Hk * D;
           float o[D / 32], lse;
-          attn_row<D>(p.q + to * D, t + 1, p.scale,
-                      [&](int j) { return p.k + kv + j * step; },
-                      [&](int j) { return p.v + kv + j * step; }, o, lse);
-          store_row<D>(p.out, p.out_bf16, to, o);
+          if constexpr (kPrefix) {
+            const int k0 = it.kv0 * kKeys;
+            const int k1 = min(min(keys_seen(p, t / p.nq, t % p.nq), p.shared), k0 + n * kKeys);
+            auto at_key = [&](const __nv_bfloat16* base, int j) -> const __nv_bfloat16* {
+              const int key = k0 + j, pg = p.table[key >> p.page_shift];
+              if (pg < 0 || pg >= p.n_pages) return nullptr;
+              return base + ((((size_t)pg * p.Hk + it.hk) << p.page_shift) + (key & (p.page - 1))) * D;
+            };
+            attn_row<D>(p.q + to * D, k1 - k0, p.scale, [&](int j) { return at_key(p.k, j); },
+                        [&](int j) { return at_key(p.v, j); }, o, lse);
+            const size_t row = split * p.T * p.H + to;
+            store_row<D>(parts.o, false, row, o);
+            if (lane == 0)
+              parts.ml[row] = make_float2(lse * 1.44269504088896340736f, lse == -INFINITY ? 0.f : 1.f);
+          } else {
+            const size_t kv = ((size_t)it.base * p.Hk + it.hk) * D, step = (size_t)p.Hk * D;
+            attn_row<D>(p.q + to * D, t + 1, p.scale,
+                        [&](int j) { return p.k + kv + j * step; },
+                        [&](int j) { return p.v + kv + j * step; }, o, lse);
+            store_row<D>(p.out, p.out_bf16, to, o);
+          }
         }
       }
     }
   } else if (warp < 12) {
     regs_dec<88>();
     // ---------------------------------------------------------------- loads
-    if (warp == 8 && lane == 0) {
+    if (warp == 8 && (kPrefix || lane == 0)) {
       uint32_t slot = 0, loads[2] = {0, 0};
       uint32_t kv_uses = 0, raw_uses = 0, is_raw = 0;  // per stage: uses (mod 2), the last one
       for (uint32_t k = 0;; ++k) {
         wait(&B.item_full[k & 1], k >> 1);
         const AttnItem it = B.item[k & 1];
-        mbar_arrive(&B.item_empty[k & 1]);
+        if constexpr (kPrefix) __syncwarp();
+        if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
         if (!it.valid || !wait.ok) break;
         const int n = max(it.nA, it.nB);
         auto load_q = [&](int X) {
           if (X && it.nB == 0) return;
           wait(&B.q_empty[X], loads[X] + 1);
           ++loads[X];
+          if (lane != 0) return;
           mbar_expect_tx(&B.q_full[X], (uint32_t)(nt * p.G * D * 2));
           for (int d = 0; d < D; d += 64)
             tma_load_3d(smem + S::kQ + X * S::kTile + d * 256, &tm_q, d, it.hk * p.G,
                         it.base + it.tok + X * nt, &B.q_full[X]);
         };
+        // Page of this lane's part of key tile j (prefix): a tile is up to eight pages, one
+        // lane each, or part of one; -1 past the prefix. Looked up a tile ahead.
+        auto page_of = [&](int j) -> int {
+          const int key = (it.kv0 + j) * kKeys + lane * min(p.page, kKeys);
+          return lane * p.page < kKeys && key < p.shared ? p.table[key >> p.page_shift] : -1;
+        };
+        int page = kPrefix ? page_of(0) : 0;
         auto load_kv = [&](const CUtensorMap* tm, int j, bool raw) {
           const int st = slot % kStages;
           wait(&B.kv_empty[st], slot / kStages + 1);
@@ -429,18 +518,34 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
           uint64_t* bar = raw ? &B.v_raw[st] : &B.kv_full[st];
           (raw ? raw_uses : kv_uses) ^= 1u << st;
           is_raw = (is_raw & ~(1u << st)) | ((uint32_t)raw << st);
-          mbar_expect_tx(bar, S::kTile);
-          for (int d = 0; d < D; d += 64)
-            tma_load_3d(smem + S::kRing + st * S::kTile + d * 256, tm, d, it.hk,
-                        it.base + j * kKeys, bar);
+          char* dst = smem + S::kRing + st * S::kTile;
+          if constexpr (kPrefix) {
+            const int key = (it.kv0 + j) * kKeys, box = min(p.page, kKeys);
+            const int rows = min(kKeys, p.shared - key);
+            if (lane == 0) mbar_expect_tx(bar, (uint32_t)(rows * D * 2));
+            __syncwarp();
+            if (lane * box < rows) {
+              const bool ok = page >= 0 && page < p.n_pages;
+              if (!ok) set_status(p.status, GDN_DEV_BAD_PAGE_TABLE);
+              // a page that does not exist: past the tensor's end, which reads zeros
+              const int64_t group = (((int64_t)(ok ? page : p.n_pages) * p.Hk + (ok ? it.hk : 0))
+                                     << p.page_shift) + (ok ? key & (p.page - 1) : 0);
+              tma_load_4d(dst + lane * box * D * 2, tm, 0, 0, 0, (int)(group >> 3), bar);
+            }
+          } else {
+            mbar_expect_tx(bar, S::kTile);
+            for (int d = 0; d < D; d += 64)
+              tma_load_3d(dst + d * 256, tm, d, it.hk, it.base + j * kKeys, bar);
+          }
         };
         load_q(0);
         load_kv(&tm_k, 0, false);
         load_q(1);
-        load_kv(&tm_v, 0, it.mask0 == 0);
-        for (int j = 1; j < n; ++j) {
-          load_kv(&tm_k, j, false);
+        for (int j = 0; j < n; ++j) {
+          if (j > 0) load_kv(&tm_k, j, false);
+          const int page_next = kPrefix && j + 1 < n ? page_of(j + 1) : 0;
           load_kv(&tm_v, j, j >= it.mask0);
+          page = page_next;
         }
       }
       if (!wait.ok) {  // copies in flight end before the CTA does
@@ -457,8 +562,8 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
       const uint64_t dQ = sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024);
-      const uint64_t dK = sdesc_sw128(smem_addr(smem + S::kRing), 16, 1024);
-      const uint64_t dV = sdesc_sw128(smem_addr(smem + S::kRing), 16384, 1024);
+      const uint64_t dK = sdesc_sw128(smem_addr(smem + S::kRing), 16, S::kGroup);
+      const uint64_t dV = sdesc_sw128(smem_addr(smem + S::kRing), S::kHalf, S::kGroup);
       uint32_t base = 0;                          // ring place of the item's K_0
       // parities to wait for, a bit per barrier
       uint32_t kvs = 0, fixes = 0, qs = 0, ps = 0, os = 3;
@@ -476,8 +581,8 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
         const uint64_t a = dQ + X * (S::kTile >> 4), b = dK + st * (S::kTile >> 4);
 #pragma unroll
         for (int d = 0; d < D; d += 16) {
-          const uint32_t off = ((d >> 6) * 16384 + (d & 63) * 2) >> 4;
-          umma_bf16(tmem + X * 128, a + off, b + off, kIdS, d > 0);
+          umma_bf16(tmem + X * 128, a + (((d >> 6) * 16384 + (d & 63) * 2) >> 4),
+                    b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kIdS, d > 0);
         }
         umma_commit(&B.s_full[X]);
         if (last) umma_commit(&B.q_empty[X]);
@@ -529,7 +634,8 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
               const uint64_t b = dV + vst * (S::kTile >> 4);
 #pragma unroll
               for (int t = 0; t < kKeys; t += 16)
-                umma_bf16_ts(tmem + 256 + X * D, tmem + X * 128 + (t >> 1), b + t * 8, kIdO,
+                umma_bf16_ts(tmem + 256 + X * D, tmem + X * 128 + (t >> 1),
+                             b + ((t >> 3) * S::kGroup >> 4), kIdO,
                              j > 0 || t > 0);
               if (j == nX - 1) umma_commit(&B.o_full[X]);
             }
@@ -550,8 +656,15 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
     }
     // ---------------------------------------------------------------- work items
     if (warp == 10) {
-      PromptItems items{bounds, p.N, 2 * nt, p.Hk, 0, 0};
-      items.init();
+      auto items = [&] {
+        if constexpr (kPrefix) {
+          return PrefixItems(p, parts, 2 * nt);
+        } else {
+          PromptItems x{bounds, p.N, 2 * nt, p.Hk, 0, 0};
+          x.init();
+          return x;
+        }
+      }();
       const int grid = (int)gridDim.x, b = (int)blockIdx.x;
       for (uint32_t k = 0;; ++k) {
         // every other round dealt backwards, which evens out the falling sizes
@@ -585,12 +698,14 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
         wait(&B.v_raw[st], raws >> st);
         raws ^= 1u << st;
         char* tile = smem + S::kRing + st * S::kTile;
-        const int rows = it.len - j * kKeys;  // of this tile inside the sequence
+        // rows of this tile inside the sequence, the prefix
+        const int rows = (kPrefix ? p.shared : it.len) - (it.kv0 + j) * kKeys;
         bool found = false;
 #pragma unroll 4
         for (int i = tid; i < S::kTile / 16; i += 128) {
           uint4* v = reinterpret_cast<uint4*>(tile) + i;
-          if (((i >> 3) & 127) >= rows) {
+          const int row = kPrefix ? i / D * 8 + ((i >> 3) & 7) : (i >> 3) & 127;
+          if (row >= rows) {
             *v = make_uint4(0, 0, 0, 0);
           } else {
             const uint4 x = *v;  // a bf16 exponent of all ones, in either half
@@ -613,6 +728,22 @@ attn_prompt_kernel(const AttnParams p, const __grid_constant__ CUtensorMap tm_q,
   __syncthreads();
   tc_fence_after();
   if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// One launch over the q rows [T, H, D]; the items' number bounds the grid.
+template <int D, bool kPrefix>
+bool launch_attn_tc(const AttnParams& p, const PrefixParts& parts, const CUtensorMap& tm_k,
+                    const CUtensorMap& tm_v, int64_t items, cudaStream_t s) {
+  const uint32_t box[3] = {64, (uint32_t)p.G, (uint32_t)(kRows / p.G)};
+  const uint64_t dim[3] = {D, (uint64_t)p.H, (uint64_t)p.T}, str[2] = {D * 2, (uint64_t)p.H * D * 2};
+  CUtensorMap tm_q;
+  if (!encode_bf16_tmap(&tm_q, p.q, 3, dim, str, box)) return false;
+  const auto kernel = attn_tc_kernel<D, kPrefix>;
+  constexpr int smem = AttnSmem<D, kPrefix>::kBytes;
+  ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+  const int64_t sms = num_sms();
+  kernel<<<(unsigned)(items < sms ? items : sms), kAttnThreads, smem, s>>>(p, parts, tm_q, tm_k, tm_v);
+  return true;
 }
 
 }  // namespace gdn

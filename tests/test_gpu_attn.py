@@ -325,6 +325,38 @@ def test_decode_shared_equals_unshared():
         check_decode([512 + 3 * i for i in range(12)], 8, 2, 128, 32, shared=shared, seed=6)
 
 
+@pytest.mark.parametrize("what", ["nan", "inf", "lowest"])
+@pytest.mark.parametrize("shared", [0, 128, 160])
+def test_decode_unseen_values_have_no_influence(what, shared):
+    """Values that a later token of the batch or a longer sequence sees, and an earlier token
+    or a shorter sequence does not: NaN, infinities, the type's lowest value."""
+    bad = dict(nan=float("nan"), inf=float("inf"), lowest=torch.finfo(BF).min)[what]
+    g = torch.Generator().manual_seed(11)
+    lens, H, Hk, D, page, nq = [190, 100, 133, 60], 4, 2, 128, 16, 4
+    if shared == 0:
+        lens = [190, 100, 50, 3]
+    kc, vc, table = make_cache(g, lens, Hk, D, page, shared)
+    q = randn(g, 4, nq, H, D)
+    kz, vz = kc.clone(), vc.clone()
+    spots = [(0, lens[0] - 1), (0, lens[0] - 2), (1, 98), (2, lens[2] - 3)]
+    for n, t in spots:  # last tokens; with a prefix, token 98 belongs to all
+        p = int(table[n, t // page])
+        for c, z in ((kc, kz), (vc, vz)):
+            c[p, :, t % page] = bad
+            z[p, :, t % page] = 0
+    out = B.gdn_attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(),
+                            torch.tensor(lens, dtype=torch.int32).cuda(), shared, out_dtype=F32)
+    ref, mag, rl = A.decode(np64(q), np64(kz), np64(vz), table.numpy(), lens, shared)
+    hit = np.zeros((4, nq), bool)  # rows that see a spoilt key
+    for n in range(4):
+        for i in range(nq):
+            mine = [t for m, t in spots if m == n or t < shared]
+            hit[n, i] = any(t <= lens[n] - nq + i for t in mine)
+    assert hit.any() and not hit.all()
+    close_attention(out.view(4 * nq, H, D), None, ref.reshape(4 * nq, H, D),
+                    mag.reshape(4 * nq, H, D), None, ~hit.reshape(-1))
+
+
 def test_decode_bad_pages_and_lengths():
     g = torch.Generator().manual_seed(3)
     kc, vc, table = make_cache(g, [100, 90], 2, 64, 16, fill=0.0)
