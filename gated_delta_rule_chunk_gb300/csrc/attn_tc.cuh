@@ -95,6 +95,15 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
+// True in one lane of a converged warp. Code around it stays uniform, so that the MMA
+// operands live in uniform registers: issuing from `lane == 0` instead costs a move per
+// operand word, and the issuing warp, whose instructions the row warps keep evicting from
+// the instruction cache, then takes longer than the products (5,000 cycles a step).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
+  return p != 0;
+}
 // D[tmem] += A[tmem] * B: A is M x 16 bf16, two to a 32-bit column.
 __device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
                                              uint32_t idesc, uint32_t accumulate) {
@@ -261,7 +270,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   int* bounds = reinterpret_cast<int*>(smem + S::kBounds);
   auto& B = *reinterpret_cast<AttnBars<kStages>*>(smem + S::kBars);
   static_assert(sizeof(AttnBars<kStages>) <= 512, "barrier area");
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int nt = kRows / p.G;  // tokens of a row tile
   if (kPrefix) pdl_release();  // the decode kernel needs nothing from here
 
@@ -314,7 +323,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = B.tmem;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
   Waiter wait(p.status);
 
   // ------------------------------------------------------------------ rows
@@ -558,7 +567,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       }
     }
     // ---------------------------------------------------------------- products
-    if (warp == 9 && lane == 0) {
+    if (warp == 9) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
       const uint64_t dQ = sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024);
@@ -579,38 +588,45 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         }
         tc_fence_after();
         const uint64_t a = dQ + X * (S::kTile >> 4), b = dK + st * (S::kTile >> 4);
+        if (elect_one()) {
 #pragma unroll
-        for (int d = 0; d < D; d += 16) {
-          umma_bf16(tmem + X * 128, a + (((d >> 6) * 16384 + (d & 63) * 2) >> 4),
-                    b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kIdS, d > 0);
+          for (int d = 0; d < D; d += 16) {
+            umma_bf16(tmem + X * 128, a + (((d >> 6) * 16384 + (d & 63) * 2) >> 4),
+                      b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kIdS, d > 0);
+          }
+          umma_commit(&B.s_full[X]);
+          if (last) umma_commit(&B.q_empty[X]);
         }
-        umma_commit(&B.s_full[X]);
-        if (last) umma_commit(&B.q_empty[X]);
+        __syncwarp();
       };
-      wait(&B.item_full[0], 0);
-      int nx[2] = {B.item[0].nA, B.item[0].nB}, mask0 = B.item[0].mask0;
-      bool valid = B.item[0].valid && wait.ok;
-      mbar_arrive(&B.item_empty[0]);
-      if (valid) {
+      auto commit = [&](uint64_t* bar) {
+        if (elect_one()) umma_commit(bar);
+        __syncwarp();
+      };
+      // The fields of item k that count here, the same in all lanes.
+      auto item = [&](uint32_t k, int (&nx)[2], int& mask0) {
+        wait(&B.item_full[k & 1], k >> 1);
+        const AttnItem& it = B.item[k & 1];
+        const bool ok = __shfl_sync(0xffffffffu, it.valid && wait.ok, 0);
+        nx[0] = ok ? __shfl_sync(0xffffffffu, it.nA, 0) : 0;
+        nx[1] = ok ? __shfl_sync(0xffffffffu, it.nB, 0) : 0;
+        mask0 = __shfl_sync(0xffffffffu, it.mask0, 0);
+        if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
+        __syncwarp();
+      };
+      int nx[2], mask0;
+      item(0, nx, mask0);
+      if (nx[0]) {
         scores(0, 0, true, true, nx[0] == 1);
         if (nx[1]) scores(1, 0, false, true, nx[1] == 1);
-        umma_commit(&B.kv_empty[0]);
+        commit(&B.kv_empty[0]);
       }
-      for (uint32_t k = 1; valid; ++k) {
+      for (uint32_t k = 1; nx[0]; ++k) {
         const int n = max(nx[0], nx[1]);
         int next[2] = {0, 0}, next0 = 0;
         for (int j = 0; j < n; ++j) {
           const bool end = j == n - 1;
-          if (end) {
-            wait(&B.item_full[k & 1], k >> 1);
-            valid = B.item[k & 1].valid && wait.ok;
-            if (valid) {
-              next[0] = B.item[k & 1].nA;
-              next[1] = B.item[k & 1].nB;
-              next0 = B.item[k & 1].mask0;
-            }
-            mbar_arrive(&B.item_empty[k & 1]);
-          }
+          if (end) item(k, next, next0);
           const uint32_t vp = base + 2 * j + 1, vst = vp % kStages;
           if (j >= mask0) {
             wait(&B.v_fixed[vst], fixes >> vst);
@@ -632,12 +648,14 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
               }
               tc_fence_after();
               const uint64_t b = dV + vst * (S::kTile >> 4);
+              if (elect_one()) {
 #pragma unroll
-              for (int t = 0; t < kKeys; t += 16)
-                umma_bf16_ts(tmem + 256 + X * D, tmem + X * 128 + (t >> 1),
-                             b + ((t >> 3) * S::kGroup >> 4), kIdO,
-                             j > 0 || t > 0);
-              if (j == nX - 1) umma_commit(&B.o_full[X]);
+                for (int t = 0; t < kKeys; t += 16)
+                  umma_bf16_ts(tmem + 256 + X * D, tmem + X * 128 + (t >> 1),
+                               b + ((t >> 3) * S::kGroup >> 4), kIdO, j > 0 || t > 0);
+                if (j == nX - 1) umma_commit(&B.o_full[X]);
+              }
+              __syncwarp();
             }
             const bool more = j + 1 < nX;
             if (more || (end && nextX)) {
@@ -645,8 +663,8 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
               load = false;
             }
           }
-          umma_commit(&B.kv_empty[vst]);
-          if (!end || valid) umma_commit(&B.kv_empty[(vp + 1) % kStages]);
+          commit(&B.kv_empty[vst]);
+          if (!end || next[0]) commit(&B.kv_empty[(vp + 1) % kStages]);
         }
         base += 2 * n;
         nx[0] = next[0];
