@@ -27,6 +27,8 @@
 
 #include <cuda.h>
 
+#include <type_traits>
+
 #include "attn_common.cuh"
 #include "umma.cuh"
 #include "warp_mma.cuh"
@@ -95,22 +97,51 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
       : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
   return d;
 }
-// True in one lane of a converged warp. Code around it stays uniform, so that the MMA
-// operands live in uniform registers: issuing from `lane == 0` instead costs a move per
-// operand word, and the issuing warp, whose instructions the row warps keep evicting from
-// the instruction cache, then takes longer than the products (5,000 cycles a step).
-__device__ __forceinline__ bool elect_one() {
+// The warp that issues the MMAs runs converged, and everything it issues is predicated on one
+// lane, chosen once: then descriptors and addresses live in uniform registers and the loop is
+// straight-line. (Issued from a `lane == 0` branch, every operand word takes a move, and a
+// step's issue takes longer than its products: 5,000 cycles at D = 128 for 2,048 of MMAs.)
+__device__ __forceinline__ uint32_t elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}\n" : "=r"(p));
-  return p != 0;
+  return p;
 }
-// D[tmem] += A[tmem] * B: A is M x 16 bf16, two to a 32-bit column.
-__device__ __forceinline__ void umma_bf16_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc,
-                                             uint32_t idesc, uint32_t accumulate) {
+// The same value in all lanes, known as such to the compiler.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __reduce_or_sync(0xffffffffu, x); }
+
+// D[tmem] (+)= A * B with A and B in shared memory; `el` != 0 in the issuing lane only.
+__device__ __forceinline__ void mma_ss(uint32_t el, uint32_t d, uint32_t a_lo, uint32_t a_hi,
+                                       uint32_t b_lo, uint32_t b_hi, uint32_t idesc, uint32_t acc) {
   asm volatile(
-      "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-      " tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "{\n .reg .pred p, e;\n .reg .b64 a, b;\n setp.ne.b32 p, %6, 0;\n setp.ne.b32 e, %7, 0;\n"
+      " mov.b64 a, {%1, %2};\n mov.b64 b, {%3, %4};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %5, p;\n}\n" ::"r"(d),
+      "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(el)
+      : "memory");
+}
+// The same with A in TMEM: M x 16 bf16, two to a 32-bit column.
+__device__ __forceinline__ void mma_ts(uint32_t el, uint32_t d, uint32_t a, uint32_t b_lo,
+                                       uint32_t b_hi, uint32_t idesc, uint32_t acc) {
+  asm volatile(
+      "{\n .reg .pred p, e;\n .reg .b64 b;\n setp.ne.b32 p, %5, 0;\n setp.ne.b32 e, %6, 0;\n"
+      " mov.b64 b, {%2, %3};\n"
+      " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %4, p;\n}\n" ::"r"(d),
+      "r"(a), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(acc), "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ void mma_commit(uint32_t el, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+      " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}\n" ::"r"(
+          smem_addr(bar)),
+      "r"(el)
+      : "memory");
+}
+__device__ __forceinline__ void arrive_one(uint32_t el, uint64_t* bar) {
+  asm volatile(
+      "{\n .reg .pred e;\n .reg .b64 st;\n setp.ne.b32 e, %1, 0;\n"
+      " @e mbarrier.arrive.shared::cta.b64 st, [%0];\n}\n" ::"r"(smem_addr(bar)),
+      "r"(el)
       : "memory");
 }
 __device__ __forceinline__ void tmem_st32u(uint32_t taddr, const uint32_t (&v)[32]) {
@@ -164,14 +195,16 @@ struct AttnBars {
 
 // A bounded wait: once one has run out, this thread waits for nothing any more.
 struct Waiter {
-  bool ok = true;
+  uint32_t limit = kPolls;
   int32_t* status;
   __device__ explicit Waiter(int32_t* s) : status(s) {}
+  __device__ __forceinline__ bool ok() const { return limit != 0; }
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t phase) {
-    if (ok && !mbar_wait(bar, phase & 1u, kPolls)) {
-      ok = false;
-      set_status(status, GDN_DEV_TIMEOUT);
-    }
+    if (mbar_try_wait(bar, phase & 1u)) return;
+    for (uint32_t i = 0; i < limit; ++i)
+      if (mbar_try_wait(bar, phase & 1u)) return;
+    if (limit) set_status(status, GDN_DEV_TIMEOUT);
+    limit = 0;
   }
 };
 
@@ -323,7 +356,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = __shfl_sync(0xffffffffu, B.tmem, 0);
+  const uint32_t tmem = B.tmem;
   Waiter wait(p.status);
 
   // ------------------------------------------------------------------ rows
@@ -340,7 +373,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       const AttnItem it = B.item[k & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
-      if (!it.valid || !wait.ok) break;
+      if (!it.valid || !wait.ok()) break;
       const int n = X ? it.nB : it.nA;
       if (n == 0) continue;
       const int tok = it.tok + X * nt + rt;
@@ -501,7 +534,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         const AttnItem it = B.item[k & 1];
         if constexpr (kPrefix) __syncwarp();
         if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
-        if (!it.valid || !wait.ok) break;
+        if (!it.valid || !wait.ok()) break;
         const int n = max(it.nA, it.nB);
         auto load_q = [&](int X) {
           if (X && it.nB == 0) return;
@@ -557,7 +590,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           page = page_next;
         }
       }
-      if (!wait.ok) {  // copies in flight end before the CTA does
+      if (!wait.ok()) {  // copies in flight end before the CTA does
         for (uint32_t i = 0; i < kStages && i < slot; ++i) {
           if ((is_raw >> i) & 1) mbar_wait(&B.v_raw[i], ((raw_uses >> i) & 1) ^ 1, kPolls);
           else mbar_wait(&B.kv_full[i], ((kv_uses >> i) & 1) ^ 1, kPolls);
@@ -570,106 +603,119 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
     if (warp == 9) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
+      constexpr uint32_t kT = S::kTile >> 4;
+      // descriptor words (sdesc_sw128): the low ones hold the address, the high ones the strides
       const uint64_t dQ = sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024);
       const uint64_t dK = sdesc_sw128(smem_addr(smem + S::kRing), 16, S::kGroup);
       const uint64_t dV = sdesc_sw128(smem_addr(smem + S::kRing), S::kHalf, S::kGroup);
-      uint32_t base = 0;                          // ring place of the item's K_0
+      const uint32_t q_lo = uniform((uint32_t)dQ), k_lo = uniform((uint32_t)dK),
+                     v_lo = uniform((uint32_t)dV);
+      constexpr uint32_t kHi = (1u << 14) | (2u << 29);
+      constexpr uint32_t kQHi = kHi | (1024 >> 4), kKHi = kHi | (S::kGroup >> 4);
+      const uint32_t el = elect_one(), tm = uniform(tmem);
       // parities to wait for, a bit per barrier
       uint32_t kvs = 0, fixes = 0, qs = 0, ps = 0, os = 3;
-      auto scores = [&](int X, uint32_t place, bool load, bool first, bool last) {
-        const uint32_t st = place % kStages;
-        if (first) {
-          wait(&B.q_full[X], qs >> X);
-          qs ^= 1u << X;
+
+      auto wait_kv = [&](uint32_t st) {
+        wait(&B.kv_full[st], kvs >> st);
+        kvs ^= 1u << st;
+      };
+      auto wait_v = [&](uint32_t st, bool masked) {
+        if (masked) {
+          wait(&B.v_fixed[st], fixes >> st);
+          fixes ^= 1u << st;
+        } else {
+          wait_kv(st);
         }
-        if (load) {
-          wait(&B.kv_full[st], kvs >> st);
-          kvs ^= 1u << st;
+      };
+      auto scores = [&](auto x, uint32_t st, bool last) {  // S_X = Q_X K^T
+        constexpr int X = decltype(x)::value;
+        tc_fence_after();
+        const uint32_t b = k_lo + st * kT;
+#pragma unroll
+        for (int d = 0; d < D; d += 16)
+          mma_ss(el, tm + X * 128, q_lo + X * kT + (((d >> 6) * 16384 + (d & 63) * 2) >> 4), kQHi,
+                 b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kKHi, kIdS, d > 0);
+        mma_commit(el, &B.s_full[X]);
+        if (last) mma_commit(el, &B.q_empty[X]);
+      };
+      auto weigh = [&](auto x, uint32_t st, bool first, bool last) {  // O_X (+)= P_X V
+        constexpr int X = decltype(x)::value;
+        wait(&B.p_full[X], ps >> X);
+        ps ^= 1u << X;
+        if (first) {
+          wait(&B.o_empty[X], os >> X);
+          os ^= 1u << X;
         }
         tc_fence_after();
-        const uint64_t a = dQ + X * (S::kTile >> 4), b = dK + st * (S::kTile >> 4);
-        if (elect_one()) {
+        const uint32_t b = v_lo + st * kT;
 #pragma unroll
-          for (int d = 0; d < D; d += 16) {
-            umma_bf16(tmem + X * 128, a + (((d >> 6) * 16384 + (d & 63) * 2) >> 4),
-                      b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kIdS, d > 0);
-          }
-          umma_commit(&B.s_full[X]);
-          if (last) umma_commit(&B.q_empty[X]);
-        }
-        __syncwarp();
+        for (int t = 0; t < kKeys; t += 16)
+          mma_ts(el, tm + 256 + X * D, tm + X * 128 + (t >> 1), b + ((t >> 3) * S::kGroup >> 4),
+                 kKHi, kIdO, t > 0 || !first);
+        if (last) mma_commit(el, &B.o_full[X]);
       };
-      auto commit = [&](uint64_t* bar) {
-        if (elect_one()) umma_commit(bar);
-        __syncwarp();
+      auto wait_q = [&](int X) {
+        wait(&B.q_full[X], qs >> X);
+        qs ^= 1u << X;
       };
-      // The fields of item k that count here, the same in all lanes.
-      auto item = [&](uint32_t k, int (&nx)[2], int& mask0) {
+      // The fields of item k that count here (no tiles: the end).
+      auto item = [&](uint32_t k, int& a, int& b, int& mask0) {
         wait(&B.item_full[k & 1], k >> 1);
         const AttnItem& it = B.item[k & 1];
-        const bool ok = __shfl_sync(0xffffffffu, it.valid && wait.ok, 0);
-        nx[0] = ok ? __shfl_sync(0xffffffffu, it.nA, 0) : 0;
-        nx[1] = ok ? __shfl_sync(0xffffffffu, it.nB, 0) : 0;
-        mask0 = __shfl_sync(0xffffffffu, it.mask0, 0);
-        if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
-        __syncwarp();
+        const bool ok = it.valid && wait.ok();
+        a = (int)uniform(ok ? it.nA : 0);
+        b = (int)uniform(ok ? it.nB : 0);
+        mask0 = (int)uniform(it.mask0);
+        arrive_one(el, &B.item_empty[k & 1]);
       };
-      int nx[2], mask0;
-      item(0, nx, mask0);
-      if (nx[0]) {
-        scores(0, 0, true, true, nx[0] == 1);
-        if (nx[1]) scores(1, 0, false, true, nx[1] == 1);
-        commit(&B.kv_empty[0]);
-      }
-      for (uint32_t k = 1; nx[0]; ++k) {
-        const int n = max(nx[0], nx[1]);
-        int next[2] = {0, 0}, next0 = 0;
-        for (int j = 0; j < n; ++j) {
-          const bool end = j == n - 1;
-          if (end) item(k, next, next0);
-          const uint32_t vp = base + 2 * j + 1, vst = vp % kStages;
-          if (j >= mask0) {
-            wait(&B.v_fixed[vst], fixes >> vst);
-            fixes ^= 1u << vst;
-          } else {
-            wait(&B.kv_full[vst], kvs >> vst);
-            kvs ^= 1u << vst;
-          }
-          bool load = true;  // the next K tile is still to be waited for
-#pragma unroll 1
-          for (int X = 0; X < 2; ++X) {
-            const int nX = X ? nx[1] : nx[0], nextX = X ? next[1] : next[0];
-            if (j < nX) {
-              wait(&B.p_full[X], ps >> X);
-              ps ^= 1u << X;
-              if (j == 0) {
-                wait(&B.o_empty[X], os >> X);
-                os ^= 1u << X;
-              }
-              tc_fence_after();
-              const uint64_t b = dV + vst * (S::kTile >> 4);
-              if (elect_one()) {
-#pragma unroll
-                for (int t = 0; t < kKeys; t += 16)
-                  umma_bf16_ts(tmem + 256 + X * D, tmem + X * 128 + (t >> 1),
-                               b + ((t >> 3) * S::kGroup >> 4), kIdO, j > 0 || t > 0);
-                if (j == nX - 1) umma_commit(&B.o_full[X]);
-              }
-              __syncwarp();
-            }
-            const bool more = j + 1 < nX;
-            if (more || (end && nextX)) {
-              scores(X, base + 2 * (j + 1), load, !more, more ? j + 2 == nX : nextX == 1);
-              load = false;
-            }
-          }
-          commit(&B.kv_empty[vst]);
-          if (!end || next[0]) commit(&B.kv_empty[(vp + 1) % kStages]);
+      constexpr std::integral_constant<int, 0> A{};
+      constexpr std::integral_constant<int, 1> Bt{};
+      int nA, nB, mask0;
+      uint32_t kst = 0;  // ring place of the K tile at hand (its V tile is the next place)
+      item(0, nA, nB, mask0);
+      if (nA) {
+        wait_q(0);
+        wait_kv(0);
+        scores(A, 0, nA == 1);
+        if (nB) {
+          wait_q(1);
+          scores(Bt, 0, nB == 1);
         }
-        base += 2 * n;
-        nx[0] = next[0];
-        nx[1] = next[1];
-        mask0 = next0;
+        mma_commit(el, &B.kv_empty[0]);
+      }
+      for (uint32_t k = 1; nA; ++k) {
+        const int n = max(nA, nB);
+        int a2 = 0, b2 = 0, m2 = 0;  // the next item
+        wait_v(kst + 1, mask0 == 0);
+        for (int j = 0; j < n; ++j) {
+          const uint32_t vst = kst + 1, nst = kst + 2 == kStages ? 0 : kst + 2;
+          const bool end = j == n - 1;
+          if (end) item(k, a2, b2, m2);
+          if (j < nA) weigh(A, vst, j == 0, j == nA - 1);
+          const bool k_next = !end || a2;  // another K tile follows
+          if (k_next) wait_kv(nst);
+          if (j + 1 < nA) {
+            scores(A, nst, j + 2 == nA);
+          } else if (end && a2) {
+            wait_q(0);
+            scores(A, nst, a2 == 1);
+          }
+          if (!end) wait_v(nst + 1, j + 1 >= mask0);
+          if (j < nB) weigh(Bt, vst, j == 0, j == nB - 1);
+          mma_commit(el, &B.kv_empty[vst]);
+          if (j + 1 < nB) {
+            scores(Bt, nst, j + 2 == nB);
+          } else if (end && b2) {
+            wait_q(1);
+            scores(Bt, nst, b2 == 1);
+          }
+          if (k_next) mma_commit(el, &B.kv_empty[nst]);
+          kst = nst;
+        }
+        nA = a2;
+        nB = b2;
+        mask0 = m2;
       }
     }
     // ---------------------------------------------------------------- work items
@@ -695,7 +741,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         }
         __syncwarp();
         // a round dealt backwards may skip this CTA in the last, partial round only
-        if (!it.valid || !wait.ok) break;
+        if (!it.valid || !wait.ok()) break;
       }
     }
     __syncwarp();
@@ -709,7 +755,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       const AttnItem it = B.item[k & 1];
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
-      if (!it.valid || !wait.ok) break;
+      if (!it.valid || !wait.ok()) break;
       const int n = max(it.nA, it.nB);
       for (int j = it.mask0; j < n; ++j) {
         const uint32_t st = (base + 2 * j + 1) % kStages;
