@@ -38,7 +38,7 @@ namespace gdn {
 constexpr int kAttnThreads = 512;
 constexpr int kRows = 128;           // rows of a tile
 constexpr int kKeys = 128;           // keys of a tile
-constexpr int kAttnSeqs = 4096;      // sequences of one launch
+constexpr int kAttnSeqs = 2048;      // sequences of one launch
 constexpr uint32_t kPolls = 1u << 22;
 constexpr float kGrow = 8.0f;
 
@@ -70,8 +70,8 @@ struct AttnSmem {
   static constexpr int kHalf = kPrefix ? 1024 : 128 * 128;  // ... from a half to the other
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kQ = 0, kRing = 2 * kTile;
-  static constexpr int kBounds = kRing + kStages * kTile;      // sanitized cu_seqlens
-  static constexpr int kBars = kBounds + 4 * (kAttnSeqs + 4);
+  static constexpr int kBounds = kRing + kStages * kTile;      // sanitized cu_seqlens, pairs
+  static constexpr int kBars = kBounds + 8 * (kAttnSeqs + 4);
   static constexpr int kBytes = kBars + 512 + 1024;            // + alignment of the tiles
 };
 
@@ -210,50 +210,61 @@ struct Waiter {
 
 // The work items of a batch of prompts, the ones with most keys first: pair i of a sequence
 // is its tokens [i * span, (i + 1) * span); the pairs of all sequences are numbered by
-// falling i, so that those that start last are the shortest. Called by one warp.
+// falling i, so that those that start last are the shortest. Called by one warp; each lane
+// keeps the pair count of one sequence in a register (more sequences: in shared memory),
+// because the first tile's loads wait for the first item.
 struct PromptItems {
   const int* bounds;  // [N + 1] in shared memory
-  int N, span, Hk, total;  // total: items of all key heads
-  int most;                // pairs of the longest sequence
+  const int* pairs;   // [N] in shared memory
+  int N, span, Hk, mine, most, total;  // most: pairs of the longest sequence; total: items
 
-  __device__ int pairs(int n) const { return (bounds[n + 1] - bounds[n] + span - 1) / span; }
-  // pairs numbered i or higher, over all sequences
-  __device__ int count(int i) const {
-    int c = 0;
-    for (int n = threadIdx.x & 31; n < N; n += 32) c += max(0, pairs(n) - i);
-    return __reduce_add_sync(0xffffffffu, c);
-  }
-  __device__ void init() {
-    int m = 0;
-    for (int n = threadIdx.x & 31; n < N; n += 32) m = max(m, pairs(n));
+  __device__ PromptItems(const int* bounds_, const int* pairs_, int N_, int span_, int Hk_)
+      : bounds(bounds_), pairs(pairs_), N(N_), span(span_), Hk(Hk_) {
+    const int lane = threadIdx.x & 31;
+    mine = lane < N ? pairs[lane] : 0;
+    int m = mine;
+    for (int n = lane + 32; n < N; n += 32) m = max(m, pairs[n]);
     most = __reduce_max_sync(0xffffffffu, m);
     total = count(0) * Hk;
+  }
+  // pairs numbered i or higher, over all sequences
+  __device__ int count(int i) const {
+    int c = max(0, mine - i);
+    for (int n = (threadIdx.x & 31) + 32; n < N; n += 32) c += max(0, pairs[n] - i);
+    return __reduce_add_sync(0xffffffffu, c);
   }
   __device__ AttnItem get(int idx, int nt) const {
     AttnItem it{};
     if (idx >= total) return it;
     const int s = idx / Hk, lane = threadIdx.x & 31;
-    int lo = 0, hi = most - 1;  // the largest i with count(i) > s
-    while (lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (count(m) > s) lo = m;
-      else hi = m - 1;
-    }
-    int r = s - count(lo + 1);  // the r-th sequence that has a pair lo
-    for (int n0 = 0; n0 < N; n0 += 32) {
-      const bool has = n0 + lane < N && pairs(n0 + lane) > lo;
-      const uint32_t mask = __ballot_sync(0xffffffffu, has);
-      const int c = __popc(mask);
-      if (r < c) {
-        const int n = n0 + __fns(mask, 0, r + 1);
-        it.base = bounds[n];
-        it.len = bounds[n + 1] - bounds[n];
-        break;
+    int i, n = 0;
+    if (N == 1) {
+      i = most - 1 - s;
+    } else {
+      int lo = 0, hi = most - 1;  // the largest i with count(i) > s
+      while (lo < hi) {
+        const int m = (lo + hi + 1) >> 1;
+        if (count(m) > s) lo = m;
+        else hi = m - 1;
       }
-      r -= c;
+      i = lo;
+      int r = s - count(i + 1);  // of the sequences that have a pair i, the r-th
+      for (int n0 = 0; n0 < N; n0 += 32) {
+        const bool has = n0 + lane < N && (n0 ? pairs[n0 + lane] : mine) > i;
+        const uint32_t mask = __ballot_sync(0xffffffffu, has);
+        const bool it_is = has && __popc(mask & ((1u << lane) - 1u)) == r;
+        const uint32_t hit = __ballot_sync(0xffffffffu, it_is);
+        if (hit) {
+          n = n0 + __ffs(hit) - 1;
+          break;
+        }
+        r -= __popc(mask);
+      }
     }
-    it.tok = lo * span;
-    it.hk = idx % Hk;
+    it.base = bounds[n];
+    it.len = bounds[n + 1] - it.base;
+    it.tok = i * span;
+    it.hk = idx - s * Hk;
     it.nA = (min(it.tok + nt, it.len) + kKeys - 1) / kKeys;
     it.nB = it.tok + nt < it.len ? (min(it.tok + 2 * nt, it.len) + kKeys - 1) / kKeys : 0;
     it.mask0 = (it.tok + 1) / kKeys;
@@ -301,6 +312,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   int* bounds = reinterpret_cast<int*>(smem + S::kBounds);
+  int* pairs = bounds + kAttnSeqs + 4;  // pairs of row tiles of each sequence
   auto& B = *reinterpret_cast<AttnBars<kStages>*>(smem + S::kBars);
   static_assert(sizeof(AttnBars<kStages>) <= 512, "barrier area");
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -332,26 +344,30 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
     tmem_relinquish();
   }
   if (!kPrefix && warp == 10) {  // cu_seqlens, each entry clamped and raised to the largest before it
-    int carry = p.cu ? min(max(p.cu[0], 0), p.T) : 0;
-    bool bad = p.cu && p.cu[0] != carry;
-    if (lane == 0) bounds[0] = carry;
-    for (int n0 = 1; n0 <= p.N; n0 += 32) {
+    const int span = 2 * nt;
+    int carry = 0;
+    bool bad = false;
+    for (int n0 = 0; n0 <= p.N; n0 += 32) {
       const int n = n0 + lane;
-      const int raw = n <= p.N ? (p.cu ? p.cu[n] : p.T) : 0;
-      int e = n <= p.N ? min(max(raw, 0), p.T) : 0;
+      const int raw = n > p.N ? 0 : p.cu ? p.cu[n] : n ? p.T : 0;
+      int e = min(max(raw, 0), p.T);
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, e, o);
         if (lane >= o) e = max(e, x);
       }
       e = max(e, carry);
+      int before = __shfl_up_sync(0xffffffffu, e, 1);
+      if (lane == 0) before = n ? carry : e;
       if (n <= p.N) {
         bounds[n] = e;
+        if (n) pairs[n - 1] = (e - before + span - 1) / span;
         bad |= raw != e;
       }
       carry = __shfl_sync(0xffffffffu, e, 31);
     }
     if (bad && blockIdx.x == 0) set_status(p.status, GDN_DEV_BAD_CU_SEQLENS);
+    __syncwarp();
   }
   tc_fence_before();
   __syncthreads();
@@ -724,9 +740,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         if constexpr (kPrefix) {
           return PrefixItems(p, parts, 2 * nt);
         } else {
-          PromptItems x{bounds, p.N, 2 * nt, p.Hk, 0, 0};
-          x.init();
-          return x;
+          return PromptItems(bounds, pairs, p.N, 2 * nt, p.Hk);
         }
       }();
       const int grid = (int)gridDim.x, b = (int)blockIdx.x;
