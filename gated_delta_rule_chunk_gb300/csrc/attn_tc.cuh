@@ -38,7 +38,7 @@ namespace gdn {
 constexpr int kAttnThreads = 512;
 constexpr int kRows = 128;           // rows of a tile
 constexpr int kKeys = 128;           // keys of a tile
-constexpr int kAttnSeqs = 2048;      // sequences of one launch
+constexpr int kAttnSeqs = 1024;      // sequences of one launch
 constexpr uint32_t kPolls = 1u << 22;
 constexpr float kGrow = 8.0f;
 
@@ -71,7 +71,9 @@ struct AttnSmem {
   static constexpr int kStages = D == 128 ? 4 : 8;
   static constexpr int kQ = 0, kRing = 2 * kTile;
   static constexpr int kBounds = kRing + kStages * kTile;      // sanitized cu_seqlens, pairs
-  static constexpr int kBars = kBounds + 8 * (kAttnSeqs + 4);
+  static constexpr int kOutRow = 80;                           // 64 bytes of a row, padded
+  static constexpr int kOut = kBounds + 8 * (kAttnSeqs + 4);   // 32 rows a row warp
+  static constexpr int kBars = kOut + 8 * 32 * kOutRow;
   static constexpr int kBytes = kBars + 512 + 1024;            // + alignment of the tiles
 };
 
@@ -468,42 +470,70 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       wait(&B.o_full[X], tiles);
       ++tiles;
       tc_fence_after();
-      size_t at = (size_t)(it.base + tok) * p.H + it.hk * p.G + rh;
-      size_t split = 0;
+      int64_t at = (int64_t)(it.base + tok) * p.H + it.hk * p.G + rh;
+      int64_t split = 0;
       if constexpr (kPrefix) {
-        split = (size_t)(((int64_t)it.kv0 * parts.splits + parts.tiles - 1) / parts.tiles);
+        split = ((int64_t)it.kv0 * parts.splits + parts.tiles - 1) / parts.tiles;
         at += split * p.T * p.H;
       }
       const bool poison = *reinterpret_cast<volatile int*>(&B.poison[k & 3]) == (int)k + 1;
-      // prefix: as they are, for the merge with the other splits; NaN stays NaN
-      const float r = kPrefix ? 1.f : l == 0.f ? 0.f : 1.f / l;
-      void* out = kPrefix ? parts.o : p.out;
+      float o[D];
 #pragma unroll
-      for (int q = 0; q < D; q += 32) {
-        float o[32];
-        tmem_ld32(tO + q, o);
-        tmem_ld_wait();
-        if (real && !poison) {
-          if (!kPrefix && p.out_bf16) {
-            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(out) + at * D + q);
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              dst[i] = make_uint4(pack_bf16(o[8 * i] * r, o[8 * i + 1] * r),
-                                  pack_bf16(o[8 * i + 2] * r, o[8 * i + 3] * r),
-                                  pack_bf16(o[8 * i + 4] * r, o[8 * i + 5] * r),
-                                  pack_bf16(o[8 * i + 6] * r, o[8 * i + 7] * r));
-          } else {
-            float4* dst = reinterpret_cast<float4*>(static_cast<float*>(out) + at * D + q);
-#pragma unroll
-            for (int i = 0; i < 8; ++i)
-              dst[i] = make_float4(o[4 * i] * r, o[4 * i + 1] * r, o[4 * i + 2] * r,
-                                   o[4 * i + 3] * r);
-          }
-        }
-      }
+      for (int q = 0; q < D; q += 32) tmem_ld32(tO + q, *reinterpret_cast<float(*)[32]>(&o[q]));
+      tmem_ld_wait();
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.o_empty[X]);
+      // prefix: as they are, for the merge with the other splits; NaN stays NaN
+      const float r = kPrefix ? 1.f : l == 0.f ? 0.f : 1.f / l;
+      // A thread holds a whole row; stored from here, every 16 bytes of a warp's store would
+      // fall into another line (4,000 cycles a pair of tiles). So 64 bytes a row at a time go
+      // through shared memory, and four lanes write one row's.
+      char* stage = smem + S::kOut + warp * (32 * S::kOutRow);
+      int64_t to[4];  // the rows that this lane writes, -1: none
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        to[i] = __shfl_sync(0xffffffffu, real && !poison ? at : -1, i * 8 + (lane >> 2));
+      char* out = static_cast<char*>(kPrefix ? static_cast<void*>(parts.o) : p.out);
+      auto flush = [&](const uint4 (&y)[4], int byte, int row_bytes) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          *reinterpret_cast<uint4*>(stage + lane * S::kOutRow + i * 16) = y[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint4 z = *reinterpret_cast<const uint4*>(stage + (i * 8 + (lane >> 2)) * S::kOutRow +
+                                                          (lane & 3) * 16);
+          if (to[i] >= 0)
+            *reinterpret_cast<uint4*>(out + to[i] * row_bytes + byte + (lane & 3) * 16) = z;
+        }
+        __syncwarp();
+      };
+      if (!kPrefix && p.out_bf16) {
+#pragma unroll
+        for (int q = 0; q < D; q += 32) {
+          uint4 y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* f = o + q + 8 * i;
+            y[i] = make_uint4(pack_bf16(f[0] * r, f[1] * r), pack_bf16(f[2] * r, f[3] * r),
+                              pack_bf16(f[4] * r, f[5] * r), pack_bf16(f[6] * r, f[7] * r));
+          }
+          flush(y, q * 2, D * 2);
+        }
+      } else {
+#pragma unroll
+        for (int q = 0; q < D; q += 16) {
+          uint4 y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float* f = o + q + 4 * i;
+            y[i] = make_uint4(__float_as_uint(f[0] * r), __float_as_uint(f[1] * r),
+                              __float_as_uint(f[2] * r), __float_as_uint(f[3] * r));
+          }
+          flush(y, q * 4, D * 4);
+        }
+      }
       if constexpr (kPrefix) {
         if (real && !poison) parts.ml[at] = make_float2(ref * c, l);
       } else {
@@ -513,7 +543,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         for (int i = 0; i < 32; ++i) {
           const int rr = (warp & 3) * 32 + i, ti = rr / p.G, t = it.tok + X * nt + ti;
           if (ti >= nt || t >= it.len) continue;
-          const size_t to = (size_t)(it.base + t) * p.H + it.hk * p.G + (rr - ti * p.G);
+          const size_t tr = (size_t)(it.base + t) * p.H + it.hk * p.G + (rr - ti * p.G);
           float o[D / 32], lse;
           if constexpr (kPrefix) {
             const int k0 = it.kv0 * kKeys;
@@ -523,18 +553,18 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
               if (pg < 0 || pg >= p.n_pages) return nullptr;
               return base + ((((size_t)pg * p.Hk + it.hk) << p.page_shift) + (key & (p.page - 1))) * D;
             };
-            attn_row<D>(p.q + to * D, k1 - k0, p.scale, [&](int j) { return at_key(p.k, j); },
+            attn_row<D>(p.q + tr * D, k1 - k0, p.scale, [&](int j) { return at_key(p.k, j); },
                         [&](int j) { return at_key(p.v, j); }, o, lse);
-            const size_t row = split * p.T * p.H + to;
+            const size_t row = split * p.T * p.H + tr;
             store_row<D>(parts.o, false, row, o);
             if (lane == 0)
               parts.ml[row] = make_float2(lse * 1.44269504088896340736f, lse == -INFINITY ? 0.f : 1.f);
           } else {
             const size_t kv = ((size_t)it.base * p.Hk + it.hk) * D, step = (size_t)p.Hk * D;
-            attn_row<D>(p.q + to * D, t + 1, p.scale,
+            attn_row<D>(p.q + tr * D, t + 1, p.scale,
                         [&](int j) { return p.k + kv + j * step; },
                         [&](int j) { return p.v + kv + j * step; }, o, lse);
-            store_row<D>(p.out, p.out_bf16, to, o);
+            store_row<D>(p.out, p.out_bf16, tr, o);
           }
         }
       }
