@@ -173,6 +173,9 @@ __device__ __forceinline__ void tma_load_4d(void* dst, const void* tmap, int x, 
       "l"(reinterpret_cast<uint64_t>(tmap)), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_addr(bar))
       : "memory");
 }
+__device__ __forceinline__ void prefetch_tmap(const CUtensorMap* tm) {
+  asm volatile("prefetch.tensormap [%0];\n" ::"l"(reinterpret_cast<uint64_t>(tm)) : "memory");
+}
 template <int N>
 __device__ __forceinline__ void regs_inc() {
   asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;\n" ::"n"(N));
@@ -319,8 +322,6 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   static_assert(sizeof(AttnBars<kStages>) <= 512, "barrier area");
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int nt = kRows / p.G;  // tokens of a row tile
-  if (kPrefix) pdl_release();  // the decode kernel needs nothing from here
-
   if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&B.kv_full[i], 1);
@@ -344,7 +345,11 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   if (warp == 8) {
     tmem_alloc(&B.tmem, 512);
     tmem_relinquish();
+    if (lane < 3) prefetch_tmap(lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v);
   }
+  // All of the above needs nothing of the launch before this one in the stream.
+  pdl_wait();
+  if (kPrefix) pdl_release();  // the decode kernel needs nothing from here
   if (!kPrefix && warp == 10) {  // cu_seqlens, each entry clamped and raised to the largest before it
     const int span = 2 * nt;
     int carry = 0;
@@ -477,63 +482,53 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         at += split * p.T * p.H;
       }
       const bool poison = *reinterpret_cast<volatile int*>(&B.poison[k & 3]) == (int)k + 1;
-      float o[D];
-#pragma unroll
-      for (int q = 0; q < D; q += 32) tmem_ld32(tO + q, *reinterpret_cast<float(*)[32]>(&o[q]));
-      tmem_ld_wait();
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.o_empty[X]);
       // prefix: as they are, for the merge with the other splits; NaN stays NaN
       const float r = kPrefix ? 1.f : l == 0.f ? 0.f : 1.f / l;
       // A thread holds a whole row; stored from here, every 16 bytes of a warp's store would
       // fall into another line (4,000 cycles a pair of tiles). So 64 bytes a row at a time go
-      // through shared memory, and four lanes write one row's.
+      // through shared memory, and four lanes write one row's. A rolled loop: this code is
+      // fetched anew for every item.
       char* stage = smem + S::kOut + warp * (32 * S::kOutRow);
       int64_t to[4];  // the rows that this lane writes, -1: none
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         to[i] = __shfl_sync(0xffffffffu, real && !poison ? at : -1, i * 8 + (lane >> 2));
-      char* out = static_cast<char*>(kPrefix ? static_cast<void*>(parts.o) : p.out);
-      auto flush = [&](const uint4 (&y)[4], int byte, int row_bytes) {
+      const bool wide = kPrefix || !p.out_bf16;  // fp32 rows
+      char* out = static_cast<char*>(kPrefix ? static_cast<void*>(parts.o) : p.out) + (lane & 3) * 16;
+#pragma unroll 1
+      for (int q = 0; q < D; q += wide ? 16 : 32) {
+        float o[32];
+        tmem_ld16(tO + q, *reinterpret_cast<float(*)[16]>(&o[0]));
+        if (!wide) tmem_ld16(tO + q + 16, *reinterpret_cast<float(*)[16]>(&o[16]));
+        tmem_ld_wait();
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-          *reinterpret_cast<uint4*>(stage + lane * S::kOutRow + i * 16) = y[i];
+        for (int i = 0; i < 4; ++i) {
+          uint4 y;
+          if (wide)
+            y = make_uint4(__float_as_uint(o[4 * i] * r), __float_as_uint(o[4 * i + 1] * r),
+                           __float_as_uint(o[4 * i + 2] * r), __float_as_uint(o[4 * i + 3] * r));
+          else
+            y = make_uint4(pack_bf16(o[8 * i] * r, o[8 * i + 1] * r),
+                           pack_bf16(o[8 * i + 2] * r, o[8 * i + 3] * r),
+                           pack_bf16(o[8 * i + 4] * r, o[8 * i + 5] * r),
+                           pack_bf16(o[8 * i + 6] * r, o[8 * i + 7] * r));
+          *reinterpret_cast<uint4*>(stage + lane * S::kOutRow + i * 16) = y;
+        }
         __syncwarp();
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const uint4 z = *reinterpret_cast<const uint4*>(stage + (i * 8 + (lane >> 2)) * S::kOutRow +
                                                           (lane & 3) * 16);
-          if (to[i] >= 0)
-            *reinterpret_cast<uint4*>(out + to[i] * row_bytes + byte + (lane & 3) * 16) = z;
+          if (to[i] >= 0) {
+            const int64_t byte = wide ? (to[i] * D + q) * 4 : (to[i] * D + q) * 2;
+            *reinterpret_cast<uint4*>(out + byte) = z;
+          }
         }
         __syncwarp();
-      };
-      if (!kPrefix && p.out_bf16) {
-#pragma unroll
-        for (int q = 0; q < D; q += 32) {
-          uint4 y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float* f = o + q + 8 * i;
-            y[i] = make_uint4(pack_bf16(f[0] * r, f[1] * r), pack_bf16(f[2] * r, f[3] * r),
-                              pack_bf16(f[4] * r, f[5] * r), pack_bf16(f[6] * r, f[7] * r));
-          }
-          flush(y, q * 2, D * 2);
-        }
-      } else {
-#pragma unroll
-        for (int q = 0; q < D; q += 16) {
-          uint4 y[4];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float* f = o + q + 4 * i;
-            y[i] = make_uint4(__float_as_uint(f[0] * r), __float_as_uint(f[1] * r),
-                              __float_as_uint(f[2] * r), __float_as_uint(f[3] * r));
-          }
-          flush(y, q * 4, D * 4);
-        }
       }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.o_empty[X]);
       if constexpr (kPrefix) {
         if (real && !poison) parts.ml[at] = make_float2(ref * c, l);
       } else {
@@ -850,8 +845,8 @@ bool launch_attn_tc(const AttnParams& p, const PrefixParts& parts, const CUtenso
   constexpr int smem = AttnSmem<D, kPrefix>::kBytes;
   ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   const int64_t sms = num_sms();
-  kernel<<<(unsigned)(items < sms ? items : sms), kAttnThreads, smem, s>>>(p, parts, tm_q, tm_k, tm_v);
-  return true;
+  return launch_pdl(kernel, dim3((unsigned)(items < sms ? items : sms)), dim3(kAttnThreads), smem, s,
+                    p, parts, tm_q, tm_k, tm_v) == cudaSuccess;
 }
 
 }  // namespace gdn
