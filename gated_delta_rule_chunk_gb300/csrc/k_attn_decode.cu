@@ -77,9 +77,8 @@ struct DecodeSmem {
   static constexpr int kRow = D * 2;                 // bytes of a key
   static constexpr int kStage = 2 * kBlk * kRow;     // a K and a V block
   static constexpr int kStages = D == 128 ? 3 : 6;   // 96 KB in flight per CTA
-  static constexpr int kLd = 36;                     // merge rows: 32 columns, padded
   static constexpr int kMerge = kWarps * kStages * kStage;
-  static constexpr int kMl = kMerge + kWarps * 16 * kLd * 4;
+  static constexpr int kMl = kMerge + 2 * kWarps * 16 * 32 * 4;
   static constexpr int kBytes = kMl + kWarps * 16 * 8;
 };
 
@@ -95,54 +94,53 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
   using S = DecodeSmem<D>;
   constexpr int kSt = S::kStages, WK = kWarps / WM, E = D / 16;
   extern __shared__ __align__(128) char smem[];
-  __shared__ int sh_sum[kWarps], sh_cur[4];
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int kg = warp / WM, mt = warp % WM;  // key group, row tile
   const int R = p.nq * p.G;
+  // With a prefix kernel before this one in the stream nothing of it is needed here, and it
+  // has waited for what came before; this kernel then only ends after it.
+  if (p.shared == 0) pdl_wait();
   pdl_release();
 
-  // ---- the CTA's part of the unit list
-  int sum = 0;
-  for (int n = tid; n < p.N; n += kWarps * 32) {
-    sum += chunks_of(p, n);
+  // ---- the CTA's part of the unit list; each warp looks it up for itself
+  int U = 0;
+  for (int n = lane; n < p.N; n += 32) {
+    U += chunks_of(p, n);
     if (blockIdx.x == 0 && (p.kv_lens[n] < 0 || p.kv_lens[n] > (p.max_pages << p.page_shift)))
       set_status(p.status, GDN_DEV_BAD_LENGTH);
   }
-  sum = __reduce_add_sync(0xffffffffu, sum);
-  if (lane == 0) sh_sum[warp] = sum;
-  __syncthreads();
-  const int U = (sh_sum[0] + sh_sum[1] + sh_sum[2] + sh_sum[3]) * p.Hk;
+  U = __reduce_add_sync(0xffffffffu, U) * p.Hk;
   const int grid = min((int)gridDim.x, U), b = (int)blockIdx.x;
   const int u0 = b < grid ? unit_of(b, U, grid) : U, u1 = b < grid ? unit_of(b + 1, U, grid) : U;
-  if (warp == 0) {
-    int before = 0;
-    for (int n0 = 0; n0 < p.N; n0 += 32) {
-      const int n = n0 + lane;
-      const int c = n < p.N ? chunks_of(p, n) : 0;
-      int inc = c;
+  Cursor cur{};
+  const bool scribe = b == 0 && warp == 0;  // writes the sequences' first units
+  int before = 0;
+  for (int n0 = 0; n0 < p.N && (scribe || before * p.Hk <= u0); n0 += 32) {
+    const int n = n0 + lane;
+    const int c = n < p.N ? chunks_of(p, n) : 0;
+    int inc = c;
 #pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      const int at = (before + inc - c) * p.Hk;
-      if (b == 0 && n < p.N) w.first[n] = at;
-      if (c > 0 && u0 >= at && u0 < at + c * p.Hk) {
-        sh_cur[0] = n;
-        sh_cur[1] = (u0 - at) / c;
-        sh_cur[2] = (u0 - at) % c;
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-      if (b != 0 && u0 < before * p.Hk) break;
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
     }
-    if (b == 0 && lane == 0) w.first[p.N] = U;
+    const int at = (before + inc - c) * p.Hk;
+    if (scribe && n < p.N) w.first[n] = at;
+    const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && u0 >= at && u0 < at + c * p.Hk);
+    if (hit) {
+      const int src = __ffs(hit) - 1;
+      const int off = u0 - __shfl_sync(0xffffffffu, at, src), ch = __shfl_sync(0xffffffffu, c, src);
+      cur.n = n0 + src;
+      cur.hk = off / ch;
+      cur.chunk = off % ch;
+    }
+    before += __shfl_sync(0xffffffffu, inc, 31);
   }
-  __syncthreads();
+  if (scribe && lane == 0) w.first[p.N] = U;
   if (u0 >= u1) {
     pdl_wait();
     return;
   }
-  Cursor cur{sh_cur[0], sh_cur[1], sh_cur[2], 0, 0};
   cur.load(p);
   Cursor ahead = cur;  // what is loaded next
 
@@ -195,30 +193,33 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
   int lim_off[2];  // keys past len that the row does not see: lim = len - lim_off
 #pragma unroll
   for (int x = 0; x < 2; ++x) lim_off[x] = p.nq - 1 - min((row0 + 8 * x) / p.G, p.nq - 1);
-  bool fresh = true;
+  // This warp's rows of the queries of the pair at `cur`.
+  auto load_q = [&] {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int r = row0 + 8 * x;
+      const __nv_bfloat16* q =
+          p.q + ((size_t)(cur.n * p.nq + r / p.G) * p.H + cur.hk * p.G + r % p.G) * D;
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        qf[e][x] = r < R ? *reinterpret_cast<const uint32_t*>(q + e * 16 + cq) : 0u;
+        qf[e][x + 2] = r < R ? *reinterpret_cast<const uint32_t*>(q + e * 16 + 8 + cq) : 0u;
+      }
+    }
+  };
+  auto reset = [&] {
+    ref[0] = ref[1] = -INFINITY;
+    l[0] = l[1] = 0.f;
+#pragma unroll
+    for (int e = 0; e < 2 * E; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
+  };
+  load_q();
+  reset();
   int seg_chunk = cur.chunk;  // first chunk of this pair in this CTA
   bool seg_first = true;      // the pair's part begins at the CTA's first unit
   int st = 0;
 
   for (int u = u0; u < u1; ++u) {
-    if (fresh) {
-      fresh = false;
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int r = row0 + 8 * x;
-        const __nv_bfloat16* q =
-            p.q + ((size_t)(cur.n * p.nq + r / p.G) * p.H + cur.hk * p.G + r % p.G) * D;
-#pragma unroll
-        for (int e = 0; e < E; ++e) {
-          qf[e][x] = r < R ? *reinterpret_cast<const uint32_t*>(q + e * 16 + cq) : 0u;
-          qf[e][x + 2] = r < R ? *reinterpret_cast<const uint32_t*>(q + e * 16 + 8 + cq) : 0u;
-        }
-        ref[x] = -INFINITY;
-        l[x] = 0.f;
-      }
-#pragma unroll
-      for (int e = 0; e < 2 * E; ++e) o[e][0] = o[e][1] = o[e][2] = o[e][3] = 0.f;
-    }
     load_next((st + kSt - 1) % kSt);
     cp_async_wait<kSt - 1>();
     if constexpr (WM == 1) __syncwarp();
@@ -323,6 +324,7 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
     if (u + 1 < u1 && cur.n == was.n && cur.hk == was.hk) continue;
 
     // ---- the end of a pair's part: merge the key groups, finish or hand over
+    if (u + 1 < u1) load_q();  // the next pair's queries arrive meanwhile
     const bool whole = seg_chunk == 0 && was.chunk == was.chunks - 1;
     const int place = 2 * blockIdx.x + (seg_first ? 0 : 1);
     float2* ml = reinterpret_cast<float2*>(smem + S::kMl);  // [WK][16 WM]
@@ -341,15 +343,18 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
       for (int k = 0; k < WK; ++k) m = fmaxf(m, ml[k * 16 * WM + row0 + 8 * x].x);
       f[x] = m == -INFINITY ? 0.f : ex2(ref[x] - m);
     }
-    float* buf = reinterpret_cast<float*>(smem + S::kMerge);  // [WK][16 WM][kLd]
+    // 32 columns at a time through two buffers [WK][16 WM][32], one barrier a round: a buffer
+    // is written again two rounds later, past a barrier that its readers have reached. 8-column
+    // pieces are swapped by row, so that a warp's eight rows do not share banks.
 #pragma unroll
     for (int q = 0; q < D / 32; ++q) {
+      float* buf = reinterpret_cast<float*>(smem + S::kMerge) + (q & 1) * (kWarps * 16 * 32);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const float* y = o[4 * q + e];
-        float* dst = buf + (kg * 16 * WM + row0) * S::kLd + e * 8 + cq;
+        float* dst = buf + (kg * 16 * WM + row0) * 32 + ((e ^ (row0 & 3)) * 8) + cq;
         *reinterpret_cast<float2*>(dst) = make_float2(y[0] * f[0], y[1] * f[0]);
-        *reinterpret_cast<float2*>(dst + 8 * S::kLd) = make_float2(y[2] * f[1], y[3] * f[1]);
+        *reinterpret_cast<float2*>(dst + 8 * 32) = make_float2(y[2] * f[1], y[3] * f[1]);
       }
       __syncthreads();
 #pragma unroll
@@ -359,7 +364,8 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
         float m = -INFINITY, d = 0.f;
 #pragma unroll
         for (int k = 0; k < WK; ++k) {
-          const float4 y = *reinterpret_cast<const float4*>(buf + (k * 16 * WM + r) * S::kLd + col);
+          const float4 y = *reinterpret_cast<const float4*>(buf + (k * 16 * WM + r) * 32 +
+                                                              (col ^ ((r & 3) * 8)));
           acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
           m = fmaxf(m, ml[k * 16 * WM + r].x);
         }
@@ -386,9 +392,9 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
           if (q == 0 && col == 0) (whole ? w.own_ml : w.part_ml)[at] = make_float2(m, d);
         }
       }
-      __syncthreads();
     }
-    fresh = true;
+    __syncthreads();
+    reset();
     seg_chunk = cur.chunk;
     seg_first = false;
   }
@@ -417,31 +423,64 @@ __global__ void __launch_bounds__(128) combine_kernel(const AttnParams p, const 
   }
   const int splits = p.shared > 0 ? w.prefix.splits : 0;
   if (parts == 1 && splits == 0) return;  // finished by its CTA
-  float m = -INFINITY, l = 0.f, o[E] = {};
-  for (int i = warp; i < splits + parts; i += 4) {
-    const float* po;
-    float2 ml;
+  // Part i's row: the prefix's splits, then the pair's parts.
+  auto row_of = [&](int i, const float2*& ml) -> const float* {
+    size_t row;
     if (i < splits) {
-      const size_t row = (size_t)i * p.T * p.H + at;
-      po = w.prefix.o + row * D;
-      ml = w.prefix.ml[row];
-    } else if (parts == 1) {
-      const size_t row = (size_t)(n * p.Hk + hk) * R + r;
-      po = w.own + row * D;
-      ml = w.own_ml[row];
-    } else {
-      const int cta = c0 + i - splits;
-      const size_t row = (size_t)(2 * cta + (unit_of(cta, U, grid) < ub ? 1 : 0)) * R + r;
-      po = w.part + row * D;
-      ml = w.part_ml[row];
+      row = (size_t)i * p.T * p.H + at;
+      ml = w.prefix.ml + row;
+      return w.prefix.o + row * D;
     }
-    if (ml.y == 0.f) continue;  // it saw no key of this part (NaN is kept)
-    const float mn = fmaxf(m, ml.x);
-    const float f = m == mn ? 1.f : ex2(m - mn), fi = ml.x == mn ? 1.f : ex2(ml.x - mn);
-    m = mn;
-    l = l * f + ml.y * fi;
+    if (parts == 1) {
+      row = (size_t)(n * p.Hk + hk) * R + r;
+      ml = w.own_ml + row;
+      return w.own + row * D;
+    }
+    const int cta = c0 + i - splits;
+    row = (size_t)(2 * cta + (unit_of(cta, U, grid) < ub ? 1 : 0)) * R + r;
+    ml = w.part_ml + row;
+    return w.part + row * D;
+  };
+  // A warp takes every fourth part, 32 at a time: a lane each for the references and
+  // denominators, so that the rows' loads wait for nothing and run side by side.
+  float m = -INFINITY, l = 0.f, o[E] = {};
+  for (int i0 = warp; i0 < splits + parts; i0 += 128) {
+    const int mine = i0 + 4 * lane;
+    float2 ml = make_float2(-INFINITY, 0.f);
+    const float* po = nullptr;
+    if (mine < splits + parts) {
+      const float2* q;
+      po = row_of(mine, q);
+      ml = *q;
+    }
+    const bool seen = ml.y != 0.f;  // the row saw a key of this part (NaN is kept)
+    float mn = seen ? ml.x : -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = o[e] * f + po[lane * E + e] * fi;
+    for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
+    mn = fmaxf(mn, m);
+    const float f = m == mn ? 1.f : ex2(m - mn), fi = !seen ? 0.f : ml.x == mn ? 1.f : ex2(ml.x - mn);
+    m = mn;
+    float li = seen ? ml.y * fi : 0.f;
+#pragma unroll
+    for (int x = 16; x > 0; x >>= 1) li += __shfl_xor_sync(0xffffffffu, li, x);
+    l = l * f + li;
+#pragma unroll
+    for (int e = 0; e < E; ++e) o[e] *= f;
+    const int cnt = min(32, (splits + parts - i0 + 3) / 4);
+#pragma unroll 4
+    for (int i = 0; i < cnt; ++i) {
+      const float wi = __shfl_sync(0xffffffffu, fi, i);
+      const float* y = reinterpret_cast<const float*>(
+          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), i));
+      const bool add = __shfl_sync(0xffffffffu, seen, i);
+      float v[E];
+      if constexpr (E == 4)
+        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y + lane * E);
+      else
+        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y + lane * E);
+#pragma unroll
+      for (int e = 0; e < E; ++e) o[e] = add ? o[e] + v[e] * wi : o[e];
+    }
   }
   if (lane == 0) sh_ml[warp] = make_float2(m, l);
 #pragma unroll
@@ -535,15 +574,8 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   const auto kernel = R <= 16 ? decode_kernel<D, 1> : R <= 32 ? decode_kernel<D, 2> : decode_kernel<D, 4>;
   constexpr int smem = DecodeSmem<D>::kBytes;
   ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
-  // The prefix kernel and this one need nothing of each other, so this one may start before
-  // the other ends (and ends after it). Without a prefix the launch before it in the stream is
-  // a stranger, whose results it may need.
-  if (p.shared > 0) {
-    if (launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w) != cudaSuccess) return false;
-  } else {
-    kernel<<<w.grid, kWarps * 32, smem, s>>>(p, w);
-  }
-  return launch_pdl(combine_kernel<D>, dim3((unsigned)((size_t)p.T * p.H)), dim3(128), 0, s, p, w) ==
+  return launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w) == cudaSuccess &&
+         launch_pdl(combine_kernel<D>, dim3((unsigned)((size_t)p.T * p.H)), dim3(128), 0, s, p, w) ==
          cudaSuccess;
 }
 
