@@ -490,6 +490,7 @@ def gdn_workspace_regions(desc: GdnDesc):
 
 # ---------------------------------------------------------------- softmax attention
 _DTYPE_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
+_decode_workspace: dict = {}  # gdn_attn_workspace_size by (N, n_q, H, Hk, D, device)
 
 
 def make_attn_desc(T: int, N: int, H: int, Hk: int, D: int, in_dtype: torch.dtype = torch.bfloat16,
@@ -514,13 +515,21 @@ def _addr(t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype] = N
     """Device address of an optional contiguous CUDA tensor of this dtype and shape."""
     if t is None:
         return None
+    if (t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype)
+            and (shape is None or t.shape == shape)):
+        return t.data_ptr()
     if not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous CUDA tensor")
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and t.shape != shape:
-        raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-    return t.data_ptr()
+    raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
+
+
+def _stream_of(stream, t: torch.Tensor) -> int:
+    """The stream's handle; without one, that of the current stream of t's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(t.get_device())
 
 
 def _num_seqs(cu_seqlens: Optional[torch.Tensor]) -> int:
@@ -582,7 +591,7 @@ def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
                        GDN_ATTN_ROPE_INTERLEAVED if interleaved else 0, norm_eps,
                        _addr(status, "status", torch.int32), None, 0)
     cache_shape = (n_pages, Hk, page, D)
-    rc = load_library().gdn_attn_front(
+    rc = (_lib or load_library()).gdn_attn_front(
         ctypes.byref(desc), _addr(x, "x", None, (T, (H + 2 * Hk) * D)),
         _addr(q_weight, "q_weight", torch.float32, (D,)),
         _addr(k_weight, "k_weight", torch.float32, (D,)), _addr(rope, "rope", torch.float32),
@@ -590,7 +599,7 @@ def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
         _addr(page_table, "page_table", torch.int32, (N, max_pages)),
         _addr(q, "q", out_dtype, (T, H, D)), _addr(k, "k", out_dtype, (T, Hk, D)),
         _addr(v, "v", out_dtype, (T, Hk, D)), _addr(k_cache, "k_cache", out_dtype, cache_shape),
-        _addr(v_cache, "v_cache", out_dtype, cache_shape), _stream_handle(stream))
+        _addr(v_cache, "v_cache", out_dtype, cache_shape), _stream_of(stream, x))
     if rc != 0:
         raise GdnError(rc, "gdn_attn_front")
     return q, k, v
@@ -613,11 +622,11 @@ def gdn_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
         lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
     desc = GdnAttnDesc(T, N, H, Hk, D, 0, 0, 0, 0, 0, _dtype_code(q.dtype), _dtype_code(out.dtype),
                        0, 0.0, _addr(status, "status", torch.int32), None, 0)
-    rc = load_library().gdn_attn_prefill(
+    rc = (_lib or load_library()).gdn_attn_prefill(
         ctypes.byref(desc), _addr(q, "q"), _addr(k, "k", q.dtype, (T, Hk, D)),
         _addr(v, "v", q.dtype, (T, Hk, D)), _addr(cu_seqlens, "cu_seqlens", torch.int32),
         0.0 if scale is None else scale, _addr(out, "out", out_dtype, (T, H, D)),
-        _addr(lse, "lse", torch.float32, (T, H)), _stream_handle(stream))
+        _addr(lse, "lse", torch.float32, (T, H)), _stream_of(stream, q))
     if rc != 0:
         raise GdnError(rc, "gdn_attn_prefill")
     return (out, lse) if return_lse else out
@@ -645,11 +654,15 @@ def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     desc = GdnAttnDesc(N * nq, N, H, Hk, D, page, n_pages, page_table.shape[1], 0, 0,
                        _dtype_code(q.dtype), _dtype_code(out.dtype), 0, 0.0,
                        _addr(status, "status", torch.int32), None, 0)
-    lib = load_library()
+    lib = _lib or load_library()
     if workspace is None:
-        n = lib.gdn_attn_workspace_size(ctypes.byref(desc))
-        if n == 0:
-            raise GdnError(lib.gdn_attn_check_desc(ctypes.byref(desc)), "gdn_attn_decode")
+        key = (N, nq, H, Hk, D, q.device.index)
+        n = _decode_workspace.get(key)
+        if n is None:
+            n = lib.gdn_attn_workspace_size(ctypes.byref(desc))
+            if n == 0:
+                raise GdnError(lib.gdn_attn_check_desc(ctypes.byref(desc)), "gdn_attn_decode")
+            _decode_workspace[key] = n
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
     desc.workspace = _addr(workspace, "workspace")
     desc.workspace_bytes = workspace.numel() * workspace.element_size()
@@ -660,7 +673,7 @@ def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
         _addr(page_table, "page_table", torch.int32, (N, page_table.shape[1])),
         _addr(kv_lens, "kv_lens", torch.int32, (N,)), shared_len, 0.0 if scale is None else scale,
         _addr(out, "out", out_dtype, q.shape), _addr(lse, "lse", torch.float32, q.shape[:-1]),
-        _stream_handle(stream))
+        _stream_of(stream, q))
     if rc != 0:
         raise GdnError(rc, "gdn_attn_decode")
     return (out, lse) if return_lse else out
