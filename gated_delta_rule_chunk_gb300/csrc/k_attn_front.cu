@@ -6,13 +6,14 @@
 // position; fp32 throughout and one rounding at the store (a rounding between norm and
 // rotation would double the error of a bf16 result). v is copied.
 //
-// D / 8 lanes hold one head row, 8 elements each (16-byte loads and stores), so the norm's
-// sum is a few shuffles; a pair's other half is 8-element aligned (rot % 16 == 0), hence one
-// shuffle away (half layout) or in the same lane (interleaved). A lane group takes R heads
-// of one token, all loaded before anything waits, with one lookup of the token's sequence,
-// position and page and one load of its cos/sin row. Bound: HBM for long prompts; latency
-// (cu_seqlens -> kv_lens -> page table and rotary row -> store, x loaded meanwhile) for a
-// decode step.
+// D / 8 lanes hold one head row, each two runs of 4 elements, so that the norm's sum is a few
+// shuffles and both halves of every rotated pair are in one lane: in the half layout the runs
+// of a rotated lane l are [4l, 4l + 4) and [rot/2 + 4l, ..), elsewhere the lane's 8 elements
+// (rot % 16 == 0). In both layouts the lane then needs the frequencies [4l, 4l + 4). A lane
+// group takes R heads of one token, all loaded before anything waits, with one lookup of the
+// token's sequence, position and page and one load of its cos/sin. Bound: HBM for long
+// prompts; latency (cu_seqlens -> kv_lens -> page table and rotary row -> store, x loaded
+// meanwhile) for a decode step.
 #include "attn_common.cuh"
 
 namespace gdn {
@@ -22,39 +23,26 @@ namespace {
 constexpr int kThreads = 128;
 
 template <bool kBf16>
-__device__ __forceinline__ void load8(const void* x, size_t at, float (&y)[8]) {
+__device__ __forceinline__ void load4(const void* x, size_t at, float* y) {
   if constexpr (kBf16) {
-    const uint4 r = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + at);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 f = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&w[i]));
-      y[2 * i] = f.x;
-      y[2 * i + 1] = f.y;
-    }
+    const uint2 r = *reinterpret_cast<const uint2*>(static_cast<const __nv_bfloat16*>(x) + at);
+    const float2 a = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.x));
+    const float2 b = __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162*>(&r.y));
+    y[0] = a.x; y[1] = a.y; y[2] = b.x; y[3] = b.y;
   } else {
-    const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
-    const float4 a = f[0], b = f[1];
-    y[0] = a.x; y[1] = a.y; y[2] = a.z; y[3] = a.w;
-    y[4] = b.x; y[5] = b.y; y[6] = b.z; y[7] = b.w;
+    const float4 r = *reinterpret_cast<const float4*>(static_cast<const float*>(x) + at);
+    y[0] = r.x; y[1] = r.y; y[2] = r.z; y[3] = r.w;
   }
 }
 
 template <bool kBf16>
-__device__ __forceinline__ void store8(void* x, size_t at, const float (&y)[8]) {
+__device__ __forceinline__ void store4(void* x, size_t at, const float* y) {
   if constexpr (kBf16) {
-    uint4 r;
-    uint32_t* w = &r.x;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-      w[i] = *reinterpret_cast<const uint32_t*>(&b);
-    }
-    *reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(x) + at) = r;
+    const __nv_bfloat162 a = __floats2bfloat162_rn(y[0], y[1]), b = __floats2bfloat162_rn(y[2], y[3]);
+    *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(x) + at) =
+        make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
   } else {
-    float4* f = reinterpret_cast<float4*>(static_cast<float*>(x) + at);
-    f[0] = make_float4(y[0], y[1], y[2], y[3]);
-    f[1] = make_float4(y[4], y[5], y[6], y[7]);
+    *reinterpret_cast<float4*>(static_cast<float*>(x) + at) = make_float4(y[0], y[1], y[2], y[3]);
   }
 }
 
@@ -83,24 +71,29 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int T, int t, 
 }
 
 template <int D, bool kInBf16, bool kOutBf16, int R>
-__global__ void __launch_bounds__(kThreads) attn_front_kernel(AttnFrontParams p) {
+__global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontParams p) {
   constexpr int L = D / 8;  // lanes of a head row
-  const int heads = p.H + 2 * p.Hk, chunks = (heads + R - 1) / R;
-  const int64_t item = ((int64_t)blockIdx.x * kThreads + threadIdx.x) / L;
+  const uint32_t heads = p.H + 2 * p.Hk, chunks = (heads + R - 1) / R;
+  const uint32_t item = (blockIdx.x * kThreads + threadIdx.x) / L;  // < 2^31: T * heads is
   const int lane = threadIdx.x % L;
-  const int64_t t64 = item / chunks;
-  const int h0 = (int)(item % chunks) * R;
-  bool live = t64 < p.T;
-  const int t = live ? (int)t64 : 0;
+  const uint32_t ti = item / chunks, h0 = (item - ti * chunks) * R;
+  bool live = ti < (uint32_t)p.T;
+  const int t = live ? (int)ti : 0;
+  // this lane's elements: [e0, e0 + 4) and [e1, e1 + 4)
+  const int half = p.rot >> 1;
+  const bool turned = lane * 8 < p.rot, split = turned && !p.interleaved;
+  const int e0 = split ? 4 * lane : 8 * lane, e1 = split ? half + 4 * lane : 8 * lane + 4;
+  pdl_wait();
 
   float y[R][8];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    if (live && h0 + r < heads) {
-      load8<kInBf16>(p.x, ((size_t)t * heads + h0 + r) * D + lane * 8, y[r]);
-    } else {
 #pragma unroll
-      for (int i = 0; i < 8; ++i) y[r][i] = 0.f;
+    for (int i = 0; i < 8; ++i) y[r][i] = 0.f;
+    if (live && h0 + r < heads) {
+      const size_t at = ((size_t)t * heads + h0 + r) * D;
+      load4<kInBf16>(p.x, at + e0, y[r]);
+      load4<kInBf16>(p.x, at + e1, y[r] + 4);
     }
   }
 
@@ -128,71 +121,68 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(AttnFrontParams p)
     }
   }
 
-  // cos and sin of this lane's elements: 8 of each (half layout) or 4 (interleaved)
-  float c[8], s[8];
-  const bool turns = live && lane * 8 < p.rot && h0 < p.H + p.Hk;
-  const int half = p.rot >> 1, pair = half >> 3;  // lanes of one half
-  if (turns) {
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live && turned) {
     if (pos < 0 || pos >= p.max_pos) {
       set_status(p.status, GDN_DEV_BAD_LENGTH);
       pos = pos < 0 ? 0 : p.max_pos - 1;
     }
-    const float* row = p.rope + (size_t)pos * p.rot;
-    if (p.interleaved) {
-      const float4 a = *reinterpret_cast<const float4*>(row + lane * 4);
-      const float4 d = *reinterpret_cast<const float4*>(row + half + lane * 4);
-      c[0] = c[1] = a.x; c[2] = c[3] = a.y; c[4] = c[5] = a.z; c[6] = c[7] = a.w;
-      s[0] = s[1] = d.x; s[2] = s[3] = d.y; s[4] = s[5] = d.z; s[6] = s[7] = d.w;
-    } else {
-      const int f = (lane < pair ? lane : lane - pair) * 8;
-      load8<false>(row, f, c);
-      load8<false>(row, half + f, s);
-    }
+    const size_t row = (size_t)pos * p.rot + 4 * lane;
+    load4<false>(p.rope, row, c);
+    load4<false>(p.rope, row + half, s);
   }
 
+  const float* w_now = nullptr;  // the norm weights held in w
+  float w[8];
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const int h = h0 + r;
-    const bool is_q = h < p.H, is_k = !is_q && h < p.H + p.Hk;
-    const float* w = is_q ? p.qw : is_k ? p.kw : nullptr;
+    const uint32_t h = h0 + r;
+    const bool is_q = h < (uint32_t)p.H, is_v = h >= (uint32_t)(p.H + p.Hk);
+    float (&z)[8] = y[r];
     float ss = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += y[r][i] * y[r][i];
+    for (int i = 0; i < 8; ++i) ss += z[i] * z[i];
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (w) {
-      const float norm = 1.0f / sqrtf(ss * (1.0f / D) + p.eps);
-      float wv[8];
-      load8<false>(w, lane * 8, wv);
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[r][i] *= norm * wv[i];
-    }
-    float z[8];  // the other halves of this lane's pairs
-    const int src = lane < pair ? lane + pair : lane - pair;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float far = __shfl_sync(0xffffffffu, y[r][i], src & (L - 1), L);
-      z[i] = p.interleaved ? y[r][i ^ 1] : far;
-    }
-    if (turns && (is_q || is_k)) {
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const bool first = p.interleaved ? (i & 1) == 0 : lane < pair;
-        z[i] = y[r][i] * c[i] + (first ? -z[i] : z[i]) * s[i];
-      }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[r][i] = z[i];
-    }
     if (!live || h >= heads) continue;
+    if (!is_v) {
+      const float* wp = is_q ? p.qw : p.kw;
+      if (wp) {
+        if (wp != w_now) {
+          load4<false>(wp, e0, w);
+          load4<false>(wp, e1, w + 4);
+          w_now = wp;
+        }
+        const float q = ss * (1.0f / D) + p.eps;
+        float norm = rsqrtf(q);  // 2 ulp; one Newton step brings it to rounding
+        norm *= 1.5f - 0.5f * q * norm * norm;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) z[i] *= norm * w[i];
+      }
+      auto turn = [&](float& a, float& d, int i) {
+        const float a0 = a;
+        a = a0 * c[i] - d * s[i];
+        d = d * c[i] + a0 * s[i];
+      };
+      if (split) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn(z[i], z[4 + i], i);
+      } else if (turned) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) turn(z[2 * i], z[2 * i + 1], i);
+      }
+    }
+    auto put = [&](void* dst, size_t row) {
+      store4<kOutBf16>(dst, row * D + e0, z);
+      store4<kOutBf16>(dst, row * D + e1, z + 4);
+    };
     if (is_q) {
-      store8<kOutBf16>(p.q, ((size_t)t * p.H + h) * D + lane * 8, y[r]);
+      put(p.q, (size_t)t * p.H + h);
     } else {
-      const int hk = is_k ? h - p.H : h - p.H - p.Hk;
-      void* dense = is_k ? p.k : p.v;
-      if (dense) store8<kOutBf16>(dense, ((size_t)t * p.Hk + hk) * D + lane * 8, y[r]);
-      if (append)
-        store8<kOutBf16>(is_k ? p.kc : p.vc,
-                         (slot + ((size_t)hk << p.page_shift)) * D + lane * 8, y[r]);
+      const uint32_t hk = is_v ? h - p.H - p.Hk : h - p.H;
+      void* dense = is_v ? p.v : p.k;
+      if (dense) put(dense, (size_t)t * p.Hk + hk);
+      if (append) put(is_v ? p.vc : p.kc, slot + ((size_t)hk << p.page_shift));
     }
   }
 }
@@ -206,9 +196,8 @@ bool launch(const AttnFrontParams& p, cudaStream_t s) {
   const bool wide = rows >= 8 * 152 * 16;
   const int64_t items = wide ? (int64_t)p.T * ((heads + 3) / 4) : rows;
   const int64_t blocks = (items + per_block - 1) / per_block;
-  if (wide) attn_front_kernel<D, kInBf16, kOutBf16, 4><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  else attn_front_kernel<D, kInBf16, kOutBf16, 1><<<(unsigned)blocks, kThreads, 0, s>>>(p);
-  return cudaPeekAtLastError() == cudaSuccess;
+  const auto kernel = wide ? attn_front_kernel<D, kInBf16, kOutBf16, 4> : attn_front_kernel<D, kInBf16, kOutBf16, 1>;
+  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, p) == cudaSuccess;
 }
 
 template <int D>
