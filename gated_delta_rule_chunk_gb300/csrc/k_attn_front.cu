@@ -70,30 +70,43 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int T, int t, 
   return b <= t && t < e && b >= 0 && e <= T ? lo : -1;
 }
 
-template <int D, bool kInBf16, bool kOutBf16, int R>
+// 1 / sqrt(x): rsqrtf is good to 2 ulp, one Newton step brings it to rounding.
+__device__ __forceinline__ float inv_sqrt(float x) {
+  const float r = rsqrtf(x);
+  return r * (1.5f - 0.5f * x * r * r);
+}
+
+template <int D, bool kInBf16, bool kOutBf16, int R, bool kInter>
 __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontParams p) {
   constexpr int L = D / 8;  // lanes of a head row
-  const uint32_t heads = p.H + 2 * p.Hk, chunks = (heads + R - 1) / R;
-  const uint32_t item = (blockIdx.x * kThreads + threadIdx.x) / L;  // < 2^31: T * heads is
+  // A token's chunks of R heads: first the query heads', then those of the keys and values, so
+  // that a lane group's heads take one path.
+  const uint32_t heads = p.H + 2 * p.Hk, q_chunks = (p.H + R - 1) / R;
+  const uint32_t chunks = q_chunks + (2 * p.Hk + R - 1) / R;
+  const uint32_t item = (blockIdx.x * kThreads + threadIdx.x) / L;
   const int lane = threadIdx.x % L;
-  const uint32_t ti = item / chunks, h0 = (item - ti * chunks) * R;
+  const uint32_t ti = item / chunks, chunk = item - ti * chunks;
   bool live = ti < (uint32_t)p.T;
   const int t = live ? (int)ti : 0;
+  const bool is_q = chunk < q_chunks;
+  const uint32_t h0 = is_q ? chunk * R : p.H + (chunk - q_chunks) * R;
+  const int cnt = live ? min(R, (int)((is_q ? p.H : heads) - h0)) : 0;
   // this lane's elements: [e0, e0 + 4) and [e1, e1 + 4)
   const int half = p.rot >> 1;
-  const bool turned = lane * 8 < p.rot, split = turned && !p.interleaved;
+  const bool turned = lane * 8 < p.rot, split = !kInter && turned;
   const int e0 = split ? 4 * lane : 8 * lane, e1 = split ? half + 4 * lane : 8 * lane + 4;
   pdl_wait();
 
   float y[R][8];
+  const size_t src = ((size_t)t * heads + h0) * D;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
+    if (r < cnt) {
+      load4<kInBf16>(p.x, src + r * D + e0, y[r]);
+      load4<kInBf16>(p.x, src + r * D + e1, y[r] + 4);
+    } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[r][i] = 0.f;
-    if (live && h0 + r < heads) {
-      const size_t at = ((size_t)t * heads + h0 + r) * D;
-      load4<kInBf16>(p.x, at + e0, y[r]);
-      load4<kInBf16>(p.x, at + e1, y[r] + 4);
+      for (int i = 0; i < 8; ++i) y[r][i] = 0.f;
     }
   }
 
@@ -108,9 +121,60 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
   int64_t pos = 0;
   if (live) pos = p.kv_lens ? (int64_t)p.kv_lens[n] - (e - t) : t - b;
 
+  // cos and sin of this lane's pairs; 1 and 0 where nothing turns
+  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
+  if (live && turned) {
+    if (pos < 0 || pos >= p.max_pos) set_status(p.status, GDN_DEV_BAD_LENGTH);
+    const int64_t row = pos < 0 ? 0 : pos < p.max_pos ? pos : p.max_pos - 1;
+    load4<false>(p.rope, (size_t)row * p.rot + 4 * lane, c);
+    load4<false>(p.rope, (size_t)row * p.rot + half + 4 * lane, s);
+  }
+  // (all lanes: the sums cross the lanes of a group)
+  auto norm_turn = [&](float (&z)[8], const float (&w)[8], bool norm) {
+    float ss = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss += z[i] * z[i];
+#pragma unroll
+    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+    const float f = norm ? inv_sqrt(ss * (1.0f / D) + p.eps) : 1.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) z[i] *= f * w[i];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float& a = kInter ? z[2 * i] : z[i];
+      float& d = kInter ? z[2 * i + 1] : z[4 + i];
+      const float a0 = a;
+      a = a0 * c[i] - d * s[i];
+      d = d * c[i] + a0 * s[i];
+    }
+  };
+  auto load_w = [&](const float* from, float (&w)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) w[i] = 1.f;
+    if (from) {
+      load4<false>(from, e0, w);
+      load4<false>(from, e1, w + 4);
+    }
+  };
+  auto put = [&](void* dst, size_t at, const float (&z)[8]) {
+    store4<kOutBf16>(dst, at + e0, z);
+    store4<kOutBf16>(dst, at + e1, z + 4);
+  };
+  float w[8];
+  load_w(is_q ? p.qw : p.kw, w);
+  if (__all_sync(0xffffffffu, is_q)) {
+    const size_t dst = ((size_t)t * p.H + h0) * D;
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      norm_turn(y[r], w, p.qw != nullptr);
+      if (live && r < cnt) put(p.q, dst + r * D, y[r]);
+    }
+    return;
+  }
+  // Keys and values (and, in a warp that holds both kinds, queries).
   size_t slot = 0;  // row of key head 0 in the cache; key head h is at slot + h * page
   bool append = false;
-  if (live && p.kc) {
+  if (live && !is_q && p.kc) {
     if (pos < 0 || (pos >> p.page_shift) >= p.max_pages) {
       set_status(p.status, GDN_DEV_BAD_LENGTH);
     } else {
@@ -120,91 +184,55 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
       slot = (((size_t)pg * p.Hk) << p.page_shift) + (pos & (p.page - 1));
     }
   }
-
-  float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (live && turned) {
-    if (pos < 0 || pos >= p.max_pos) {
-      set_status(p.status, GDN_DEV_BAD_LENGTH);
-      pos = pos < 0 ? 0 : p.max_pos - 1;
-    }
-    const size_t row = (size_t)pos * p.rot + 4 * lane;
-    load4<false>(p.rope, row, c);
-    load4<false>(p.rope, row + half, s);
-  }
-
-  const float* w_now = nullptr;  // the norm weights held in w
-  float w[8];
+  const bool norm = (is_q ? p.qw : p.kw) != nullptr;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const uint32_t h = h0 + r;
-    const bool is_q = h < (uint32_t)p.H, is_v = h >= (uint32_t)(p.H + p.Hk);
-    float (&z)[8] = y[r];
-    float ss = 0.f;
+    const uint32_t h = h0 + r, k_end = p.H + p.Hk;
+    float z[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += z[i] * z[i];
-#pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (!live || h >= heads) continue;
-    if (!is_v) {
-      const float* wp = is_q ? p.qw : p.kw;
-      if (wp) {
-        if (wp != w_now) {
-          load4<false>(wp, e0, w);
-          load4<false>(wp, e1, w + 4);
-          w_now = wp;
-        }
-        const float q = ss * (1.0f / D) + p.eps;
-        float norm = rsqrtf(q);  // 2 ulp; one Newton step brings it to rounding
-        norm *= 1.5f - 0.5f * q * norm * norm;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) z[i] *= norm * w[i];
-      }
-      auto turn = [&](float& a, float& d, int i) {
-        const float a0 = a;
-        a = a0 * c[i] - d * s[i];
-        d = d * c[i] + a0 * s[i];
-      };
-      if (split) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) turn(z[i], z[4 + i], i);
-      } else if (turned) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) turn(z[2 * i], z[2 * i + 1], i);
-      }
-    }
-    auto put = [&](void* dst, size_t row) {
-      store4<kOutBf16>(dst, row * D + e0, z);
-      store4<kOutBf16>(dst, row * D + e1, z + 4);
-    };
+    for (int i = 0; i < 8; ++i) z[i] = y[r][i];
+    norm_turn(z, w, norm);
+    if (!live || r >= cnt) continue;
     if (is_q) {
-      put(p.q, (size_t)t * p.H + h);
-    } else {
-      const uint32_t hk = is_v ? h - p.H - p.Hk : h - p.H;
-      void* dense = is_v ? p.v : p.k;
-      if (dense) put(dense, (size_t)t * p.Hk + hk);
-      if (append) put(is_v ? p.vc : p.kc, slot + ((size_t)hk << p.page_shift));
+      put(p.q, ((size_t)t * p.H + h) * D, z);
+      continue;
     }
+    const bool is_v = h >= k_end;
+    if (is_v) {
+#pragma unroll
+      for (int i = 0; i < 8; ++i) z[i] = y[r][i];
+    }
+    const uint32_t hk = is_v ? h - k_end : h - p.H;
+    void* dense = is_v ? p.v : p.k;
+    if (dense) put(dense, ((size_t)t * p.Hk + hk) * D, z);
+    if (append) put(is_v ? p.vc : p.kc, (slot + ((size_t)hk << p.page_shift)) * D, z);
   }
 }
 
-template <int D, bool kInBf16, bool kOutBf16>
+template <int D, bool kInBf16, bool kOutBf16, bool kInter>
 bool launch(const AttnFrontParams& p, cudaStream_t s) {
-  const int heads = p.H + 2 * p.Hk, per_block = kThreads / (D / 8);
-  const int64_t rows = (int64_t)p.T * heads;
+  const int per_block = kThreads / (D / 8);
+  const int64_t rows = (int64_t)p.T * (p.H + 2 * p.Hk);
   // One head per lane group while that leaves SMs idle (a decode step: the fewer steps in a
   // row the better), four when there is work for all of them.
   const bool wide = rows >= 8 * 152 * 16;
-  const int64_t items = wide ? (int64_t)p.T * ((heads + 3) / 4) : rows;
+  const int64_t items = wide ? (int64_t)p.T * ((p.H + 3) / 4 + (2 * p.Hk + 3) / 4) : rows;
   const int64_t blocks = (items + per_block - 1) / per_block;
-  const auto kernel = wide ? attn_front_kernel<D, kInBf16, kOutBf16, 4> : attn_front_kernel<D, kInBf16, kOutBf16, 1>;
+  const auto kernel = wide ? attn_front_kernel<D, kInBf16, kOutBf16, 4, kInter>
+                           : attn_front_kernel<D, kInBf16, kOutBf16, 1, kInter>;
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, p) == cudaSuccess;
+}
+
+template <int D, bool kInter>
+bool launch_t(const AttnFrontParams& p, cudaStream_t s) {
+  if (p.in_bf16)
+    return p.out_bf16 ? launch<D, true, true, kInter>(p, s) : launch<D, true, false, kInter>(p, s);
+  return p.out_bf16 ? launch<D, false, true, kInter>(p, s) : launch<D, false, false, kInter>(p, s);
 }
 
 template <int D>
 bool launch_d(const AttnFrontParams& p, cudaStream_t s) {
-  if (p.in_bf16)
-    return p.out_bf16 ? launch<D, true, true>(p, s) : launch<D, true, false>(p, s);
-  return p.out_bf16 ? launch<D, false, true>(p, s) : launch<D, false, false>(p, s);
+  return p.interleaved ? launch_t<D, true>(p, s) : launch_t<D, false>(p, s);
 }
 
 }  // namespace
