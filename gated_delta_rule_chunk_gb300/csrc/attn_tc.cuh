@@ -49,6 +49,7 @@ struct AttnItem {
   int hk;
   int kv0;         // first key tile (prompts: 0)
   int nA, nB;      // key tiles of A and B (nB = 0: no tile B)
+  int z;           // prefix: which split of the keys
   int mask0;       // first key tile that some row sees only in part
   int valid;
 };
@@ -291,16 +292,21 @@ struct PrefixItems {
   __device__ AttnItem get(int idx, int nt) const {
     AttnItem it{};
     if (idx >= total) return it;
-    const int z = idx % x.splits, at = idx / x.splits, lane = threadIdx.x & 31;
+    // The split runs fastest: CTAs that work at the same time read neighbouring keys.
+    const uint32_t at = (uint32_t)idx / x.splits, pair = at / p.Hk, lane = threadIdx.x & 31;
+    const int q = x.tiles / x.splits, rest = x.tiles - q * x.splits;  // the first have one more
+    it.z = idx - at * x.splits;
     it.len = p.T;
-    it.tok = at / p.Hk * span;
-    it.hk = at % p.Hk;
-    it.kv0 = (int)((int64_t)z * x.tiles / x.splits);
-    it.nA = (int)((int64_t)(z + 1) * x.tiles / x.splits) - it.kv0;
+    it.tok = pair * span;
+    it.hk = at - pair * p.Hk;
+    it.kv0 = it.z * q + min(it.z, rest);
+    it.nA = q + (it.z < rest);
     it.nB = it.tok + nt < it.len ? it.nA : 0;
-    int lim = p.shared;  // keys that every row of the pair sees
-    for (int t = it.tok + lane; t < min(it.tok + span, it.len); t += 32)
-      lim = min(lim, keys_seen(p, t / p.nq, t % p.nq));
+    // keys that every row of the pair sees: a sequence's first new token sees the fewest
+    int lim = p.shared;
+    const int last = min(it.tok + span, it.len) - 1;
+    for (int n = it.tok / p.nq + lane; n <= last / p.nq; n += 32)
+      lim = min(lim, keys_seen(p, n, 0));
     it.mask0 = max(__reduce_min_sync(0xffffffffu, lim) / kKeys - it.kv0, 0);
     it.valid = 1;
     return it;
@@ -476,11 +482,8 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       ++tiles;
       tc_fence_after();
       int64_t at = (int64_t)(it.base + tok) * p.H + it.hk * p.G + rh;
-      int64_t split = 0;
-      if constexpr (kPrefix) {
-        split = ((int64_t)it.kv0 * parts.splits + parts.tiles - 1) / parts.tiles;
-        at += split * p.T * p.H;
-      }
+      const int64_t part0 = kPrefix ? (int64_t)it.z * p.T * p.H : 0;  // the split's rows
+      at += part0;
       const bool poison = *reinterpret_cast<volatile int*>(&B.poison[k & 3]) == (int)k + 1;
       // prefix: as they are, for the merge with the other splits; NaN stays NaN
       const float r = kPrefix ? 1.f : l == 0.f ? 0.f : 1.f / l;
@@ -550,7 +553,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
             };
             attn_row<D>(p.q + tr * D, k1 - k0, p.scale, [&](int j) { return at_key(p.k, j); },
                         [&](int j) { return at_key(p.v, j); }, o, lse);
-            const size_t row = split * p.T * p.H + tr;
+            const size_t row = part0 + tr;
             store_row<D>(parts.o, false, row, o);
             if (lane == 0)
               parts.ml[row] = make_float2(lse * 1.44269504088896340736f, lse == -INFINITY ? 0.f : 1.f);
@@ -593,7 +596,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           const int key = (it.kv0 + j) * kKeys + lane * min(p.page, kKeys);
           return lane * p.page < kKeys && key < p.shared ? p.table[key >> p.page_shift] : -1;
         };
-        int page = kPrefix ? page_of(0) : 0;
+        int page = 0;
         auto load_kv = [&](const CUtensorMap* tm, int j, bool raw) {
           const int st = slot % kStages;
           wait(&B.kv_empty[st], slot / kStages + 1);
@@ -622,6 +625,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           }
         };
         load_q(0);
+        if (kPrefix) page = page_of(0);
         load_kv(&tm_k, 0, false);
         load_q(1);
         for (int j = 0; j < n; ++j) {
