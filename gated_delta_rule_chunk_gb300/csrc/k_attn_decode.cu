@@ -44,9 +44,15 @@ struct DecodeParts {
 __device__ __forceinline__ int chunks_of(const AttnParams& p, int n) {
   return (max(seq_len(p, n) - p.shared, 0) + kUnit - 1) / kUnit;
 }
-// The first unit of CTA c, and the CTA of unit u; grid: the CTAs at work, at most one a unit.
-__device__ __forceinline__ int unit_of(int c, int U, int grid) { return (int)((int64_t)c * U / grid); }
+// Equal parts of U units for `grid` CTAs (at most one a unit): CTA c's first unit, and the
+// CTA of unit u. The parts that are one unit longer are spread evenly: with the first CTAs
+// taking them, both CTAs of the same SMs do (64 sequences 159 -> 170 us).
+__device__ __forceinline__ int unit_of(int c, int U, int grid) {
+  if (U < 1 << 22) return (int)((uint32_t)c * (uint32_t)U / (uint32_t)grid);  // c < 1024
+  return (int)((int64_t)c * U / grid);
+}
 __device__ __forceinline__ int cta_of(int u, int U, int grid) {
+  if (U < 1 << 22) return (int)(((uint32_t)(u + 1) * grid - 1) / (uint32_t)U);
   return (int)((((int64_t)u + 1) * grid - 1) / U);
 }
 
@@ -76,7 +82,10 @@ template <int D>
 struct DecodeSmem {
   static constexpr int kRow = D * 2;                 // bytes of a key
   static constexpr int kStage = 2 * kBlk * kRow;     // a K and a V block
-  static constexpr int kStages = D == 128 ? 3 : 6;   // 96 KB in flight per CTA
+  // 64 KB of ring per CTA, half of it in flight. More only makes every other read (a row of
+  // the queries, a page number) wait longer in a saturated memory system: with 96 KB, 64
+  // sequences of up to 8192 keys took 163.4 us, with 64 KB 159.0 us.
+  static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kMerge = kWarps * kStages * kStage;
   static constexpr int kMl = kMerge + 2 * kWarps * 16 * 32 * 4;
   static constexpr int kBytes = kMl + kWarps * 16 * 8;
