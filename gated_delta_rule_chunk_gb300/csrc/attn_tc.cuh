@@ -22,7 +22,12 @@
 //                   a value that is not finite is looked for, because a weight of 0 would
 //                   not remove it (0 * inf); the rows of such a tile pair are then computed
 //                   one by one without it (rare, so only correctness counts there).
-// TMEM: S_A, S_B [0, 256), O_A, O_B [256, 256 + 2 D).
+// TMEM: score buffers of 128 columns, then O_A and O_B of D. At D = 128 there is room for two
+// buffers, one of A's and one of B's: a tile's next scores wait for its own P V, and the order
+// of issue keeps them apart. At D = 64 there are three, taken in turn by the sequence of
+// products (A and B of each key tile), so that the next scores are there before the row warps
+// have weighed these; the products are short, and two warps issue them: warp 9 Q K^T, warp 11
+// P V (one warp's issue took 1,200 cycles a product, twice the MMAs).
 #pragma once
 
 #include <cuda.h>
@@ -39,6 +44,7 @@ constexpr int kAttnThreads = 512;
 constexpr int kRows = 128;           // rows of a tile
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kAttnSeqs = 1024;      // sequences of one launch
+constexpr int kItems = 4;            // work items handed out ahead
 constexpr uint32_t kPolls = 1u << 22;
 constexpr float kGrow = 8.0f;
 
@@ -70,12 +76,13 @@ struct AttnSmem {
   static constexpr int kGroup = kPrefix ? D * 16 : 1024;    // bytes from 8 rows to the next
   static constexpr int kHalf = kPrefix ? 1024 : 128 * 128;  // ... from a half to the other
   static constexpr int kStages = D == 128 ? 4 : 8;
+  static constexpr int kBufs = D == 128 ? 2 : 3;       // score buffers
   static constexpr int kQ = 0, kRing = 2 * kTile;
   static constexpr int kBounds = kRing + kStages * kTile;      // sanitized cu_seqlens, pairs
   static constexpr int kOutRow = 80;                           // 64 bytes of a row, padded
   static constexpr int kOut = kBounds + 8 * (kAttnSeqs + 4);   // 32 rows a row warp
   static constexpr int kBars = kOut + 8 * 32 * kOutRow;
-  static constexpr int kBytes = kBars + 512 + 1024;            // + alignment of the tiles
+  static constexpr int kBytes = kBars + 768 + 1024;            // + alignment of the tiles
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -187,16 +194,23 @@ __device__ __forceinline__ void regs_dec() {
 }
 
 // Barriers of the attention kernel (all in shared memory).
-template <int kStages>
+template <int kStages, int kSet>
 struct AttnBars {
   // A V tile with masked keys completes v_raw and, once the V warps are done, v_fixed, in
   // place of kv_full: so whoever waits on one of the three sees each of its phases.
   uint64_t kv_full[kStages], kv_empty[kStages], v_raw[kStages], v_fixed[kStages];
-  uint64_t q_full[2], q_empty[2], s_full[2], p_full[2], o_full[2], o_empty[2];
-  uint64_t item_full[2], item_empty[2];
-  AttnItem item[2];
+  // s_full, p_full, o_full: A's and B's scores, weights and products into O are complete (with
+  // two score buffers, o_full: the item's last product). With three score buffers, all may hold tiles of one of them, and one side of a barrier be as
+  // many tiles ahead of the other's wait: so A's and B's tiles each take the barriers in turn.
+  // buf_empty: the product with the weights in a score buffer is complete.
+  uint64_t q_full[2], q_empty[2], s_full[2][kSet], p_full[2][kSet], o_full[2][kSet];
+  uint64_t o_empty[2], buf_empty[3];
+  uint64_t item_full[kItems], item_empty[kItems];
+  AttnItem item[kItems];
   uint32_t tmem;
-  int poison[4];  // item number + 1 of the last item in this place with an unsafe V tile
+  // Item number + 1 of the last item in this place with an unsafe V tile: the ring holds V
+  // tiles of at most four items after the one whose rows are being written.
+  int poison[8];
 };
 
 // A bounded wait: once one has run out, this thread waits for nothing any more.
@@ -319,13 +333,14 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
                const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v) {
   using S = AttnSmem<D, kPrefix>;
-  constexpr int kStages = S::kStages;
+  constexpr int kStages = S::kStages, kBufs = S::kBufs;
+  constexpr int kSet = kBufs == 2 ? 1 : kBufs;  // barriers of a kind for each of A and B
   extern __shared__ char smem_raw[];
   char* smem = smem_raw + ((1024 - (smem_addr(smem_raw) & 1023)) & 1023);
   int* bounds = reinterpret_cast<int*>(smem + S::kBounds);
   int* pairs = bounds + kAttnSeqs + 4;  // pairs of row tiles of each sequence
-  auto& B = *reinterpret_cast<AttnBars<kStages>*>(smem + S::kBars);
-  static_assert(sizeof(AttnBars<kStages>) <= 512, "barrier area");
+  auto& B = *reinterpret_cast<AttnBars<kStages, kSet>*>(smem + S::kBars);
+  static_assert(sizeof(AttnBars<kStages, kSet>) <= 768, "barrier area");
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int nt = kRows / p.G;  // tokens of a row tile
   if (threadIdx.x == 0) {
@@ -338,14 +353,19 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
     for (int i = 0; i < 2; ++i) {
       mbar_init(&B.q_full[i], 1);
       mbar_init(&B.q_empty[i], 1);
-      mbar_init(&B.s_full[i], 1);
-      mbar_init(&B.p_full[i], 4);
-      mbar_init(&B.o_full[i], 1);
       mbar_init(&B.o_empty[i], 4);
-      mbar_init(&B.item_full[i], 1);
-      mbar_init(&B.item_empty[i], 14);  // load, MMA, 8 row warps, 4 V warps
+      for (int x = 0; x < kSet; ++x) {
+        mbar_init(&B.s_full[i][x], 1);
+        mbar_init(&B.p_full[i][x], 4);
+        mbar_init(&B.o_full[i][x], 1);
+      }
     }
-    for (int i = 0; i < 4; ++i) B.poison[i] = 0;
+    for (int i = 0; i < 3; ++i) mbar_init(&B.buf_empty[i], 1);
+    for (int i = 0; i < kItems; ++i) {
+      mbar_init(&B.item_full[i], 1);
+      mbar_init(&B.item_empty[i], kBufs == 2 ? 14 : 15);  // load, MMA, 8 row warps, 4 V warps
+    }
+    for (int i = 0; i < 8; ++i) B.poison[i] = 0;
     mbar_init_fence();
   }
   if (warp == 8) {
@@ -393,17 +413,20 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
     regs_inc<192>();
     const int X = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + lanes + X * 128, tO = tmem + lanes + 256 + X * D;
+    const uint32_t tO = tmem + lanes + kBufs * 128 + X * D;
     const float c = p.scale * 1.44269504088896340736f;
     const int rt = row / p.G, rh = row - rt * p.G;  // token and head of this row in the tile
-    uint32_t steps = 0, tiles = 0;
+    // the item's first product; products into O_X and tiles written before it
+    uint32_t seq0 = 0, products = 0, written = 0;
     for (uint32_t k = 0;; ++k) {
-      wait(&B.item_full[k & 1], k >> 1);
-      const AttnItem it = B.item[k & 1];
+      wait(&B.item_full[k % kItems], k / kItems);
+      const AttnItem it = B.item[k % kItems];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
+      if (lane == 0) mbar_arrive(&B.item_empty[k % kItems]);
       if (!it.valid || !wait.ok()) break;
       const int n = X ? it.nB : it.nA;
+      const uint32_t first = seq0;
+      seq0 += it.nA + it.nB;
       if (n == 0) continue;
       const int tok = it.tok + X * nt + rt;
       const bool real = rt < nt && tok < it.len;
@@ -412,8 +435,11 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       const int lim = kPrefix ? min(keys_seen(p, last / p.nq, last % p.nq), p.shared) - it.kv0 * kKeys
                               : last + 1;
       float ref = -INFINITY, l = 0.f;            // reference of the weights, their sum
-      for (int j = 0; j < n; ++j, ++steps) {
-        wait(&B.s_full[X], steps);
+      for (int j = 0; j < n; ++j) {
+        // this tile's place among all products, and among those of X
+        const uint32_t seq = first + j + (X ? min(j + 1, it.nA) : min(j, it.nB)), own = products + j;
+        const uint32_t tS = tmem + lanes + (kBufs == 2 ? X : seq % kBufs) * 128;
+        wait(&B.s_full[X][own % kSet], own / kSet);
         tc_fence_after();
         float s[128];
 #pragma unroll
@@ -435,13 +461,17 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         }
         const float m = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3]));
         // A new reference where the maximum outgrew the old one (always in the first tile
-        // that holds a key). S being complete, the product of the tile before is too.
+        // that holds a key).
         const bool grown = m > ref && (m - ref) * c > kGrow;
         if (__any_sync(0xffffffffu, grown)) {
           const float f = grown ? ex2((ref - m) * c) : 1.f;  // 0 from -inf
           if (grown) ref = m;
           l *= f;
           if (j > 0) {
+            // (in order of issue, the product of the tile before is complete when S is; three
+            // buffers have S made before it)
+            if (kBufs > 2) wait(&B.o_full[X][(own - 1) % kSet], (own - 1) / kSet);
+            tc_fence_after();
 #pragma unroll 1
             for (int q = 0; q < D; q += 16) {
               float o[16];
@@ -476,15 +506,17 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         tmem_st_wait();
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.p_full[X]);
+        if (lane == 0) mbar_arrive(&B.p_full[X][own % kSet]);
       }
-      wait(&B.o_full[X], tiles);
-      ++tiles;
+      products += n;
+      if (kBufs == 2) wait(&B.o_full[X][0], written);
+      else wait(&B.o_full[X][(products - 1) % kSet], (products - 1) / kSet);
+      ++written;
       tc_fence_after();
       int64_t at = (int64_t)(it.base + tok) * p.H + it.hk * p.G + rh;
       const int64_t part0 = kPrefix ? (int64_t)it.z * p.T * p.H : 0;  // the split's rows
       at += part0;
-      const bool poison = *reinterpret_cast<volatile int*>(&B.poison[k & 3]) == (int)k + 1;
+      const bool poison = *reinterpret_cast<volatile int*>(&B.poison[k & 7]) == (int)k + 1;
       // prefix: as they are, for the merge with the other splits; NaN stays NaN
       const float r = kPrefix ? 1.f : l == 0.f ? 0.f : 1.f / l;
       // A thread holds a whole row; stored from here, every 16 bytes of a warp's store would
@@ -574,10 +606,10 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       uint32_t slot = 0, loads[2] = {0, 0};
       uint32_t kv_uses = 0, raw_uses = 0, is_raw = 0;  // per stage: uses (mod 2), the last one
       for (uint32_t k = 0;; ++k) {
-        wait(&B.item_full[k & 1], k >> 1);
-        const AttnItem it = B.item[k & 1];
+        wait(&B.item_full[k % kItems], k / kItems);
+        const AttnItem it = B.item[k % kItems];
         if constexpr (kPrefix) __syncwarp();
-        if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
+        if (lane == 0) mbar_arrive(&B.item_empty[k % kItems]);
         if (!it.valid || !wait.ok()) break;
         const int n = max(it.nA, it.nB);
         auto load_q = [&](int X) {
@@ -645,7 +677,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       }
     }
     // ---------------------------------------------------------------- products
-    if (warp == 9) {
+    if (kBufs == 2 && warp == 9) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
       constexpr uint32_t kT = S::kTile >> 4;
@@ -681,12 +713,12 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         for (int d = 0; d < D; d += 16)
           mma_ss(el, tm + X * 128, q_lo + X * kT + (((d >> 6) * 16384 + (d & 63) * 2) >> 4), kQHi,
                  b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kKHi, kIdS, d > 0);
-        mma_commit(el, &B.s_full[X]);
+        mma_commit(el, &B.s_full[X][0]);
         if (last) mma_commit(el, &B.q_empty[X]);
       };
       auto weigh = [&](auto x, uint32_t st, bool first, bool last) {  // O_X (+)= P_X V
         constexpr int X = decltype(x)::value;
-        wait(&B.p_full[X], ps >> X);
+        wait(&B.p_full[X][0], ps >> X);
         ps ^= 1u << X;
         if (first) {
           wait(&B.o_empty[X], os >> X);
@@ -696,9 +728,9 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         const uint32_t b = v_lo + st * kT;
 #pragma unroll
         for (int t = 0; t < kKeys; t += 16)
-          mma_ts(el, tm + 256 + X * D, tm + X * 128 + (t >> 1), b + ((t >> 3) * S::kGroup >> 4),
+          mma_ts(el, tm + kBufs * 128 + X * D, tm + X * 128 + (t >> 1), b + ((t >> 3) * S::kGroup >> 4),
                  kKHi, kIdO, t > 0 || !first);
-        if (last) mma_commit(el, &B.o_full[X]);
+        if (last) mma_commit(el, &B.o_full[X][0]);
       };
       auto wait_q = [&](int X) {
         wait(&B.q_full[X], qs >> X);
@@ -706,13 +738,13 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       };
       // The fields of item k that count here (no tiles: the end).
       auto item = [&](uint32_t k, int& a, int& b, int& mask0) {
-        wait(&B.item_full[k & 1], k >> 1);
-        const AttnItem& it = B.item[k & 1];
+        wait(&B.item_full[k % kItems], k / kItems);
+        const AttnItem& it = B.item[k % kItems];
         const bool ok = it.valid && wait.ok();
         a = (int)uniform(ok ? it.nA : 0);
         b = (int)uniform(ok ? it.nB : 0);
         mask0 = (int)uniform(it.mask0);
-        arrive_one(el, &B.item_empty[k & 1]);
+        arrive_one(el, &B.item_empty[k % kItems]);
       };
       constexpr std::integral_constant<int, 0> A{};
       constexpr std::integral_constant<int, 1> Bt{};
@@ -763,6 +795,92 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         mask0 = m2;
       }
     }
+    // Three score buffers: warp 9 issues Q K^T, warp 11 P V, in the same sequence.
+    if (kBufs == 3 && (warp == 9 || warp == 11)) {
+      constexpr uint32_t kT = S::kTile >> 4, kHi = (1u << 14) | (2u << 29);
+      constexpr uint32_t kQHi = kHi | (1024 >> 4), kKHi = kHi | (S::kGroup >> 4);
+      const uint32_t q_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024));
+      const uint32_t k_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kRing), 16, S::kGroup));
+      const uint32_t v_lo =
+          uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kRing), S::kHalf, S::kGroup));
+      const uint32_t el = elect_one(), tm = uniform(tmem);
+      const bool qk = warp == 9;
+      uint32_t kvs = 0, fixes = 0;      // parities to wait for, a bit per ring place
+      uint32_t qs = 0, os = 3;          // ... and for A and B
+      uint32_t buf = 0, turn = 0;       // score buffer of the next product, times round
+      uint32_t own[2] = {0, 0}, round[2] = {0, 0};  // barriers of A's, B's next tile, times round
+      uint32_t st = qk ? 0 : 1;         // ring place of the key tile
+      auto step = [&](auto x, int j, int n, bool first, bool end, bool masked) {
+        constexpr int X = decltype(x)::value;
+        if (qk) {
+          wait(&B.buf_empty[buf], turn + 1);
+          if (j == 0) {
+            wait(&B.q_full[X], qs >> X);
+            qs ^= 1u << X;
+          }
+          if (first) {
+            wait(&B.kv_full[st], kvs >> st);
+            kvs ^= 1u << st;
+          }
+          tc_fence_after();
+          const uint32_t b = k_lo + st * kT;
+#pragma unroll
+          for (int d = 0; d < D; d += 16)
+            mma_ss(el, tm + buf * 128, q_lo + X * kT + (((d >> 6) * 16384 + (d & 63) * 2) >> 4), kQHi,
+                   b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kKHi, idesc_bf16_f32(128, kKeys),
+                   d > 0);
+          mma_commit(el, &B.s_full[X][own[X]]);
+          if (j == n - 1) mma_commit(el, &B.q_empty[X]);
+        } else {
+          if (first && masked) {
+            wait(&B.v_fixed[st], fixes >> st);
+            fixes ^= 1u << st;
+          } else if (first) {
+            wait(&B.kv_full[st], kvs >> st);
+            kvs ^= 1u << st;
+          }
+          if (j == 0) {
+            wait(&B.o_empty[X], os >> X);
+            os ^= 1u << X;
+          }
+          wait(&B.p_full[X][own[X]], round[X]);
+          tc_fence_after();
+          const uint32_t b = v_lo + st * kT;
+#pragma unroll
+          for (int t = 0; t < kKeys; t += 16)
+            mma_ts(el, tm + kBufs * 128 + X * D, tm + buf * 128 + (t >> 1),
+                   b + ((t >> 3) * S::kGroup >> 4), kKHi, idesc_bf16_f32(128, D, false, true),
+                   t > 0 || j > 0);
+          mma_commit(el, &B.o_full[X][own[X]]);
+          mma_commit(el, &B.buf_empty[buf]);
+        }
+        if (end) {  // the last product of this key tile
+          mma_commit(el, &B.kv_empty[st]);
+          st = st + 2 >= kStages ? st + 2 - kStages : st + 2;
+        }
+        if (++buf == kBufs) {
+          buf = 0;
+          ++turn;
+        }
+        if (++own[X] == kSet) {
+          own[X] = 0;
+          ++round[X];
+        }
+      };
+      for (uint32_t k = 0;; ++k) {
+        wait(&B.item_full[k % kItems], k / kItems);
+        const AttnItem& it = B.item[k % kItems];
+        const bool ok = it.valid && wait.ok();
+        const int nA = (int)uniform(ok ? it.nA : 0), nB = (int)uniform(ok ? it.nB : 0);
+        const int mask0 = (int)uniform(it.mask0);
+        arrive_one(el, &B.item_empty[k % kItems]);
+        if (nA == 0) break;
+        for (int j = 0; j < max(nA, nB); ++j) {
+          if (j < nA) step(std::integral_constant<int, 0>{}, j, nA, true, j >= nB, j >= mask0);
+          if (j < nB) step(std::integral_constant<int, 1>{}, j, nB, j >= nA, true, j >= mask0);
+        }
+      }
+    }
     // ---------------------------------------------------------------- work items
     if (warp == 10) {
       auto items = [&] {
@@ -777,10 +895,10 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         // every other round dealt backwards, which evens out the falling sizes
         const int64_t idx = (int64_t)k * grid + ((k & 1) ? grid - 1 - b : b);
         const AttnItem it = items.get((int)min(idx, (int64_t)items.total), nt);
-        wait(&B.item_empty[k & 1], (k >> 1) + 1);
+        wait(&B.item_empty[k % kItems], k / kItems + 1);
         if (lane == 0) {
-          B.item[k & 1] = it;
-          mbar_arrive(&B.item_full[k & 1]);
+          B.item[k % kItems] = it;
+          mbar_arrive(&B.item_full[k % kItems]);
         }
         __syncwarp();
         // a round dealt backwards may skip this CTA in the last, partial round only
@@ -794,10 +912,10 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
     const int tid = threadIdx.x - 12 * 32;
     uint32_t base = 0, raws = 0;
     for (uint32_t k = 0;; ++k) {
-      wait(&B.item_full[k & 1], k >> 1);
-      const AttnItem it = B.item[k & 1];
+      wait(&B.item_full[k % kItems], k / kItems);
+      const AttnItem it = B.item[k % kItems];
       __syncwarp();
-      if (lane == 0) mbar_arrive(&B.item_empty[k & 1]);
+      if (lane == 0) mbar_arrive(&B.item_empty[k % kItems]);
       if (!it.valid || !wait.ok()) break;
       const int n = max(it.nA, it.nB);
       for (int j = it.mask0; j < n; ++j) {
@@ -823,7 +941,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
             found |= (e & 0x80008000u) != 0;
           }
         }
-        if (found) *reinterpret_cast<volatile int*>(&B.poison[k & 3]) = (int)k + 1;
+        if (found) *reinterpret_cast<volatile int*>(&B.poison[k & 7]) = (int)k + 1;
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&B.v_fixed[st]);
