@@ -1,4 +1,5 @@
-"""Thin ctypes binding over libgdn (include/gdn.h): argument marshalling only.
+"""Thin binding over libgdn (include/gdn.h, include/gdn_attn.h): argument marshalling only,
+through ctypes (the attention calls: through a small compiled module).
 
 Every step of the method runs in the CUDA kernels behind the C ABI. Torch is
 used here only to own device memory (outputs, workspace) and to name the
@@ -8,6 +9,7 @@ CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import math
 import os
 import threading
@@ -489,8 +491,27 @@ def gdn_workspace_regions(desc: GdnDesc):
 
 
 # ---------------------------------------------------------------- softmax attention
-_DTYPE_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
-_decode_workspace: dict = {}  # gdn_attn_workspace_size by (N, n_q, H, Hk, D, device)
+_attn_module = None
+
+
+def _attn():
+    """The compiled marshalling of the attention calls (csrc/attn_torch.cpp), bound to the
+    loaded library. Raises if it has not been built."""
+    global _attn_module
+    lib = load_library()
+    with _lock:
+        if _attn_module is None:
+            path = os.path.join(_PKG, "_attn_torch.so")
+            if not os.path.exists(path):
+                raise GdnError(-6, f"{path} is missing (build it with __graft_entry__.build())")
+            spec = importlib.util.spec_from_file_location("_attn_torch", path)
+            module = importlib.util.module_from_spec(spec)
+            spec.loader.exec_module(module)
+            module.init(GdnError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
+                lib.gdn_attn_front, lib.gdn_attn_prefill, lib.gdn_attn_decode,
+                lib.gdn_attn_workspace_size, lib.gdn_attn_check_desc)))
+            _attn_module = module
+        return _attn_module
 
 
 def make_attn_desc(T: int, N: int, H: int, Hk: int, D: int, in_dtype: torch.dtype = torch.bfloat16,
@@ -508,36 +529,6 @@ def gdn_attn_check_desc(desc: GdnAttnDesc) -> int:
 
 def gdn_attn_workspace_size(desc: GdnAttnDesc) -> int:
     return int(load_library().gdn_attn_workspace_size(ctypes.byref(desc)))
-
-
-def _addr(t: Optional[torch.Tensor], name: str, dtype: Optional[torch.dtype] = None,
-          shape: Optional[tuple] = None) -> Optional[int]:
-    """Device address of an optional contiguous CUDA tensor of this dtype and shape."""
-    if t is None:
-        return None
-    if (t.is_cuda and t.is_contiguous() and (dtype is None or t.dtype is dtype)
-            and (shape is None or t.shape == shape)):
-        return t.data_ptr()
-    if not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    raise ValueError(f"{name} must have shape {list(shape)}, got {list(t.shape)}")
-
-
-def _stream_of(stream, t: torch.Tensor) -> int:
-    """The stream's handle; without one, that of the current stream of t's device."""
-    if stream is not None:
-        return stream.cuda_stream
-    return torch._C._cuda_getCurrentRawStream(t.get_device())
-
-
-def _num_seqs(cu_seqlens: Optional[torch.Tensor]) -> int:
-    if cu_seqlens is None:
-        return 1
-    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 2:
-        raise ValueError("cu_seqlens must have shape [N + 1] with N >= 1")
-    return cu_seqlens.shape[0] - 1
 
 
 def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
@@ -560,49 +551,14 @@ def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
     rope.rope_table) at the token's position. With page_table [N, max_pages] int32, k_cache
     and v_cache [n_pages, Hk, page_size, D], k and v are appended to the cache; kv_lens [N]
     int32 are the cache's lengths after that (None: the tokens are the sequence's first).
-    Returns (q [T, H, D], k, v [T, Hk, D]), the last two None when output_kv is false.
-    `status`, if given, is one int32 on the device that receives the device status word.
+    out_dtype (fp32 or bf16) defaults to the cache's, else to x's. Returns (q [T, H, D], k,
+    v [T, Hk, D]), the last two None when output_kv is false; q, k, v may be given. `status`,
+    if given, is one int32 on the device that receives the device status word.
     """
-    T = x.shape[0]
-    dev = x.device
-    N = _num_seqs(cu_seqlens)
-    if out_dtype is None:
-        out_dtype = k_cache.dtype if k_cache is not None else q.dtype if q is not None else x.dtype
-    if x.dtype not in _DTYPE_CODES or out_dtype not in _DTYPE_CODES:
-        raise TypeError(f"unsupported dtype {x.dtype} -> {out_dtype}")
-    if q is None:
-        q = torch.empty((T, H, D), dtype=out_dtype, device=dev)
-    if output_kv:
-        if k is None:
-            k = torch.empty((T, Hk, D), dtype=out_dtype, device=dev)
-        if v is None:
-            v = torch.empty((T, Hk, D), dtype=out_dtype, device=dev)
-    else:
-        k = v = None
-    max_pos, rot = (0, 0) if rope is None else rope.shape
-    n_pages = page = max_pages = 0
-    if k_cache is not None:
-        if k_cache.dim() != 4 or page_table is None or page_table.dim() != 2:
-            raise ValueError("the cache needs k_cache, v_cache [n_pages, Hk, page_size, D] and "
-                             "page_table [N, max_pages]")
-        n_pages, page, max_pages = k_cache.shape[0], k_cache.shape[2], page_table.shape[1]
-    desc = GdnAttnDesc(T, N, H, Hk, D, page, n_pages, max_pages, rot, max_pos,
-                       _DTYPE_CODES[x.dtype], _DTYPE_CODES[out_dtype],
-                       GDN_ATTN_ROPE_INTERLEAVED if interleaved else 0, norm_eps,
-                       _addr(status, "status", torch.int32), None, 0)
-    cache_shape = (n_pages, Hk, page, D)
-    rc = (_lib or load_library()).gdn_attn_front(
-        ctypes.byref(desc), _addr(x, "x", None, (T, (H + 2 * Hk) * D)),
-        _addr(q_weight, "q_weight", torch.float32, (D,)),
-        _addr(k_weight, "k_weight", torch.float32, (D,)), _addr(rope, "rope", torch.float32),
-        _addr(cu_seqlens, "cu_seqlens", torch.int32), _addr(kv_lens, "kv_lens", torch.int32, (N,)),
-        _addr(page_table, "page_table", torch.int32, (N, max_pages)),
-        _addr(q, "q", out_dtype, (T, H, D)), _addr(k, "k", out_dtype, (T, Hk, D)),
-        _addr(v, "v", out_dtype, (T, Hk, D)), _addr(k_cache, "k_cache", out_dtype, cache_shape),
-        _addr(v_cache, "v_cache", out_dtype, cache_shape), _stream_of(stream, x))
-    if rc != 0:
-        raise GdnError(rc, "gdn_attn_front")
-    return q, k, v
+    return (_attn_module or _attn()).front(
+        x, H, Hk, D, q_weight, k_weight, norm_eps, rope, interleaved, cu_seqlens, kv_lens,
+        page_table, k_cache, v_cache, output_kv, out_dtype, q, k, v, status,
+        None if stream is None else stream.cuda_stream)
 
 
 def gdn_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -613,23 +569,9 @@ def gdn_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
     """Causal attention of packed prompts through the C ABI: q [T, H, D], k, v [T, Hk, D]
     bf16, D = 128 or 64, H a multiple of Hk; cu_seqlens int32 [N + 1] or None (one
     sequence). Returns out [T, H, D], or (out, lse) with lse fp32 [T, H] when return_lse."""
-    T, H, D = q.shape
-    Hk = k.shape[1]
-    N = _num_seqs(cu_seqlens)
-    if out is None:
-        out = torch.empty((T, H, D), dtype=out_dtype or q.dtype, device=q.device)
-    if return_lse and lse is None:
-        lse = torch.empty((T, H), dtype=torch.float32, device=q.device)
-    desc = GdnAttnDesc(T, N, H, Hk, D, 0, 0, 0, 0, 0, _dtype_code(q.dtype), _dtype_code(out.dtype),
-                       0, 0.0, _addr(status, "status", torch.int32), None, 0)
-    rc = (_lib or load_library()).gdn_attn_prefill(
-        ctypes.byref(desc), _addr(q, "q"), _addr(k, "k", q.dtype, (T, Hk, D)),
-        _addr(v, "v", q.dtype, (T, Hk, D)), _addr(cu_seqlens, "cu_seqlens", torch.int32),
-        0.0 if scale is None else scale, _addr(out, "out", out_dtype, (T, H, D)),
-        _addr(lse, "lse", torch.float32, (T, H)), _stream_of(stream, q))
-    if rc != 0:
-        raise GdnError(rc, "gdn_attn_prefill")
-    return (out, lse) if return_lse else out
+    return (_attn_module or _attn()).prefill(
+        q, k, v, cu_seqlens, scale, out_dtype, out, return_lse, lse, status,
+        None if stream is None else stream.cuda_stream)
 
 
 def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -644,36 +586,6 @@ def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     shared_len tokens (a multiple of page_size) are the same pages for every sequence and are
     read once for all. `workspace` (uint8, gdn_attn_workspace_size bytes) is allocated when
     not given. Returns out with q's shape, or (out, lse) when return_lse."""
-    N, H, D = q.shape[0], q.shape[-2], q.shape[-1]
-    nq = 1 if q.dim() == 3 else q.shape[1]
-    n_pages, Hk, page, _ = k_cache.shape
-    if out is None:
-        out = torch.empty(q.shape, dtype=out_dtype or q.dtype, device=q.device)
-    if return_lse and lse is None:
-        lse = torch.empty(q.shape[:-1], dtype=torch.float32, device=q.device)
-    desc = GdnAttnDesc(N * nq, N, H, Hk, D, page, n_pages, page_table.shape[1], 0, 0,
-                       _dtype_code(q.dtype), _dtype_code(out.dtype), 0, 0.0,
-                       _addr(status, "status", torch.int32), None, 0)
-    lib = _lib or load_library()
-    if workspace is None:
-        key = (N, nq, H, Hk, D, q.device.index)
-        n = _decode_workspace.get(key)
-        if n is None:
-            n = lib.gdn_attn_workspace_size(ctypes.byref(desc))
-            if n == 0:
-                raise GdnError(lib.gdn_attn_check_desc(ctypes.byref(desc)), "gdn_attn_decode")
-            _decode_workspace[key] = n
-        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
-    desc.workspace = _addr(workspace, "workspace")
-    desc.workspace_bytes = workspace.numel() * workspace.element_size()
-    cache_shape = (n_pages, Hk, page, D)
-    rc = lib.gdn_attn_decode(
-        ctypes.byref(desc), _addr(q, "q"), _addr(k_cache, "k_cache", q.dtype, cache_shape),
-        _addr(v_cache, "v_cache", q.dtype, cache_shape),
-        _addr(page_table, "page_table", torch.int32, (N, page_table.shape[1])),
-        _addr(kv_lens, "kv_lens", torch.int32, (N,)), shared_len, 0.0 if scale is None else scale,
-        _addr(out, "out", out_dtype, q.shape), _addr(lse, "lse", torch.float32, q.shape[:-1]),
-        _stream_of(stream, q))
-    if rc != 0:
-        raise GdnError(rc, "gdn_attn_decode")
-    return (out, lse) if return_lse else out
+    return (_attn_module or _attn()).decode(
+        q, k_cache, v_cache, page_table, kv_lens, shared_len, scale, out_dtype, out, return_lse,
+        lse, workspace, status, None if stream is None else stream.cuda_stream)

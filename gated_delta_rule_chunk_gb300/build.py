@@ -15,6 +15,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(PKG, "csrc")
@@ -34,6 +35,11 @@ def nvcc() -> str:
         if cand and os.path.exists(cand):
             return cand
     raise RuntimeError("nvcc not found: the CUDA toolkit is required to build libgdn")
+
+
+# The attention calls' marshalling (csrc/attn_torch.cpp), a CPython module over torch's C++ API.
+MODULE = os.path.join(PKG, "_attn_torch.so")
+MODULE_SRC = os.path.join(CSRC, "attn_torch.cpp")
 
 
 def _sources():
@@ -63,16 +69,49 @@ def _compile(src: str, debug: bool = False) -> tuple[str, str]:
     return obj, r.stdout + r.stderr
 
 
+def module_up_to_date() -> bool:
+    if not os.path.exists(MODULE):
+        return False
+    deps = [MODULE_SRC, os.path.join(PKG, "..", "include", "gdn.h"),
+            os.path.join(PKG, "..", "include", "gdn_attn.h"), os.path.abspath(__file__)]
+    t = os.path.getmtime(MODULE)
+    return all(os.path.getmtime(p) <= t for p in deps)
+
+
+def build_module() -> str:
+    """Compile _attn_torch.so with the host compiler. Returns its path."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    tmp = MODULE + ".tmp"
+    cmd = [os.environ.get("CXX", "g++"), "-O2", "-std=c++17", "-fPIC", "-shared",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+           f"-I{root}/include", f"-I{root}/include/torch/csrc/api/include", f"-I{cuda}/include",
+           f"-I{sysconfig.get_paths()['include']}", MODULE_SRC, "-o", tmp, f"-L{root}/lib",
+           "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch", "-ltorch_python"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"g++ failed for {MODULE_SRC}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, MODULE)
+    return MODULE
+
+
 def build(force: bool = False, verbose: bool = False, debug: bool = False) -> str:
-    """Compile libgdn.so (libgdn_debug.so with debug=True) unless it is newer than every
-    source. Returns its path."""
+    """Compile libgdn.so (libgdn_debug.so with debug=True), and beside it _attn_torch.so,
+    unless they are newer than their sources. Returns the library's path."""
     lib, bdir = (LIB_DEBUG, BUILD_DEBUG) if debug else (LIB, BUILD)
+    module = not debug and (force or not module_up_to_date())
     if not force and up_to_date(lib):
+        if module:
+            build_module()
         return lib
     os.makedirs(bdir, exist_ok=True)
     srcs = _sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs), os.cpu_count() or 4)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
+        pending = ex.submit(build_module) if module else None
         results = list(ex.map(lambda src: _compile(src, debug), srcs))
+        if pending:
+            pending.result()
     with open(os.path.join(bdir, "ptxas.log"), "w") as f:
         for (obj, log), src in zip(results, srcs):
             f.write(f"==== {os.path.basename(src)}\n{log}\n")
