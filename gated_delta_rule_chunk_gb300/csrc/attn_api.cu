@@ -140,7 +140,7 @@ int gdn_attn_decode(const gdn_attn_desc* desc, const void* q, const void* k_cach
     return GDN_ERR_BAD_SHAPE;
   if ((int64_t)(d.T / d.N) * (d.H / d.Hk) > 64) return GDN_ERR_UNSUPPORTED;
   // 64-key units of all pairs are counted in 31 bits
-  if ((int64_t)d.N * d.Hk * ((int64_t)d.max_pages * d.page_size / 64 + 1) >= ((int64_t)1 << 31))
+  if ((int64_t)d.N * d.Hk * ((int64_t)d.max_pages * d.page_size / 64 + 4) >= ((int64_t)1 << 31))
     return GDN_ERR_BAD_SHAPE;
   const void* ptrs16[] = {q, k_cache, v_cache, out};
   for (const void* p : ptrs16)

@@ -26,6 +26,11 @@ namespace gdn {
 namespace {
 
 constexpr int kUnit = 64;   // keys of a unit
+// Units that a pair counts for beside its keys', for its queries, merge and results: without
+// them the CTAs that get many short sequences end last (64 sequences of up to 8192 keys
+// 155.4 us, with one 150.2, two 148.5, three 149.3; of up to 1024 behind a prefix 67.2, 61.3,
+// 60.7, 59.7; the price: one sequence of 8191 keys 12.3 -> 12.9, as some CTAs get less).
+constexpr int kPair = 2;
 constexpr int kBlk = 16;    // keys of a warp's block
 constexpr int kWarps = 4;
 
@@ -41,8 +46,10 @@ struct DecodeParts {
   PrefixParts prefix;
 };
 
+// Units of each of sequence n's pairs: its keys' and, before them, kPair for the pair itself.
 __device__ __forceinline__ int chunks_of(const AttnParams& p, int n) {
-  return (max(seq_len(p, n) - p.shared, 0) + kUnit - 1) / kUnit;
+  const int keys = seq_len(p, n) - p.shared;
+  return keys > 0 ? kPair + (keys + kUnit - 1) / kUnit : 0;
 }
 // Equal parts of U units for `grid` CTAs (at most one a unit): CTA c's first unit, and the
 // CTA of unit u. The parts that are one unit longer are spread evenly: with the first CTAs
@@ -56,16 +63,23 @@ __device__ __forceinline__ int cta_of(int u, int U, int grid) {
   return (int)((((int64_t)u + 1) * grid - 1) / U);
 }
 
-// A place in the unit list.
+// A place in the unit list: unit u, `chunk` of a pair's. The units that stand for the pair
+// itself are passed over.
 struct Cursor {
-  int n, hk, chunk, chunks, len;
+  int u, n, hk, chunk, chunks, len;
   __device__ void load(const AttnParams& p) {
     len = seq_len(p, n);
     chunks = chunks_of(p, n);
   }
+  __device__ void settle() {
+    u += max(kPair - chunk, 0);
+    chunk = max(chunk, kPair);
+  }
   __device__ void next(const AttnParams& p) {
+    ++u;
     if (++chunk < chunks) return;
     chunk = 0;
+    settle();
     if (++hk < p.Hk) return;
     hk = 0;
     do {
@@ -76,6 +90,7 @@ struct Cursor {
       load(p);
     } while (chunks == 0);
   }
+  __device__ int key() const { return (chunk - kPair) * kUnit; }  // first key, past the prefix
 };
 
 template <int D>
@@ -146,28 +161,32 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (scribe && lane == 0) w.first[p.N] = U;
-  if (u0 >= u1) {
+  if (u0 < u1) {
+    cur.u = u0;
+    cur.load(p);
+    cur.settle();
+  }
+  if (u0 >= u1 || cur.u >= u1) {
     pdl_wait();
     return;
   }
-  cur.load(p);
   Cursor ahead = cur;  // what is loaded next
 
   // ---- loads: this warp's block of unit `ahead`, into ring place `st`
   const uint32_t ring = smem_u32(smem) + warp * kSt * S::kStage;
   auto page_of = [&]() -> int {
-    const int key = p.shared + ahead.chunk * kUnit + warp * kBlk;
+    const int key = p.shared + ahead.key() + warp * kBlk;
     if (key >= ahead.len) return -1;
     return p.table[(size_t)(key < p.common ? 0 : ahead.n) * p.max_pages + (key >> p.page_shift)];
   };
-  int page = page_of(), u_ahead = u0;
+  int page = page_of();
   // Keys and values are read once, so they leave L2 first: what stays is what is read again,
   // above all the prefix's parts (with 64 sequences behind a prefix, 73.7 -> 65.7 us).
   uint64_t once;
   asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(once));
   auto load_next = [&](int st) {
-    if (u_ahead < u1) {
-      const int key = p.shared + ahead.chunk * kUnit + warp * kBlk;
+    if (ahead.u < u1) {
+      const int key = p.shared + ahead.key() + warp * kBlk;
       if (key < ahead.len) {
         const bool ok = page >= 0 && page < p.n_pages;
         if (!ok && lane == 0) set_status(p.status, GDN_DEV_BAD_PAGE_TABLE);
@@ -189,9 +208,8 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
                        "l"(n ? v + x * 16 : reinterpret_cast<const char*>(p.v)), "r"(n), "l"(once));
         }
       }
-      ++u_ahead;
       ahead.next(p);
-      if (u_ahead < u1) page = page_of();  // used a step later
+      if (ahead.u < u1) page = page_of();  // used a step later
     }
     cp_async_commit();
   };
@@ -232,7 +250,7 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
   bool seg_first = true;      // the pair's part begins at the CTA's first unit
   int st = 0;
 
-  for (int u = u0; u < u1; ++u) {
+  while (cur.u < u1) {
     load_next((st + kSt - 1) % kSt);
     cp_async_wait<kSt - 1>();
     if constexpr (WM == 1) __syncwarp();
@@ -240,7 +258,7 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
 #pragma unroll 1
     for (int b = 0; b < WM; ++b) {
       const int blk = kg * WM + b;
-      const int key0 = p.shared + cur.chunk * kUnit + blk * kBlk;
+      const int key0 = p.shared + cur.key() + blk * kBlk;
       if (key0 >= cur.len) break;
       const uint32_t kb = smem_u32(smem) + (blk * kSt + st) * S::kStage;
       const uint32_t vb = kb + kBlk * S::kRow;
@@ -334,11 +352,11 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
 
     const Cursor was = cur;
     cur.next(p);
-    if (u + 1 < u1 && cur.n == was.n && cur.hk == was.hk) continue;
+    if (cur.u < u1 && cur.n == was.n && cur.hk == was.hk) continue;
 
     // ---- the end of a pair's part: merge the key groups, finish or hand over
-    if (u + 1 < u1) load_q();  // the next pair's queries arrive meanwhile
-    const bool whole = seg_chunk == 0 && was.chunk == was.chunks - 1;
+    if (cur.u < u1) load_q();  // the next pair's queries arrive meanwhile
+    const bool whole = seg_chunk == kPair && was.chunk == was.chunks - 1;
     const int place = 2 * blockIdx.x + (seg_first ? 0 : 1);
     float2* ml = reinterpret_cast<float2*>(smem + S::kMl);  // [WK][16 WM]
 #pragma unroll
@@ -431,7 +449,7 @@ __global__ void __launch_bounds__(W * 32) combine_kernel(const AttnParams p, con
   const int grid = min(w.grid, U);
   int c0 = 0, parts = 0;
   if (c > 0) {
-    c0 = cta_of(ub, U, grid);
+    c0 = cta_of(ub + kPair, U, grid);
     parts = cta_of(ub + c - 1, U, grid) - c0 + 1;
   }
   const int splits = p.shared > 0 ? w.prefix.splits : 0;
