@@ -581,3 +581,40 @@ def test_prompt_then_decode_equals_a_longer_prompt():
             got = B.gdn_attn_decode(q1[None], kc, vc, table, kv, out_dtype=F32)[0]
         # both sides round their weights to bf16: twice the oracle's tolerance, |v| < 6
         assert np.abs(np64(got) - want[b:e]).max() <= 2 * REL * 6
+
+
+@pytest.mark.parametrize("document, own", [(512, 37), (200, 5), (64, 1)])
+def test_example_layer(document, own):
+    """The example's serving loop against its one-prompt form; both sides round their weights
+    to bf16: twice the oracle's tolerance, |v| < 6."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples",
+                        "attention_layer.py")
+    spec = importlib.util.spec_from_file_location("attention_layer", path)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    assert m.main(document=document, own=own) <= 2 * REL * 6
+
+
+def test_outputs_and_workspace_stay_in_their_bounds():
+    """Outputs lie between guard rows that no call touches."""
+    g = torch.Generator().manual_seed(12)
+    H, Hk, D, T = 6, 2, 64, 77
+    buf = torch.full((T + 8, H, D), 3.0, dtype=BF, device="cuda")
+    q, k, v = (randn(g, T, h, D).cuda() for h in (H, Hk, Hk))
+    B.gdn_attn_prefill(q, k, v, out=buf[4:-4])
+    assert (buf[:4] == 3.0).all() and (buf[-4:] == 3.0).all()
+    kc, vc, table = (x.cuda() for x in make_cache(g, [90, 33], Hk, D, 16, fill=0.0))
+    kv = torch.tensor([90, 33], dtype=torch.int32, device="cuda")
+    out = torch.full((10, H, D), 3.0, dtype=BF, device="cuda")
+    n = B.gdn_attn_workspace_size(B.make_attn_desc(2, 2, H, Hk, D, page_size=16, n_pages=kc.shape[0],
+                                                   max_pages=table.shape[1]))
+    work = torch.full((n + 8192,), 7, dtype=torch.uint8, device="cuda")
+    for shared in (0, 16):
+        t = table.clone()
+        t[:, :shared // 16] = t[0, :shared // 16]
+        B.gdn_attn_decode(q[:2].contiguous(), kc, vc, t, kv, shared, out=out[4:6],
+                          workspace=work[4096:4096 + n])
+        assert (out[:4] == 3.0).all() and (out[6:] == 3.0).all()
+        assert (work[:4096] == 7).all() and (work[4096 + n:] == 7).all()
