@@ -39,7 +39,7 @@ EXPORTED = ("gdn_check_desc", "gdn_nt_max", "gdn_workspace_size", "gdn_build_chu
             "gdn_debug_build", "gdn_test_debug_poison",
             "gdn_recurrent_fwd", "gdn_conv_front", "gdn_bwd_workspace_size", "gdn_chunk_bwd",
             "gdn_attn_check_desc", "gdn_attn_workspace_size", "gdn_attn_front",
-            "gdn_attn_prefill", "gdn_attn_decode")
+            "gdn_attn_prefill", "gdn_attn_decode", "gdn_test_attn_prefix")
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
 GDN_ATTN_ROPE_INTERLEAVED = 1
 
@@ -126,6 +126,8 @@ def load_library(path: str = LIB_PATH):
         lib.gdn_attn_workspace_size.restype = ctypes.c_size_t
         lib.gdn_attn_front.argtypes = [P(GdnAttnDesc)] + [vp] * 13
         lib.gdn_attn_front.restype = ctypes.c_int
+        lib.gdn_test_attn_prefix.argtypes = [i32]
+        lib.gdn_test_attn_prefix.restype = None
         lib.gdn_attn_prefill.argtypes = [P(GdnAttnDesc), vp, vp, vp, vp, ctypes.c_float, vp, vp,
                                          vp]
         lib.gdn_attn_prefill.restype = ctypes.c_int
@@ -589,3 +591,8 @@ def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     return (_attn_module or _attn()).decode(
         q, k_cache, v_cache, page_table, kv_lens, shared_len, scale, out_dtype, out, return_lse,
         lse, workspace, status, None if stream is None else stream.cuda_stream)
+
+
+def gdn_test_attn_prefix(always: bool) -> None:
+    """Testing hook: gdn_attn_decode gives a common prefix its own pass at every size."""
+    load_library().gdn_test_attn_prefix(1 if always else 0)

@@ -2,9 +2,18 @@
 // validation and launches. No allocation, no synchronization, no device reads.
 #include <math.h>
 
+#include <atomic>
+
 #include "attn_common.cuh"
 
 using namespace gdn;
+
+namespace gdn {
+
+static std::atomic<bool> g_prefix_always{false};
+bool attn_prefix_always() { return g_prefix_always.load(std::memory_order_relaxed); }
+
+}  // namespace gdn
 
 namespace {
 
@@ -59,6 +68,10 @@ AttnParams attn_params(const gdn_attn_desc& d, const void* q, const void* k, con
 }  // namespace
 
 extern "C" {
+
+void gdn_test_attn_prefix(int32_t always) {
+  g_prefix_always.store(always != 0, std::memory_order_relaxed);
+}
 
 int gdn_attn_check_desc(const gdn_attn_desc* desc) { return check_impl(desc); }
 

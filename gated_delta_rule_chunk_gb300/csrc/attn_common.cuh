@@ -46,6 +46,9 @@ struct AttnParams {
   int out_bf16;
 };
 
+// Testing hook (gdn_test_attn_prefix): a common prefix takes its own kernel at every size.
+bool attn_prefix_always();
+
 bool launch_attn_front(const AttnFrontParams& p, cudaStream_t s);
 bool launch_attn_prefill(const AttnParams& p, cudaStream_t s);
 bool launch_attn_decode(const AttnParams& p, void* workspace, cudaStream_t s);

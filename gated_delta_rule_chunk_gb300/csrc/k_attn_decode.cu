@@ -432,17 +432,19 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
   pdl_wait();
 }
 
-// One query row per CTA: the parts of a pair that spans CTAs, merged in the order of the
-// keys; zeros for a row that saw no key. W warps take every W-th part.
+// The parts of a pair that spans CTAs, merged in the order of the keys; zeros for a row that
+// saw no key. W warps a row take every W-th part; a CTA has W warps, or four with a row each.
 template <int D, int W>
-__global__ void __launch_bounds__(W * 32) combine_kernel(const AttnParams p, const DecodeParts w) {
+__global__ void __launch_bounds__(W == 1 ? 128 : W * 32)
+combine_kernel(const AttnParams p, const DecodeParts w) {
   constexpr int E = D / 32;
   __shared__ float sh_o[W][D];
   __shared__ float2 sh_ml[W];
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const size_t at = blockIdx.x;  // (n, i, h)
-  const int h = (int)(at % p.H), t = (int)(at / p.H), n = t / p.nq, hk = h / p.G;
-  const int R = p.nq * p.G, r = (t % p.nq) * p.G + h % p.G;
+  const int warp = W == 1 ? 0 : threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t at = W == 1 ? blockIdx.x * 4 + (threadIdx.x >> 5) : blockIdx.x;  // (n, i, h)
+  if (at >= (uint32_t)(p.T * p.H)) return;
+  const int t = (int)(at / (uint32_t)p.H), h = (int)at - t * p.H, n = t / p.nq, hk = h / p.G;
+  const int R = p.nq * p.G, r = (t - n * p.nq) * p.G + h - hk * p.G;
   pdl_wait();
   const int U = w.first[p.N], b = w.first[n], c = (w.first[n + 1] - b) / p.Hk;
   const int ub = b + hk * c;  // the pair's units [ub, ub + c)
@@ -513,24 +515,26 @@ __global__ void __launch_bounds__(W * 32) combine_kernel(const AttnParams p, con
       for (int e = 0; e < E; ++e) o[e] = add ? o[e] + v[e] * wi : o[e];
     }
   }
-  if (lane == 0) sh_ml[warp] = make_float2(m, l);
+  if constexpr (W > 1) {
+    if (lane == 0) sh_ml[warp] = make_float2(m, l);
 #pragma unroll
-  for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
-  __syncthreads();
-  if (warp != 0) return;
-  m = sh_ml[0].x;
+    for (int e = 0; e < E; ++e) sh_o[warp][lane * E + e] = o[e];
+    __syncthreads();
+    if (warp != 0) return;
+    m = sh_ml[0].x;
 #pragma unroll
-  for (int i = 1; i < W; ++i) m = fmaxf(m, sh_ml[i].x);
-  l = 0.f;
+    for (int i = 1; i < W; ++i) m = fmaxf(m, sh_ml[i].x);
+    l = 0.f;
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
+    for (int e = 0; e < E; ++e) o[e] = 0.f;
 #pragma unroll
-  for (int i = 0; i < W; ++i) {
-    if (sh_ml[i].y == 0.f) continue;
-    const float f = sh_ml[i].x == m ? 1.f : ex2(sh_ml[i].x - m);
-    l += sh_ml[i].y * f;
+    for (int i = 0; i < W; ++i) {
+      if (sh_ml[i].y == 0.f) continue;
+      const float f = sh_ml[i].x == m ? 1.f : ex2(sh_ml[i].x - m);
+      l += sh_ml[i].y * f;
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] += sh_o[i][lane * E + e] * f;
+      for (int e = 0; e < E; ++e) o[e] += sh_o[i][lane * E + e] * f;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
@@ -598,23 +602,31 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   w.prefix.ml = reinterpret_cast<float2*>(ws + L.prefix_ml);
   w.prefix.tiles = (p.common + kKeys - 1) / kKeys;
   w.prefix.splits = L.splits < w.prefix.tiles ? L.splits : w.prefix.tiles;
-  p.shared = p.N > 1 && p.n_pages > 0 ? p.common : 0;
+  // The prefix kernel and the merge of its parts cost about 5 us; without them every sequence
+  // reads the prefix's keys itself, mostly from L2, and with many query rows also multiplies
+  // them in WM row tiles at warp-MMA speed. Measured (GB300; bytes read again, with / without):
+  // 32 MB 16.9 / 12.8 us, 59 MB 18.0 / 15.9, 66 MB 25.8 / 21.6, 126 MB 18.6 / 21.7, 235 MB
+  // 20.9 / 33.8; with 40 rows a pair 33 MB 29.3 / 32.2.
+  const int R = p.nq * p.G, WM = R <= 16 ? 1 : R <= 32 ? 2 : 4;
+  const int64_t again = (int64_t)(p.N - 1) * p.common * p.Hk * D * 4 * WM;
+  p.shared = p.n_pages > 0 && p.N > 1 && (again >= (int64_t)80 << 20 || attn_prefix_always())
+                 ? p.common : 0;
   if (p.shared > 0 && !launch_prefix<D>(p, w.prefix, s)) return false;
   // no more CTAs than units there can be
   const int64_t most = (int64_t)p.N * p.Hk * (((int64_t)p.max_pages * p.page + kUnit - 1) / kUnit);
   w.grid = (int)(most < L.grid ? (most > 0 ? most : 1) : L.grid);
-  const int R = p.nq * p.G;
   const auto kernel = R <= 16 ? decode_kernel<D, 1> : R <= 32 ? decode_kernel<D, 2> : decode_kernel<D, 4>;
   constexpr int smem = DecodeSmem<D>::kBytes;
   ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
-  const size_t rows = (size_t)p.T * p.H;
-  // Few rows have many parts each (one sequence of 8191 keys: 77 a row): eight warps a row
-  // while all CTAs fit the GPU at once (13.4 -> 12.5 us), else four (2048 rows: 157.0 us for
-  // the call, with eight 159.6 us).
-  const bool few = rows <= 8 * (size_t)num_sms();
-  const auto combine = few ? combine_kernel<D, 8> : combine_kernel<D, 4>;
+  // Warps of a merged row: eight while all their CTAs fit the GPU at once (a row has many
+  // parts then: one sequence of 8191 keys 13.4 us with four, 12.5 with eight), four up to as
+  // many rows as those fit, one beyond.
+  const size_t rows = (size_t)p.T * p.H, sms = (size_t)num_sms();
+  const int W = rows <= 8 * sms ? 8 : rows <= 32 * sms ? 4 : 1;
+  const auto combine = W == 8 ? combine_kernel<D, 8> : W == 4 ? combine_kernel<D, 4> : combine_kernel<D, 1>;
   return launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w) == cudaSuccess &&
-         launch_pdl(combine, dim3((unsigned)rows), dim3(few ? 256 : 128), 0, s, p, w) == cudaSuccess;
+         launch_pdl(combine, dim3((unsigned)(W == 1 ? (rows + 3) / 4 : rows)), dim3(W == 8 ? 256 : 128), 0,
+                    s, p, w) == cudaSuccess;
 }
 
 }  // namespace

@@ -145,7 +145,7 @@ int gdn_attn_prefill(const gdn_attn_desc* desc, const void* q, const void* k, co
  *                length 0 (padding) gets zeros
  *   shared_len   the first shared_len tokens of every sequence are the same pages (a
  *                multiple of page_size; their columns are read from page_table's first row
- *                only); 0: none. A sequence may be shorter than shared_len.
+ *                only), which are read once for all where that pays; 0: none. A sequence may be shorter than shared_len.
  *   scale, out, lse  as for gdn_attn_prefill ([N, n_q, H, D], [N, n_q, H])
  * A length outside [0, max_pages * page_size] is clamped (GDN_DEV_BAD_LENGTH); keys and
  * values of a page outside [0, n_pages) read as zeros (GDN_DEV_BAD_PAGE_TABLE). Rows of the
@@ -154,6 +154,13 @@ int gdn_attn_prefill(const gdn_attn_desc* desc, const void* q, const void* k, co
 int gdn_attn_decode(const gdn_attn_desc* desc, const void* q, const void* k_cache,
                     const void* v_cache, const int32_t* page_table, const int32_t* kv_lens,
                     int32_t shared_len, float scale, void* out, float* lse, cudaStream_t stream);
+
+/*
+ * Testing hook. gdn_attn_decode gives a common prefix its own pass only where that pays (many
+ * sequences behind a long prefix); with always != 0 it does so at every size in the calls that
+ * follow, so that tests can reach that path with small inputs. 0 (the default) turns it off.
+ */
+void gdn_test_attn_prefix(int32_t always);
 
 #ifdef __cplusplus
 }

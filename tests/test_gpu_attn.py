@@ -219,6 +219,18 @@ def test_prefill_long(H, Hk, D):
 
 
 # ---------------------------------------------------------------- decode
+@pytest.fixture(params=["by rule", "always"])
+def prefix_pass(request):
+    """The shared prefix with its own pass where the library's rule says so (not at most sizes
+    here), and with it at every size."""
+    B.gdn_test_attn_prefix(request.param == "always")
+    yield
+    B.gdn_test_attn_prefix(False)
+
+
+both = pytest.mark.usefixtures("prefix_pass")
+
+
 def make_cache(g, lens, Hk, D, page, shared=0, extra=3, fill=float("nan")):
     """A paged cache in scattered page order whose unused rows hold `fill`; returns
     (k_cache, v_cache, table, n_pages) on the CPU."""
@@ -296,6 +308,29 @@ def test_decode_scale_and_bf16_output():
     check_decode([100, 33], 4, 2, 128, 16, out_dtype=BF)
 
 
+def test_decode_many_rows():
+    """Enough merged rows for one warp each."""
+    check_decode([5 + 7 * i % 60 for i in range(130)] + [700] * 5, 8, 2, 64, 16, nq=5, seed=8)
+
+
+def test_decode_more_units_than_22_bits():
+    """Every sequence reads the same few pages, so that the lengths add up without the memory."""
+    g = torch.Generator().manual_seed(9)
+    N, H, D, page, cols = 4100, 8, 64, 256, 32
+    kc, vc = randn(g, 5, H, page, D), randn(g, 5, H, page, D)
+    table = torch.randint(0, 5, (N, cols), generator=g, dtype=torch.int32)
+    lens = torch.full((N,), cols * page, dtype=torch.int32)
+    lens[::7] -= 3
+    assert N * H * (cols * page // 64 + 2) > 1 << 22
+    q = randn(g, N, H, D)
+    out = B.gdn_attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), lens.cuda(), out_dtype=F32)
+    for n in (0, 1, 2049, N - 1):
+        ref, mag, _ = A.decode(np64(q[n:n + 1, None]), np64(kc), np64(vc), table[n:n + 1].numpy(),
+                               lens[n:n + 1].tolist())
+        close_attention(out[n:n + 1], None, ref, mag, None)
+
+
+@both
 @pytest.mark.parametrize("shared, page", [(16, 16), (128, 16), (112, 16), (384, 128), (256, 256),
                                           (1280, 64)])
 @pytest.mark.parametrize("D", [64, 128])
@@ -303,6 +338,7 @@ def test_decode_shared_prefix(shared, page, D):
     check_decode([shared + x for x in (1, 0, 40, 17, 300)], 8, 2, D, page, shared=shared, seed=shared)
 
 
+@both
 @pytest.mark.parametrize("N, H, Hk, nq", [(70, 8, 2, 1), (33, 5, 1, 3), (3, 64, 1, 1), (9, 21, 3, 8),
                                           (1, 4, 1, 1), (130, 1, 1, 1)])
 def test_decode_shared_prefix_rows(N, H, Hk, nq):
@@ -310,21 +346,25 @@ def test_decode_shared_prefix_rows(N, H, Hk, nq):
     check_decode([320 + 5 + 7 * i % 90 for i in range(N)], H, Hk, 64, 32, nq=nq, shared=320, seed=N)
 
 
+@both
 def test_decode_sequences_shorter_than_the_prefix():
     check_decode([200, 64, 0, 1, 320, 319, 257], 4, 2, 128, 64, shared=320, seed=4)
     check_decode([2, 64, 0, 1, 320, 65], 4, 2, 128, 64, nq=3, shared=320, seed=4)
 
 
+@both
 def test_decode_long_shared_prefix():
     check_decode([8192 + 1 + i for i in range(20)], 16, 2, 128, 64, shared=8192, seed=5)
 
 
+@both
 def test_decode_shared_equals_unshared():
     """The same batch with and without the hint, each within its tolerance of the oracle."""
     for shared in (0, 512):
         check_decode([512 + 3 * i for i in range(12)], 8, 2, 128, 32, shared=shared, seed=6)
 
 
+@both
 @pytest.mark.parametrize("what", ["nan", "inf", "lowest"])
 @pytest.mark.parametrize("shared", [0, 128, 160])
 def test_decode_unseen_values_have_no_influence(what, shared):
@@ -357,6 +397,7 @@ def test_decode_unseen_values_have_no_influence(what, shared):
                     mag.reshape(4 * nq, H, D), None, ~hit.reshape(-1))
 
 
+@both
 def test_decode_bad_pages_and_lengths():
     g = torch.Generator().manual_seed(3)
     kc, vc, table = make_cache(g, [100, 90], 2, 64, 16, fill=0.0)
@@ -374,6 +415,7 @@ def test_decode_bad_pages_and_lengths():
         close_attention(out, lse, ref, mag, rl)
 
 
+@both
 def test_decode_cache_past_32_bit_offsets():
     """Pages whose element offsets pass 2^32."""
     Hk, D, page, n_pages = 8, 128, 256, 18000
@@ -397,6 +439,7 @@ def test_decode_cache_past_32_bit_offsets():
         close_attention(out, None, ref, mag, rl)
 
 
+@both
 def test_decode_repeatable_other_stream_and_graph():
     g = torch.Generator().manual_seed(7)
     lens = [900, 3, 400, 1500]
@@ -583,6 +626,7 @@ def test_prompt_then_decode_equals_a_longer_prompt():
         assert np.abs(np64(got) - want[b:e]).max() <= 2 * REL * 6
 
 
+@both
 @pytest.mark.parametrize("document, own", [(512, 37), (200, 5), (64, 1)])
 def test_example_layer(document, own):
     """The example's serving loop against its one-prompt form; both sides round their weights
@@ -597,6 +641,7 @@ def test_example_layer(document, own):
     assert m.main(document=document, own=own) <= 2 * REL * 6
 
 
+@both
 def test_outputs_and_workspace_stay_in_their_bounds():
     """Outputs lie between guard rows that no call touches."""
     g = torch.Generator().manual_seed(12)
