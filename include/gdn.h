@@ -1,6 +1,7 @@
 /*
  * gdn.h -- C ABI of libgdn: the chunked gated-delta-rule prefill forward
- * on one NVIDIA GB300 (sm_103a).
+ * on one NVIDIA GB300 (sm_103a). The softmax-attention layers that stand
+ * between gated-delta-rule layers are in gdn_attn.h.
  *
  * The operation (per sequence n, value head hv, key head h = hv / (Hv / H);
  * the per-head fp32 state S has one row per key dimension):

@@ -130,7 +130,7 @@ int gdn_attn_front(const gdn_attn_desc* desc, const void* x, const float* q_weig
  *   out          [T, H, D] in out_dtype; rows outside every sequence are not written
  *   lse          [T, H] fp32 or NULL
  * Entries of a malformed cu_seqlens are clamped to [0, T] and raised to the largest entry
- * before them (GDN_DEV_BAD_CU_SEQLENS). What a row does not see has no influence on it,
+ * before them (GDN_DEV_BAD_CU_SEQLENS; past 1024 sequences, to the largest of their 1024). What a row does not see has no influence on it,
  * infinities and NaN included.
  */
 int gdn_attn_prefill(const gdn_attn_desc* desc, const void* q, const void* k, const void* v,

@@ -91,6 +91,11 @@ def test_prefill_packed(lens, D):
     check_prefill(lens, 4, 2, D, seed=len(lens), lead=3, tail=9)
 
 
+def test_prefill_many_sequences():
+    """More sequences than one launch takes, empty ones among them."""
+    check_prefill([1 + 13 * i % 9 if i % 5 else 0 for i in range(1100)] + [140, 0, 3], 2, 1, 64, seed=7)
+
+
 @pytest.mark.parametrize("mul", [0.01, 4.0, 8.0])
 def test_prefill_score_ranges(mul):
     """Nearly uniform weights, and weights of a few keys whose maximum grows along the row."""
