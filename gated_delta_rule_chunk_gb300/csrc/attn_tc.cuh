@@ -925,11 +925,13 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         char* tile = smem + S::kRing + st * S::kTile;
         // rows of this tile inside the sequence, the prefix
         const int rows = (kPrefix ? p.shared : it.len) - (it.kv0 + j) * kKeys;
+        // Prompts: keys up to the first row's own are seen by all rows of the item and stay as
+        // they are. (A prefix's rows may end anywhere.) Rolled loops: unrolled, the code that
+        // is fetched for every item costs more than they save (8 ragged prompts 64.6 against
+        // 62.2 us).
+        const int seen = kPrefix ? 0 : max(it.tok + 1 - j * kKeys, 0);
         bool found = false;
-#pragma unroll 4
-        for (int i = tid; i < S::kTile / 16; i += 128) {
-          uint4* v = reinterpret_cast<uint4*>(tile) + i;
-          const int row = kPrefix ? i / D * 8 + ((i >> 3) & 7) : (i >> 3) & 127;
+        auto look = [&](uint4* v, int row) {
           if (row >= rows) {
             *v = make_uint4(0, 0, 0, 0);
           } else {
@@ -939,6 +941,17 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
                                ((x.z & 0x7F807F80u) + 0x00800080u) |
                                ((x.w & 0x7F807F80u) + 0x00800080u);
             found |= (e & 0x80008000u) != 0;
+          }
+        };
+        uint4* v = reinterpret_cast<uint4*>(tile);
+        if constexpr (kPrefix) {
+#pragma unroll 1
+          for (int i = tid; i < S::kTile / 16; i += 128) look(v + i, i / D * 8 + ((i >> 3) & 7));
+        } else {
+#pragma unroll 1
+          for (int i = seen * 8 + tid; i < kKeys * 8; i += 128) {
+#pragma unroll
+            for (int h = 0; h < D / 64; ++h) look(v + h * kKeys * 8 + i, i >> 3);
           }
         }
         if (found) *reinterpret_cast<volatile int*>(&B.poison[k & 7]) = (int)k + 1;
