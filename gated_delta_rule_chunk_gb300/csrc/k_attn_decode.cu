@@ -456,63 +456,61 @@ combine_kernel(const AttnParams p, const DecodeParts w) {
   }
   const int splits = p.shared > 0 ? w.prefix.splits : 0;
   if (parts == 1 && splits == 0) return;  // finished by its CTA
-  // Part i's row: the prefix's splits, then the pair's parts.
+  // Part i's row: the prefix's splits, then the pair's parts. Only its first CTA can have begun
+  // with another pair, so that the pair's part is the CTA's second.
+  const int second = c > 0 && unit_of(c0, U, grid) < ub;
   auto row_of = [&](int i, const float2*& ml) -> const float* {
+    const float* o;
     size_t row;
     if (i < splits) {
       row = (size_t)i * p.T * p.H + at;
-      ml = w.prefix.ml + row;
-      return w.prefix.o + row * D;
-    }
-    if (parts == 1) {
+      o = w.prefix.o;
+      ml = w.prefix.ml;
+    } else if (parts == 1) {
       row = (size_t)(n * p.Hk + hk) * R + r;
-      ml = w.own_ml + row;
-      return w.own + row * D;
+      o = w.own;
+      ml = w.own_ml;
+    } else {
+      const int j = i - splits;
+      row = (size_t)(2 * (c0 + j) + (j == 0 ? second : 0)) * R + r;
+      o = w.part;
+      ml = w.part_ml;
     }
-    const int cta = c0 + i - splits;
-    row = (size_t)(2 * cta + (unit_of(cta, U, grid) < ub ? 1 : 0)) * R + r;
-    ml = w.part_ml + row;
-    return w.part + row * D;
+    ml += row;
+    return o + row * D;
   };
-  // 32 parts at a time: a lane each for the references and
-  // denominators, so that the rows' loads wait for nothing and run side by side.
+  // A warp takes every W-th part, kAtOnce of them loaded side by side (the row with its
+  // reference and denominator, which all lanes read) before the first is used: what counts is
+  // the number of round trips to L2 (one sequence of 8191 keys, eight warps, the whole call:
+  // 4 at once 13.9 us, 6 12.5, 8 11.5, 10 10.4, 12 10.5).
+  constexpr int kAtOnce = W == 8 ? 10 : 6;
   float m = -INFINITY, l = 0.f, o[E] = {};
-  for (int i0 = warp; i0 < splits + parts; i0 += 32 * W) {
-    const int mine = i0 + W * lane;
-    float2 ml = make_float2(-INFINITY, 0.f);
-    const float* po = nullptr;
-    if (mine < splits + parts) {
-      const float2* q;
-      po = row_of(mine, q);
-      ml = *q;
+#pragma unroll 1
+  for (int i0 = warp; i0 < splits + parts; i0 += kAtOnce * W) {
+    float2 ml[kAtOnce];
+    float v[kAtOnce][E];
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
+      ml[x] = make_float2(-INFINITY, 0.f);
+      if (i0 + x * W < splits + parts) {
+        const float2* q;
+        const float* y = row_of(i0 + x * W, q);
+        ml[x] = *q;
+        if constexpr (E == 4)
+          *reinterpret_cast<float4*>(v[x]) = *reinterpret_cast<const float4*>(y + lane * E);
+        else
+          *reinterpret_cast<float2*>(v[x]) = *reinterpret_cast<const float2*>(y + lane * E);
+      }
     }
-    const bool seen = ml.y != 0.f;  // the row saw a key of this part (NaN is kept)
-    float mn = seen ? ml.x : -INFINITY;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, x));
-    mn = fmaxf(mn, m);
-    const float f = m == mn ? 1.f : ex2(m - mn), fi = !seen ? 0.f : ml.x == mn ? 1.f : ex2(ml.x - mn);
-    m = mn;
-    float li = seen ? ml.y * fi : 0.f;
+    for (int x = 0; x < kAtOnce; ++x) {
+      if (ml[x].y == 0.f) continue;  // the row saw no key of this part (NaN is kept)
+      const float mn = fmaxf(m, ml[x].x);
+      const float f = m == mn ? 1.f : ex2(m - mn), fi = ml[x].x == mn ? 1.f : ex2(ml[x].x - mn);
+      m = mn;
+      l = l * f + ml[x].y * fi;
 #pragma unroll
-    for (int x = 16; x > 0; x >>= 1) li += __shfl_xor_sync(0xffffffffu, li, x);
-    l = l * f + li;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= f;
-    const int cnt = min(32, (splits + parts - i0 + W - 1) / W);
-#pragma unroll (W == 8 ? 8 : 4)
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, fi, i);
-      const float* y = reinterpret_cast<const float*>(
-          __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(po), i));
-      const bool add = __shfl_sync(0xffffffffu, seen, i);
-      float v[E];
-      if constexpr (E == 4)
-        *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(y + lane * E);
-      else
-        *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(y + lane * E);
-#pragma unroll
-      for (int e = 0; e < E; ++e) o[e] = add ? o[e] + v[e] * wi : o[e];
+      for (int e = 0; e < E; ++e) o[e] = o[e] * f + v[x][e] * fi;
     }
   }
   if constexpr (W > 1) {
@@ -619,8 +617,9 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   constexpr int smem = DecodeSmem<D>::kBytes;
   ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
   // Warps of a merged row: eight while all their CTAs fit the GPU at once (a row has many
-  // parts then: one sequence of 8191 keys 13.4 us with four, 12.5 with eight), four up to as
-  // many rows as those fit, one beyond.
+  // parts then: one sequence of 8191 keys 13.4 us with four, 12.5 with eight; 64 sequences,
+  // 2048 rows, 157.0 with four, 159.6 with eight), four up to as many rows as those fit, one
+  // beyond (64 sequences x 5 tokens x 64 heads behind 256 keys 46.7 us with four, 29.2 with one).
   const size_t rows = (size_t)p.T * p.H, sms = (size_t)num_sms();
   const int W = rows <= 8 * sms ? 8 : rows <= 32 * sms ? 4 : 1;
   const auto combine = W == 8 ? combine_kernel<D, 8> : W == 4 ? combine_kernel<D, 4> : combine_kernel<D, 1>;
