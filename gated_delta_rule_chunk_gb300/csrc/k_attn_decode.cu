@@ -46,9 +46,10 @@ struct DecodeParts {
   PrefixParts prefix;
 };
 
-// Units of each of sequence n's pairs: its keys' and, before them, kPair for the pair itself.
-__device__ __forceinline__ int chunks_of(const AttnParams& p, int n) {
-  const int keys = seq_len(p, n) - p.shared;
+// Units of each pair of a sequence of `len` keys: its keys' and, before them, kPair for the
+// pair itself.
+__device__ __forceinline__ int chunks_of(const AttnParams& p, int len) {
+  const int keys = len - p.shared;
   return keys > 0 ? kPair + (keys + kUnit - 1) / kUnit : 0;
 }
 // Equal parts of U units for `grid` CTAs (at most one a unit): CTA c's first unit, and the
@@ -69,7 +70,7 @@ struct Cursor {
   int u, n, hk, chunk, chunks, len;
   __device__ void load(const AttnParams& p) {
     len = seq_len(p, n);
-    chunks = chunks_of(p, n);
+    chunks = chunks_of(p, len);
   }
   __device__ void settle() {
     u += max(kPair - chunk, 0);
@@ -127,9 +128,11 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
   pdl_release();
 
   // ---- the CTA's part of the unit list; each warp looks it up for itself
-  int U = 0;
+  int U = 0, len32 = 0;  // len32: of this lane's sequence among the first 32
   for (int n = lane; n < p.N; n += 32) {
-    U += chunks_of(p, n);
+    const int len = seq_len(p, n);
+    if (n == lane) len32 = len;
+    U += chunks_of(p, len);
     if (blockIdx.x == 0 && (p.kv_lens[n] < 0 || p.kv_lens[n] > (p.max_pages << p.page_shift)))
       set_status(p.status, GDN_DEV_BAD_LENGTH);
   }
@@ -141,7 +144,8 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
   int before = 0;
   for (int n0 = 0; n0 < p.N && (scribe || before * p.Hk <= u0); n0 += 32) {
     const int n = n0 + lane;
-    const int c = n < p.N ? chunks_of(p, n) : 0;
+    const int len = n0 == 0 ? len32 : n < p.N ? seq_len(p, n) : 0;
+    const int c = n < p.N ? chunks_of(p, len) : 0;
     int inc = c;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -157,13 +161,14 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
       cur.n = n0 + src;
       cur.hk = off / ch;
       cur.chunk = off % ch;
+      cur.chunks = ch;
+      cur.len = __shfl_sync(0xffffffffu, len, src);
     }
     before += __shfl_sync(0xffffffffu, inc, 31);
   }
   if (scribe && lane == 0) w.first[p.N] = U;
   if (u0 < u1) {
     cur.u = u0;
-    cur.load(p);
     cur.settle();
   }
   if (u0 >= u1 || cur.u >= u1) {
