@@ -557,7 +557,7 @@ DecodeLayout layout(int T, int N, int H, int Hk, int D) {
   const int G = H / Hk, span = 2 * (kRows / G);
   const size_t R = (size_t)(T / N) * G, rows = (size_t)T * H;
   L.grid = 2 * num_sms();
-  const int64_t pairs = ((int64_t)T + span - 1) / span * Hk;
+  const int64_t pairs = (T > 0 ? ((int64_t)T + span - 1) / span : 1) * Hk;
   L.splits = pairs >= num_sms() ? 1 : (int)(num_sms() / pairs);
   size_t o = 0;
   auto take = [&](size_t bytes) {

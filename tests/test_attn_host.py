@@ -43,6 +43,13 @@ def test_check_desc(lib, kw, want):
         assert B.gdn_attn_workspace_size(desc(**kw)) == 0
 
 
+def test_workspace_of_no_rows(lib):
+    # a decode call without rows is allowed and asks for its workspace like any other
+    for kw in (dict(T=0), dict(T=0, N=1, H=1, Hk=1, D=64), dict(T=0, N=300, H=64, Hk=64)):
+        assert 0 < B.gdn_attn_workspace_size(desc(**kw)) <= B.gdn_attn_workspace_size(
+            desc(**{**kw, "T": desc(**kw).N}))
+
+
 def test_check_desc_null_and_dtype(lib):
     assert lib.gdn_attn_check_desc(None) == -1
     d = desc()

@@ -296,6 +296,15 @@ def test_decode_empty_sequences():
     check_decode([1, 3, 0], 2, 1, 64, 16, nq=4)  # rows before the sequence's start see nothing
 
 
+def test_decode_no_rows():
+    kc = torch.zeros(3, 2, 16, 64, dtype=BF, device="cuda")
+    table, kv = (torch.zeros(n, dtype=torch.int32, device="cuda") for n in ((4, 3), (4,)))
+    status = torch.full((1,), 9, dtype=torch.int32, device="cuda")
+    q = torch.empty(4, 0, 6, 64, dtype=BF, device="cuda")
+    assert B.gdn_attn_decode(q, kc, kc, table, kv, status=status).shape == (4, 0, 6, 64)
+    assert status.item() == 0
+
+
 def test_decode_long_and_uneven():
     """One long axis to split beside many short ones; and a single long sequence."""
     check_decode([9000, 1, 2, 300, 17, 1025], 8, 2, 128, 64, seed=1)
