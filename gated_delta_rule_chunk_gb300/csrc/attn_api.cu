@@ -32,10 +32,10 @@ int check_impl(const gdn_attn_desc* d) {
   const bool dt_ok = (d->in_dtype == GDN_F32 || d->in_dtype == GDN_BF16) &&
                      (d->out_dtype == GDN_F32 || d->out_dtype == GDN_BF16);
   if (!dt_ok || (d->flags & ~(uint32_t)GDN_ATTN_ROPE_INTERLEAVED)) return GDN_ERR_UNSUPPORTED;
-  // Positions and row counts stay within 31 bits, grids within their limits (element offsets
-  // are 64-bit).
+  // Positions (with those of the tile that a sequence ends in) and row counts stay within 31
+  // bits, grids within their limits (element offsets are 64-bit).
   if ((int64_t)d->T * (d->H + 2 * (int64_t)d->Hk) >= ((int64_t)1 << 31) ||
-      (int64_t)d->max_pages * ps >= ((int64_t)1 << 31) ||
+      (int64_t)d->max_pages * ps > ((int64_t)1 << 31) - 4096 ||
       (int64_t)d->n_pages * d->Hk * ps >= ((int64_t)1 << 34) || d->H > 65535 || d->N > 65535 * 16)
     return GDN_ERR_BAD_SHAPE;
   return GDN_OK;

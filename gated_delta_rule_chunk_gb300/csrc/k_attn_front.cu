@@ -83,7 +83,7 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
   // that a lane group's heads take one path.
   const uint32_t heads = p.H + 2 * p.Hk, q_chunks = (p.H + R - 1) / R;
   const uint32_t chunks = q_chunks + (2 * p.Hk + R - 1) / R;
-  const uint32_t item = (blockIdx.x * kThreads + threadIdx.x) / L;
+  const uint32_t item = blockIdx.x * (kThreads / L) + threadIdx.x / L;
   const int lane = threadIdx.x % L;
   const uint32_t ti = item / chunks, chunk = item - ti * chunks;
   bool live = ti < (uint32_t)p.T;

@@ -43,6 +43,14 @@ def test_check_desc(lib, kw, want):
         assert B.gdn_attn_workspace_size(desc(**kw)) == 0
 
 
+def test_positions_stay_within_31_bits(lib):
+    # a tile or copy that a sequence ends in reaches past its last position, before its clamp
+    for page in (16, 32, 64, 128, 256):
+        most = ((1 << 31) - 4096) // page
+        assert B.gdn_attn_check_desc(desc(page_size=page, max_pages=most)) == 0
+        assert B.gdn_attn_check_desc(desc(page_size=page, max_pages=most + 1)) == -2
+
+
 def test_workspace_of_no_rows(lib):
     # a decode call without rows is allowed and asks for its workspace like any other
     for kw in (dict(T=0), dict(T=0, N=1, H=1, Hk=1, D=64), dict(T=0, N=300, H=64, Hk=64)):
