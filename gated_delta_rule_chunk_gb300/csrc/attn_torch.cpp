@@ -105,15 +105,33 @@ int32_t i32(int64_t v) {
   return (int32_t)v;
 }
 
-cudaStream_t stream_of(PyObject* o, const at::Tensor& t) {
-  if (o != Py_None) return reinterpret_cast<cudaStream_t>((uintptr_t)number(o));
-  return c10::cuda::getCurrentCUDAStream(t.device().index()).stream();
-}
+// Makes the tensor's device current while the call runs, and finds the call's stream. What is
+// allocated comes from the current stream's memory; where the call runs in another one, `keep`
+// has it not go to new work, when it is given back, before that stream is done with it (a
+// workspace is given back when the call returns).
+struct Place {
+  c10::cuda::CUDAGuard device;
+  c10::cuda::CUDAStream on;
+  cudaStream_t stream;
+  bool other;
+  Place(PyObject* o, const at::Tensor& t)
+      : device(t.device()), on(c10::cuda::getCurrentCUDAStream(t.device().index())),
+        stream(on.stream()), other(false) {
+    if (o == Py_None) return;
+    stream = reinterpret_cast<cudaStream_t>((uintptr_t)number(o));
+    other = stream != on.stream();
+    if (other) on = c10::cuda::getStreamFromExternal(stream, t.device().index());
+  }
+  at::Tensor keep(at::Tensor t) const {
+    if (other) t.record_stream(on.unwrap());
+    return t;
+  }
+};
 
 at::Tensor made(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType dtype,
-                const at::Tensor& like) {
+                const at::Tensor& like, const Place& place) {
   const at::Tensor* t = tensor(o, name);
-  return t ? *t : at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device()));
+  return t ? *t : place.keep(at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device())));
 }
 
 void argc(Py_ssize_t n, Py_ssize_t want) {
@@ -151,12 +169,12 @@ PyObject* front(PyObject*, PyObject* const* a, Py_ssize_t n) {
   d.status = static_cast<int32_t*>(address(status, "status", kI32, {}));
   const void* px = address(&x, "x", x.scalar_type(), {T, (H + 2 * Hk) * D});
   const at::Tensor *qw = tensor(a[4], "q_weight"), *kw = tensor(a[5], "k_weight");
-  const c10::cuda::CUDAGuard guard(x.device());
+  const Place place(a[20], x);
   const bool dense = PyObject_IsTrue(a[14]);
-  at::Tensor q = made(a[16], "q", {T, H, D}, out, x), k, v;
+  at::Tensor q = made(a[16], "q", {T, H, D}, out, x, place), k, v;
   if (dense) {
-    k = made(a[17], "k", {T, Hk, D}, out, x);
-    v = made(a[18], "v", {T, Hk, D}, out, x);
+    k = made(a[17], "k", {T, Hk, D}, out, x, place);
+    v = made(a[18], "v", {T, Hk, D}, out, x, place);
   }
   const int rc = f_front(
       &d, px, static_cast<float*>(address(qw, "q_weight", kF32, {D})),
@@ -168,7 +186,7 @@ PyObject* front(PyObject*, PyObject* const* a, Py_ssize_t n) {
       address(&q, "q", out, {T, H, D}), address(dense ? &k : nullptr, "k", out, {T, Hk, D}),
       address(dense ? &v : nullptr, "v", out, {T, Hk, D}),
       address(kc, "k_cache", out, {pages, Hk, page, D}),
-      address(vc, "v_cache", out, {pages, Hk, page, D}), stream_of(a[20], x));
+      address(vc, "v_cache", out, {pages, Hk, page, D}), place.stream);
   if (rc != GDN_OK) fail(rc, "gdn_attn_front");
   PyObject* r = PyTuple_New(3);
   if (!r) throw python_error();
@@ -203,15 +221,15 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   d.out_dtype = dtype_code(to);
   d.status = static_cast<int32_t*>(address(status, "status", kI32, {}));
   const void* pq = address(&q, "q", t, {});
-  const c10::cuda::CUDAGuard guard(q.device());
-  at::Tensor out = made(a[6], "out", {T, H, D}, to, q), lse;
+  const Place place(a[10], q);
+  at::Tensor out = made(a[6], "out", {T, H, D}, to, q, place), lse;
   const bool want_lse = PyObject_IsTrue(a[7]) || a[8] != Py_None;
-  if (want_lse) lse = made(a[8], "lse", {T, H}, kF32, q);
+  if (want_lse) lse = made(a[8], "lse", {T, H}, kF32, q, place);
   const int rc = f_prefill(&d, pq, address(&k, "k", t, {T, Hk, D}), address(&v, "v", t, {T, Hk, D}),
                            static_cast<int32_t*>(address(cu, "cu_seqlens", kI32, {})),
                            (float)real(a[4]), address(&out, "out", to, {T, H, D}),
                            static_cast<float*>(address(want_lse ? &lse : nullptr, "lse", kF32, {T, H})),
-                           stream_of(a[10], q));
+                           place.stream);
   if (rc != GDN_OK) fail(rc, "gdn_attn_prefill");
   return with_lse(out, PyObject_IsTrue(a[7]) ? &lse : nullptr);
   END_HANDLE_TH_ERRORS
@@ -237,17 +255,18 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   d.out_dtype = dtype_code(to);
   d.status = static_cast<int32_t*>(address(status, "status", kI32, {}));
   const void* pq = address(&q, "q", t, {});
-  const c10::cuda::CUDAGuard guard(q.device());
-  at::Tensor out = made(a[8], "out", q.sizes(), to, q), lse, work;
+  const Place place(a[13], q);
+  at::Tensor out = made(a[8], "out", q.sizes(), to, q, place), lse, work;
   const at::IntArrayRef rows = q.sizes().slice(0, q.dim() - 1);
   const bool want_lse = PyObject_IsTrue(a[9]) || a[10] != Py_None;
-  if (want_lse) lse = made(a[10], "lse", rows, kF32, q);
+  if (want_lse) lse = made(a[10], "lse", rows, kF32, q, place);
   if (const at::Tensor* w = tensor(a[11], "workspace")) {
     work = *w;
   } else {
     const size_t bytes = f_workspace(&d);
     if (bytes == 0) fail(f_check(&d), "gdn_attn_decode");
-    work = at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(q.device()));
+    work = place.keep(
+        at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(q.device())));
   }
   d.workspace = address(&work, "workspace", work.scalar_type(), {});
   d.workspace_bytes = work.nbytes();
@@ -257,7 +276,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           static_cast<int32_t*>(address(&kv, "kv_lens", kI32, {N})),
                           i32(number(a[5])), (float)real(a[6]), address(&out, "out", to, q.sizes()),
                           static_cast<float*>(address(want_lse ? &lse : nullptr, "lse", kF32, rows)),
-                          stream_of(a[13], q));
+                          place.stream);
   if (rc != GDN_OK) fail(rc, "gdn_attn_decode");
   return with_lse(out, PyObject_IsTrue(a[9]) ? &lse : nullptr);
   END_HANDLE_TH_ERRORS

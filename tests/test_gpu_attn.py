@@ -615,6 +615,39 @@ def test_front_graph_and_stream():
     assert all(torch.equal(u, t) for u, t in zip(a, b))
 
 
+@pytest.mark.parametrize("call", ["front", "prefill", "decode"])
+def test_memory_waits_for_the_calls_stream(call):
+    """What a call allocates, its workspace included, is not free for other work while the
+    stream that it was given still has the call before it."""
+    x = torch.zeros(8, 6 * 128, dtype=BF, device="cuda")
+    q, k = (torch.zeros(8, h, 128, dtype=BF, device="cuda") for h in (4, 1))
+    kc = torch.zeros(3, 1, 16, 128, dtype=BF, device="cuda")
+    table = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    kv = torch.full((8,), 20, dtype=torch.int32, device="cuda")
+    run = {"front": lambda s: B.gdn_attn_front(x, 4, 1, 128, stream=s),
+           "prefill": lambda s: B.gdn_attn_prefill(q, k, k, stream=s),
+           "decode": lambda s: B.gdn_attn_decode(q, kc, kc, table, kv, stream=s)}[call]
+
+    def waiting():
+        return [b["size"] for seg in torch.cuda.memory_snapshot() for b in seg["blocks"]
+                if b["state"] == "active_awaiting_free" or b["state"] == "active_pending_free"]
+
+    s = torch.cuda.Stream()
+    run(None)
+    torch.cuda.synchronize()
+    assert not waiting()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(200_000_000)  # about 0.1 s
+    out = run(s)
+    held = len(waiting())
+    assert held == (1 if call == "decode" else 0)
+    del out
+    assert len(waiting()) == held + (3 if call == "front" else 1)
+    s.synchronize()
+    torch.cuda.empty_cache()
+    assert not waiting()
+
+
 # ---------------------------------------------------------------- together
 def test_prompt_then_decode_equals_a_longer_prompt():
     """front + prefill of a prompt, then front + decode of the next tokens, give the rows that
