@@ -39,7 +39,7 @@ EXPORTED = ("gdn_check_desc", "gdn_nt_max", "gdn_workspace_size", "gdn_build_chu
             "gdn_debug_build", "gdn_test_debug_poison",
             "gdn_recurrent_fwd", "gdn_conv_front", "gdn_bwd_workspace_size", "gdn_chunk_bwd",
             "gdn_attn_check_desc", "gdn_attn_workspace_size", "gdn_attn_front",
-            "gdn_attn_prefill", "gdn_attn_decode", "gdn_test_attn_prefix")
+            "gdn_attn_prefill", "gdn_attn_decode", "gdn_test_attn_prefix", "gdn_test_attn_tiles")
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
 GDN_ATTN_ROPE_INTERLEAVED = 1
 
@@ -128,6 +128,8 @@ def load_library(path: str = LIB_PATH):
         lib.gdn_attn_front.restype = ctypes.c_int
         lib.gdn_test_attn_prefix.argtypes = [i32]
         lib.gdn_test_attn_prefix.restype = None
+        lib.gdn_test_attn_tiles.argtypes = [i32]
+        lib.gdn_test_attn_tiles.restype = None
         lib.gdn_attn_prefill.argtypes = [P(GdnAttnDesc), vp, vp, vp, vp, ctypes.c_float, vp, vp,
                                          vp]
         lib.gdn_attn_prefill.restype = ctypes.c_int
@@ -596,3 +598,8 @@ def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
 def gdn_test_attn_prefix(always: bool) -> None:
     """Testing hook: gdn_attn_decode gives a common prefix its own pass at every size."""
     load_library().gdn_test_attn_prefix(1 if always else 0)
+
+
+def gdn_test_attn_tiles(tiles: int) -> None:
+    """Testing hook: gdn_attn_prefill's work items hold 1 or 2 row tiles; 0: by its rule."""
+    load_library().gdn_test_attn_tiles(tiles)

@@ -13,6 +13,9 @@ namespace gdn {
 static std::atomic<bool> g_prefix_always{false};
 bool attn_prefix_always() { return g_prefix_always.load(std::memory_order_relaxed); }
 
+static std::atomic<int> g_prefill_tiles{0};
+int attn_prefill_tiles() { return g_prefill_tiles.load(std::memory_order_relaxed); }
+
 }  // namespace gdn
 
 namespace {
@@ -71,6 +74,10 @@ extern "C" {
 
 void gdn_test_attn_prefix(int32_t always) {
   g_prefix_always.store(always != 0, std::memory_order_relaxed);
+}
+
+void gdn_test_attn_tiles(int32_t tiles) {
+  g_prefill_tiles.store(tiles == 1 || tiles == 2 ? tiles : 0, std::memory_order_relaxed);
 }
 
 int gdn_attn_check_desc(const gdn_attn_desc* desc) { return check_impl(desc); }

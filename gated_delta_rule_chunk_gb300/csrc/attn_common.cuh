@@ -44,10 +44,13 @@ struct AttnParams {
   float* lse;                         // or null
   int32_t* status;                    // or null
   int out_bf16;
+  int tiles;                          // prefill: row tiles of a work item, 1 or 2
 };
 
 // Testing hook (gdn_test_attn_prefix): a common prefix takes its own kernel at every size.
 bool attn_prefix_always();
+// Testing hook (gdn_test_attn_tiles): row tiles of a prompt's work items, 0: by the rule.
+int attn_prefill_tiles();
 
 bool launch_attn_front(const AttnFrontParams& p, cudaStream_t s);
 bool launch_attn_prefill(const AttnParams& p, cudaStream_t s);

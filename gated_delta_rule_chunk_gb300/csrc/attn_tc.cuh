@@ -286,7 +286,7 @@ struct PromptItems {
     it.tok = i * span;
     it.hk = idx - s * Hk;
     it.nA = (min(it.tok + nt, it.len) + kKeys - 1) / kKeys;
-    it.nB = it.tok + nt < it.len ? (min(it.tok + 2 * nt, it.len) + kKeys - 1) / kKeys : 0;
+    it.nB = span > nt && it.tok + nt < it.len ? (min(it.tok + 2 * nt, it.len) + kKeys - 1) / kKeys : 0;
     it.mask0 = (it.tok + 1) / kKeys;
     it.valid = 1;
     return it;
@@ -377,7 +377,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   pdl_wait();
   if (kPrefix) pdl_release();  // the decode kernel needs nothing from here
   if (!kPrefix && warp == 10) {  // cu_seqlens, each entry clamped and raised to the largest before it
-    const int span = 2 * nt;
+    const int span = p.tiles * nt;
     int carry = 0;
     bool bad = false;
     for (int n0 = 0; n0 <= p.N; n0 += 32) {
@@ -896,7 +896,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         if constexpr (kPrefix) {
           return PrefixItems(p, parts, 2 * nt);
         } else {
-          return PromptItems(bounds, pairs, p.N, 2 * nt, p.Hk);
+          return PromptItems(bounds, pairs, p.N, p.tiles * nt, p.Hk);
         }
       }();
       const int grid = (int)gridDim.x, b = (int)blockIdx.x;

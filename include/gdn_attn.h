@@ -162,6 +162,13 @@ int gdn_attn_decode(const gdn_attn_desc* desc, const void* q, const void* k_cach
  */
 void gdn_test_attn_prefix(int32_t always);
 
+/*
+ * Testing hook. gdn_attn_prefill works on one or two tiles of rows at a time, by a rule on the
+ * sizes; 1 or 2 fixes that for the calls that follow, 0 (the default) is the rule. Results are
+ * the same bit for bit (where all values are finite).
+ */
+void gdn_test_attn_tiles(int32_t tiles);
+
 #ifdef __cplusplus
 }
 #endif

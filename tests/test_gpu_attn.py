@@ -48,6 +48,18 @@ def close_attention(out, lse, ref, mag, ref_lse, rows=None):
 
 
 # ---------------------------------------------------------------- prefill
+@pytest.fixture(params=["by rule", "two"])
+def row_tiles(request):
+    """Work items of one or two row tiles as the sizes have it (one, in small tests), and of
+    two always."""
+    B.gdn_test_attn_tiles(2 if request.param == "two" else 0)
+    yield
+    B.gdn_test_attn_tiles(0)
+
+
+either = pytest.mark.usefixtures("row_tiles")
+
+
 def run_prefill(lens, H, Hk, D, seed=0, lead=0, tail=0, mul=1.0, scale=None, out_dtype=F32,
                 spoil=None):
     g = torch.Generator().manual_seed(seed)
@@ -72,18 +84,21 @@ def check_prefill(*a, **kw):
     assert (out[torch.tensor(~inside)] == 7.0).all() and (lse[torch.tensor(~inside)] == 7.0).all()
 
 
+@either
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("L", [1, 2, 31, 63, 64, 65, 127, 128, 129, 255, 257, 400])
 def test_prefill_lengths(L, D):
     check_prefill([L], 2, 1, D, seed=L)
 
 
+@either
 @pytest.mark.parametrize("H, Hk", [(1, 1), (3, 3), (3, 1), (5, 1), (6, 2), (7, 1), (8, 1), (16, 2),
                                    (24, 2), (33, 1), (64, 1)])
 def test_prefill_groups(H, Hk):
     check_prefill([70, 1, 150], H, Hk, 128, seed=H)
 
 
+@either
 @pytest.mark.parametrize("lens", [[0, 5, 0, 130, 1, 0], [300, 1, 1, 64], [128, 128], [1] * 70,
                                   [3, 250, 17, 129, 66]])
 @pytest.mark.parametrize("D", [64, 128])
@@ -91,17 +106,20 @@ def test_prefill_packed(lens, D):
     check_prefill(lens, 4, 2, D, seed=len(lens), lead=3, tail=9)
 
 
+@either
 def test_prefill_many_sequences():
     """More sequences than one launch takes, empty ones among them."""
     check_prefill([1 + 13 * i % 9 if i % 5 else 0 for i in range(1100)] + [140, 0, 3], 2, 1, 64, seed=7)
 
 
+@either
 @pytest.mark.parametrize("mul", [0.01, 4.0, 8.0])
 def test_prefill_score_ranges(mul):
     """Nearly uniform weights, and weights of a few keys whose maximum grows along the row."""
     check_prefill([385], 2, 1, 128, mul=mul, seed=3, out_dtype=F32)
 
 
+@either
 def test_prefill_growing_maximum():
     """Every block of keys scores far above the one before: each running maximum is replaced."""
     def spoil(q, k, v):
@@ -115,11 +133,13 @@ def test_prefill_growing_maximum():
     check_prefill([500], 2, 1, 64, spoil=falling)
 
 
+@either
 def test_prefill_scale_and_bf16_output():
     check_prefill([200], 4, 1, 128, scale=0.3, seed=5)
     check_prefill([200], 4, 1, 64, seed=6, out_dtype=BF)
 
 
+@either
 @pytest.mark.parametrize("D", [64, 128])
 @pytest.mark.parametrize("what", ["nan", "inf", "lowest"])
 def test_prefill_unseen_values_have_no_influence(what, D):
@@ -144,6 +164,7 @@ def test_prefill_unseen_values_have_no_influence(what, D):
         assert torch.isnan(out[2 + 130:2 + 200]).all()  # NaN that is seen is not hidden
 
 
+@either
 def test_prefill_one_nan_value_reaches_only_the_rows_that_see_it():
     def spoil(q, k, v):
         v[77, 0, 5] = float("nan")
@@ -158,6 +179,7 @@ def test_prefill_one_nan_value_reaches_only_the_rows_that_see_it():
     close_attention(out[:77], lse[:77], ref[:77], mag[:77], rl[:77])
 
 
+@either
 def test_prefill_malformed_cu_seqlens():
     g = torch.Generator().manual_seed(1)
     q, k, v = (randn(g, 300, h, 64).cuda() for h in (4, 2, 2))
@@ -173,6 +195,7 @@ def test_prefill_malformed_cu_seqlens():
         assert torch.equal(outs[0][0], outs[1][0])
 
 
+@either
 def test_prefill_repeatable_other_stream_and_graph():
     g = torch.Generator().manual_seed(2)
     q, k, v = (randn(g, 700, h, 128).cuda() for h in (8, 2, 2))
@@ -198,11 +221,27 @@ def test_prefill_repeatable_other_stream_and_graph():
     assert torch.equal(c[:650], d[:650])
 
 
+@pytest.mark.parametrize("lens, H, Hk, D", [([700, 3, 129, 64], 6, 2, 128), ([900, 130], 4, 4, 64)])
+def test_prefill_same_with_one_or_two_tiles(lens, H, Hk, D):
+    g = torch.Generator().manual_seed(12)
+    q, k, v = (randn(g, sum(lens), h, D).cuda() for h in (H, Hk, Hk))
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32).cuda()
+    res = []
+    for tiles in (1, 2):
+        B.gdn_test_attn_tiles(tiles)
+        try:
+            res.append(B.gdn_attn_prefill(q, k, v, cu, return_lse=True, out_dtype=F32))
+        finally:
+            B.gdn_test_attn_tiles(0)
+    assert all(torch.equal(a, b) for a, b in zip(*res))
+
+
 def test_prefill_empty():
     e = torch.empty(0, 4, 64, dtype=BF, device="cuda")
     assert B.gdn_attn_prefill(e, e, e).shape == (0, 4, 64)
 
 
+@either
 @pytest.mark.parametrize("H, Hk, D", [(16, 4, 128), (8, 8, 64)])
 def test_prefill_long(H, Hk, D):
     """Many key tiles and many work items at once, against 64-bit products on the GPU."""
