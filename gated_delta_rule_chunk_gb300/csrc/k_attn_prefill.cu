@@ -26,9 +26,11 @@ bool launch(const AttnParams& p, cudaStream_t s) {
     // prompts, as an SM's longest item is what counts there. Measured with one / two tiles an
     // item: 2 x 2010 tokens x 2 heads of 64 16.9 / 22.7 us, 75 tokens x 15 heads 7.4 / 8.8 (no
     // more than one item an SM); 960 x 20 heads 16.1 / 18.6, 9632 x 4 heads 76.8 / 83.1, but
-    // 19 x 164 tokens x 8 heads 11.2 / 9.9 (two); 1785 x 5 x 8 heads 47.7 / 32.3 (four).
+    // 19 x 164 tokens x 8 heads 11.2 / 9.9 (two); 1785 x 5 x 8 heads 47.7 / 32.3 (four). The
+    // lengths are on the device: half a tile a sequence stands for the ragged ends.
     const int64_t each = (int64_t)p.T >= 256 * (int64_t)p.N ? 2 : 1;
-    a.tiles = attn_prefill_tiles() ? attn_prefill_tiles() : items_of(nt) <= each * num_sms() ? 1 : 2;
+    const int64_t singles = (((int64_t)p.T + nt - 1) / nt + a.N / 2) * p.Hk;
+    a.tiles = attn_prefill_tiles() ? attn_prefill_tiles() : singles <= each * num_sms() ? 1 : 2;
     const int64_t items = items_of(a.tiles * nt);
     if (!launch_attn_tc<D, false>(a, PrefixParts{}, tm_k, tm_v, items, s)) return false;
   }
