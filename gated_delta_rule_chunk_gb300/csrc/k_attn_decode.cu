@@ -607,12 +607,14 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   w.prefix.splits = L.splits < w.prefix.tiles ? L.splits : w.prefix.tiles;
   // The prefix kernel and the merge of its parts cost about 5 us; without them every sequence
   // reads the prefix's keys itself, mostly from L2, and with many query rows also multiplies
-  // them in WM row tiles at warp-MMA speed. Measured (GB300; bytes read again, with / without):
-  // 32 MB 16.9 / 12.8 us, 59 MB 18.0 / 15.9, 66 MB 25.8 / 21.6, 126 MB 18.6 / 21.7, 235 MB
-  // 20.9 / 33.8; with 40 rows a pair 33 MB 29.3 / 32.2.
+  // them in WM row tiles at warp-MMA speed. What counts is how many keys that is, of either head
+  // size. Measured (GB300; thousands of keys read again, with / without the prefix kernel):
+  // 84 17.7 / 14.3 us, 129 15.4 / 15.0, 172 27.3 / 24.7, 188 17.9 / 20.4, 224 17.7 / 21.5,
+  // 429 17.4 / 29.9; D = 64: 157 20.9 / 20.7, 237 15.1 / 18.1, 396 15.6 / 24.1; four row tiles
+  // behind a short prefix: 199 24.3 / 20.8.
   const int R = p.nq * p.G, WM = R <= 16 ? 1 : R <= 32 ? 2 : 4;
-  const int64_t again = (int64_t)(p.N - 1) * p.common * p.Hk * D * 4 * WM;
-  p.shared = p.n_pages > 0 && p.N > 1 && (again >= (int64_t)80 << 20 || attn_prefix_always())
+  const int64_t again = (int64_t)(p.N - 1) * p.common * p.Hk * WM;
+  p.shared = p.n_pages > 0 && p.N > 1 && (again >= 180000 || attn_prefix_always())
                  ? p.common : 0;
   if (p.shared > 0 && !launch_prefix<D>(p, w.prefix, s)) return false;
   // no more CTAs than units there can be
