@@ -19,6 +19,9 @@
 // Weights are 2^(c s - ref) with c = scale * log2(e) and ref a running maximum that is
 // replaced when outgrown by 2^8, as in attn_tc.cuh; rounded to bf16 for the second product,
 // summed in fp32 before that.
+//
+// Measured (GB300): 64 sequences of up to 8192 keys 148.5 to 152 us (6.8 TB/s), one of 8191 keys
+// 10.0 us, 64 behind 16384 shared keys 54 to 59 us.
 #include "attn_tc.cuh"
 
 namespace gdn {
