@@ -1,6 +1,5 @@
 // Shared definitions of the softmax-attention kernels (include/gdn_attn.h): launch
-// parameters, the sequence lookup and the row-by-row attention that the tiled kernels
-// are checked against.
+// parameters and the sequence lookup.
 #pragma once
 
 #include "../../include/gdn_attn.h"
@@ -63,55 +62,6 @@ __device__ __forceinline__ int seq_len(const AttnParams& p, int n) {
 }
 __device__ __forceinline__ int keys_seen(const AttnParams& p, int n, int i) {
   return max(seq_len(p, n) - p.nq + i + 1, 0);
-}
-
-// Attention of one query row by one warp, in fp32 throughout: keys 32 at a time, one per
-// lane for the scores, then the lanes own D / 32 output columns each. kp(j) and vp(j) give
-// key j's rows, or null for a row of zeros. Nothing past n_keys is read.
-template <int D, typename KP, typename VP>
-__device__ void attn_row(const __nv_bfloat16* __restrict__ q, int n_keys, float scale, KP kp,
-                         VP vp, float (&o)[D / 32], float& lse) {
-  constexpr int E = D / 32;
-  const int lane = threadIdx.x & 31;
-  float m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = 0.f;
-  for (int j0 = 0; j0 < n_keys; j0 += 32) {
-    const int j = j0 + lane;
-    float s = -INFINITY;
-    if (j < n_keys) {
-      const __nv_bfloat16* kr = kp(j);
-      float acc = 0.f;
-      if (kr)
-        for (int d = 0; d < D; ++d) acc += __bfloat162float(q[d]) * __bfloat162float(kr[d]);
-      s = acc * scale;
-    }
-    float mt = s;
-#pragma unroll
-    for (int x = 16; x > 0; x >>= 1) mt = fmaxf(mt, __shfl_xor_sync(0xffffffffu, mt, x));
-    const float mn = fmaxf(m, mt);
-    const float ref = mn == -INFINITY ? 0.f : mn;  // no key with a weight yet
-    const float c = expf(m - ref), w = expf(s - ref);
-    m = mn;
-    l = l * c + w;  // this lane's keys
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] *= c;
-    const int cnt = min(32, n_keys - j0);
-    for (int i = 0; i < cnt; ++i) {
-      const float wi = __shfl_sync(0xffffffffu, w, i);
-      const __nv_bfloat16* vr = vp(j0 + i);
-      if (vr) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) o[e] += wi * __bfloat162float(vr[lane * E + e]);
-      }
-    }
-  }
-#pragma unroll
-  for (int x = 16; x > 0; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-  const float r = l == 0.f ? 0.f : 1.f / l;  // a row without keys: zeros
-#pragma unroll
-  for (int e = 0; e < E; ++e) o[e] *= r;
-  lse = l == 0.f ? -INFINITY : m + logf(l);
 }
 
 // One lane's D / 32 output columns of row `row` (a [rows, D] array).

@@ -20,9 +20,9 @@
 //                   O += P V (P in TMEM). While A's rows are weighed, B's products run.
 //   warp 10         hands out the work items (persistent CTAs, one per SM)
 //   warps 12-15     V tiles with masked keys: rows past the sequence's end are zeroed, and
-//                   a value that is not finite is looked for, because a weight of 0 would
-//                   not remove it (0 * inf); the rows of such a tile pair are then computed
-//                   one by one without it (rare, so only correctness counts there).
+//                   so is a value that is not finite, because a weight of 0 would not remove
+//                   it (0 * inf). The rows that do see one get it added to their result (no
+//                   weight changes what it makes of it).
 // TMEM: score buffers of 128 columns, then O_A and O_B of D. At D = 128 there is room for two
 // buffers, one of A's and one of B's: a tile's next scores wait for its own P V, and the order
 // of issue keeps them apart. At D = 64 there are three, taken in turn by the sequence of
@@ -215,7 +215,7 @@ struct AttnBars {
   uint64_t item_full[kItems], item_empty[kItems];
   AttnItem item[kItems];
   uint32_t tmem;
-  // Item number + 1 of the last item in this place with an unsafe V tile: the ring holds V
+  // Item number + 1 of the last item in this place with a value taken out of a V tile: the ring holds V
   // tiles of at most four items after the one whose rows are being written.
   int poison[8];
 };
@@ -542,7 +542,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       int64_t to[4];  // the rows that this lane writes, -1: none
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        to[i] = __shfl_sync(0xffffffffu, real && !poison ? at : -1, i * 8 + (lane >> 2));
+        to[i] = __shfl_sync(0xffffffffu, real ? at : -1, i * 8 + (lane >> 2));
       const bool wide = kPrefix || !p.out_bf16;  // fp32 rows
       char* out = static_cast<char*>(kPrefix ? static_cast<void*>(parts.o) : p.out) + (lane & 3) * 16;
 #pragma unroll 1
@@ -580,36 +580,48 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.o_empty[X]);
       if constexpr (kPrefix) {
-        if (real && !poison) parts.ml[at] = make_float2(ref * c, l);
+        if (real) parts.ml[at] = make_float2(ref * c, l);
       } else {
         if (real && p.lse) p.lse[at] = l == 0.f ? -INFINITY : ref * p.scale + logf(l);
       }
-      if (poison) {  // this warp's rows one by one, from global memory
-        for (int i = 0; i < 32; ++i) {
-          const int rr = (warp & 3) * 32 + i, ti = rr / p.G, t = it.tok + X * nt + ti;
-          if (ti >= nt || t >= it.len) continue;
-          const size_t tr = (size_t)(it.base + t) * p.H + it.hk * p.G + (rr - ti * p.G);
-          float o[D / 32], lse;
+      if (poison) {  // values that were taken out of V tiles go to this warp's rows that see them
+        __syncwarp();
+        constexpr int E = D / 32;
+        const int sees = real ? lim : 0;
+        const int end = __reduce_max_sync(0xffffffffu, min(sees, n * kKeys));
+#pragma unroll 1
+        for (int key = kPrefix ? it.mask0 * kKeys : it.tok + 1; key < end; ++key) {
+          const __nv_bfloat16* v = p.v + lane * E;
           if constexpr (kPrefix) {
-            const int k0 = it.kv0 * kKeys;
-            const int k1 = min(min(keys_seen(p, t / p.nq, t % p.nq), p.shared), k0 + n * kKeys);
-            auto at_key = [&](const __nv_bfloat16* base, int j) -> const __nv_bfloat16* {
-              const int key = k0 + j, pg = p.table[key >> p.page_shift];
-              if (pg < 0 || pg >= p.n_pages) return nullptr;
-              return base + ((((size_t)pg * p.Hk + it.hk) << p.page_shift) + (key & (p.page - 1))) * D;
-            };
-            attn_row<D>(p.q + tr * D, k1 - k0, p.scale, [&](int j) { return at_key(p.k, j); },
-                        [&](int j) { return at_key(p.v, j); }, o, lse);
-            const size_t row = part0 + tr;
-            store_row<D>(parts.o, false, row, o);
-            if (lane == 0)
-              parts.ml[row] = make_float2(lse * 1.44269504088896340736f, lse == -INFINITY ? 0.f : 1.f);
+            const int at_key = it.kv0 * kKeys + key, pg = p.table[at_key >> p.page_shift];
+            if (pg < 0 || pg >= p.n_pages) continue;
+            v += ((((size_t)pg * p.Hk + it.hk) << p.page_shift) + (at_key & (p.page - 1))) * D;
           } else {
-            const size_t kv = ((size_t)it.base * p.Hk + it.hk) * D, step = (size_t)p.Hk * D;
-            attn_row<D>(p.q + tr * D, t + 1, p.scale,
-                        [&](int j) { return p.k + kv + j * step; },
-                        [&](int j) { return p.v + kv + j * step; }, o, lse);
-            store_row<D>(p.out, p.out_bf16, tr, o);
+            v += ((size_t)(it.base + key) * p.Hk + it.hk) * D;
+          }
+          float x[E];
+          bool bad = false;
+#pragma unroll
+          for (int e = 0; e < E; ++e) {
+            x[e] = __bfloat162float(v[e]);
+            bad |= !isfinite(x[e]);
+          }
+          if (!__any_sync(0xffffffffu, bad)) continue;
+#pragma unroll 1
+          for (int i = 0; i < 32; ++i) {
+            const int64_t row = __shfl_sync(0xffffffffu, at, i);
+            if (key >= __shfl_sync(0xffffffffu, sees, i)) continue;
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+              if (isfinite(x[e])) continue;
+              const int64_t to_e = row * D + lane * E + e;
+              if (wide) {
+                (kPrefix ? parts.o : static_cast<float*>(p.out))[to_e] += x[e];
+              } else {
+                __nv_bfloat16* y = static_cast<__nv_bfloat16*>(p.out) + to_e;
+                *y = __float2bfloat16_rn(__bfloat162float(*y) + x[e]);
+              }
+            }
           }
         }
       }
@@ -957,7 +969,13 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
                                ((x.y & 0x7F807F80u) + 0x00800080u) |
                                ((x.z & 0x7F807F80u) + 0x00800080u) |
                                ((x.w & 0x7F807F80u) + 0x00800080u);
-            found |= (e & 0x80008000u) != 0;
+            if (e & 0x80008000u) {
+              found = true;
+              uint16_t* y = reinterpret_cast<uint16_t*>(v);
+#pragma unroll 1
+              for (int i = 0; i < 8; ++i)
+                if ((y[i] & 0x7F80) == 0x7F80) y[i] = 0;
+            }
           }
         };
         uint4* v = reinterpret_cast<uint4*>(tile);

@@ -179,6 +179,39 @@ def test_prefill_one_nan_value_reaches_only_the_rows_that_see_it():
     close_attention(out[:77], lse[:77], ref[:77], mag[:77], rl[:77])
 
 
+def same_where_not_finite(out, ref):
+    """NaN and infinities where the formula has them, with their signs."""
+    o = np64(out).reshape(ref.shape)
+    assert np.array_equal(np.isnan(o), np.isnan(ref))
+    assert np.array_equal(np.isposinf(o), np.isposinf(ref))
+    assert np.array_equal(np.isneginf(o), np.isneginf(ref))
+
+
+@either
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_prefill_infinities_where_they_are_seen(D, out_dtype):
+    """Values that are not finite at keys in and outside tiles with masked keys, several in one
+    column: each row has of them what it sees."""
+    inf, nan = float("inf"), float("nan")
+    spots = [(0, 0, 3, inf), (70, 1, 5, -inf), (129, 0, 3, inf), (130, 0, 7, -inf), (131, 0, 7, inf),
+             (200, 1, D - 1, nan), (255, 0, 0, inf), (256, 1, 9, -inf), (299, 0, 11, nan),
+             (300, 0, 1, inf), (340, 1, D // 2, -inf), (379, 1, 2, inf)]  # the second prompt: 300 on
+
+    def spoil(q, k, v):
+        for t, h, d, x in spots:
+            v[t, h, d] = x
+
+    q, k, v, cu, out, lse = run_prefill([300, 80], 4, 2, D, seed=21, out_dtype=out_dtype, spoil=spoil)
+    with np.errstate(invalid="ignore"):
+        ref, mag, rl, inside = A.prefill(np64(q), np64(k), np64(v), cu.numpy(), None)
+    same_where_not_finite(out, ref)
+    o, fin = np64(out).reshape(ref.shape), np.isfinite(ref)
+    tol = REL * mag[fin] + (2.0 ** -8 * np.abs(ref[fin]) if out_dtype == BF else 0.0) + 1e-6
+    assert (np.abs(o[fin] - ref[fin]) <= tol).all() and fin.mean() > 0.5
+    assert np.abs(np64(lse) - rl.reshape(lse.shape)).max() <= 1e-3
+
+
 @either
 def test_prefill_malformed_cu_seqlens():
     g = torch.Generator().manual_seed(1)
@@ -403,6 +436,30 @@ def test_decode_shared_prefix_rows(N, H, Hk, nq):
 def test_decode_sequences_shorter_than_the_prefix():
     check_decode([200, 64, 0, 1, 320, 319, 257], 4, 2, 128, 64, shared=320, seed=4)
     check_decode([2, 64, 0, 1, 320, 65], 4, 2, 128, 64, nq=3, shared=320, seed=4)
+
+
+@both
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode_infinities_where_they_are_seen(D):
+    """Infinities and NaN in a prefix that some sequences end inside, and in own tokens."""
+    g = torch.Generator().manual_seed(22)
+    lens, H, Hk, page, nq, shared = [500, 290, 262, 400, 140, 384], 4, 2, 32, 3, 384
+    kc, vc, table = make_cache(g, [max(n, shared) for n in lens], Hk, D, page, shared)
+    q = randn(g, len(lens), nq, H, D)
+    spots = [(0, 5, 0, 1, float("inf")), (0, 139, 1, 2, -float("inf")), (0, 200, 0, 4, float("inf")),
+             (0, 261, 0, 4, -float("inf")), (0, 289, 1, D - 1, float("nan")), (0, 300, 0, 7, float("inf")),
+             (0, 498, 1, 8, -float("inf")), (3, 390, 0, 9, float("inf")), (3, 399, 1, 0, float("nan"))]
+    for n, t, h, d, x in spots:
+        vc[int(table[n, t // page]), h, t % page, d] = x
+    kv = torch.tensor(lens, dtype=torch.int32)
+    out, lse = B.gdn_attn_decode(q.cuda(), kc.cuda(), vc.cuda(), table.cuda(), kv.cuda(), shared,
+                                 out_dtype=F32, return_lse=True)
+    with np.errstate(invalid="ignore"):
+        ref, mag, rl = A.decode(np64(q), np64(kc), np64(vc), table.numpy(), lens, shared)
+    same_where_not_finite(out, ref)
+    fin = np.isfinite(ref)
+    assert (np.abs(np64(out)[fin] - ref[fin]) <= REL * mag[fin] + 1e-6).all() and fin.mean() > 0.5
+    assert np.abs(np64(lse) - rl).max() <= 1e-3
 
 
 @both
