@@ -32,8 +32,8 @@
 //
 // Bound: at D = 128 the chain of a step (scores, weights, products; 2,600 cycles, 2,048 of them
 // MMAs); short prompts by the start and the output of an item, about 2.3 steps. Measured
-// (GB300): 16384 tokens x 32 heads 1.28 ms (1,720 TFLOP/s; 1.39 ms under the power limit), 4096
-// x 16 heads 52 us (1,316 TFLOP/s), 8 ragged prompts x 32 heads 62.5 us (962 TFLOP/s), 4001 x 16
+// (GB300): 16384 tokens x 32 heads 1.27 ms (1,730 TFLOP/s; 1.39 ms under the power limit), 4096
+// x 16 heads 52 us (1,320 TFLOP/s), 8 ragged prompts x 32 heads 62.1 us (968 TFLOP/s), 4001 x 16
 // heads of 64 39.6 us (828 TFLOP/s).
 #pragma once
 
@@ -215,8 +215,8 @@ struct AttnBars {
   uint64_t item_full[kItems], item_empty[kItems];
   AttnItem item[kItems];
   uint32_t tmem;
-  // Item number + 1 of the last item in this place with a value taken out of a V tile: the ring holds V
-  // tiles of at most four items after the one whose rows are being written.
+  // Item number + 1 of the last item in this place with a value taken out of a V tile: the
+  // ring holds V tiles of at most four items after the one whose rows are being written.
   int poison[8];
 };
 

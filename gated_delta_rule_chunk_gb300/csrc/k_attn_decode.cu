@@ -21,7 +21,7 @@
 // summed in fp32 before that.
 //
 // Measured (GB300): 64 sequences of up to 8192 keys 148.5 to 152 us (6.8 TB/s), one of 8191 keys
-// 10.0 us, 64 behind 16384 shared keys 54 to 59 us.
+// 10.0 us, 64 behind 16384 shared keys 53 to 58 us.
 #include "attn_tc.cuh"
 
 namespace gdn {
