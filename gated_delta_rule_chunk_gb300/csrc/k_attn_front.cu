@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
   int64_t pos = 0;
   if (live) pos = p.kv_lens ? (int64_t)p.kv_lens[n] - (e - t) : t - b;
 
-  // cos and sin of this lane's pairs; 1 and 0 where nothing turns
+  // cos and sin of this lane's pairs
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
   if (live && turned) {
     if (pos < 0 || pos >= p.max_pos) set_status(p.status, GDN_DEV_BAD_LENGTH);
@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
       float& a = kInter ? z[2 * i] : z[i];
       float& d = kInter ? z[2 * i + 1] : z[4 + i];
       const float a0 = a;
-      a = a0 * c[i] - d * s[i];
-      d = d * c[i] + a0 * s[i];
+      // (elsewhere as it is: a sin of 0 would make NaN of an infinity)
+      a = turned ? a0 * c[i] - d * s[i] : a0;
+      d = turned ? d * c[i] + a0 * s[i] : d;
     }
   };
   auto load_w = [&](const float* from, float (&w)[8]) {

@@ -669,6 +669,32 @@ def test_front_small_and_zero_rows():
     check_front([3], 2, 1, 128, 64, mul=0.0)
 
 
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("D, rot", [(64, 16), (128, 0), (128, 32)])
+@pytest.mark.parametrize("x_dtype, out_dtype", [(BF, BF), (F32, F32)])
+def test_front_elements_that_do_not_turn_are_copied(D, rot, inter, x_dtype, out_dtype):
+    """Without a norm, what lies past the rotated part comes out as it went in: an infinity or a
+    NaN there changes no other element."""
+    g = torch.Generator().manual_seed(31)
+    H, Hk, T = 4, 2, 21
+    x = randn(g, T, H + 2 * Hk, D, dtype=x_dtype)
+    for i, bad in enumerate((float("inf"), -float("inf"), float("nan"))):
+        for d in (rot, rot + 5, D - 1):
+            x[(5 * i + d) % T, :, d] = bad
+    rope = rope_table(T, rot).cuda() if rot else None
+    got = B.gdn_attn_front(x.view(T, -1).cuda(), H, Hk, D, rope=rope, interleaved=inter,
+                           out_dtype=out_dtype)
+    finite = torch.where(torch.isfinite(x), x, torch.zeros_like(x))
+    ref = A.front(np64(finite).reshape(T, -1), H, Hk, D, rope=None if rope is None else np64(rope),
+                  interleaved=inter)
+    for y, want, at in zip(got, ref, (0, H, H + Hk)):
+        heads = slice(at, at + y.shape[1])
+        first = 0 if at == H + Hk else rot
+        same = x[:, heads, first:].to(out_dtype).float()
+        torch.testing.assert_close(y[..., first:].float().cpu(), same, rtol=0, atol=0, equal_nan=True)
+        close_front(y[..., :first], want[..., :first], out_dtype)
+
+
 def test_front_without_lengths_and_bad_places():
     g = torch.Generator().manual_seed(5)
     x = randn(g, 40, 4 * 64).cuda()
