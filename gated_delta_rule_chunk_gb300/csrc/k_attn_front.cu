@@ -72,10 +72,11 @@ __device__ __forceinline__ int find_seq(const int32_t* cu, int N, int T, int t, 
   return b <= t && t < e && b >= 0 && e <= T ? lo : -1;
 }
 
-// 1 / sqrt(x): rsqrtf is good to 2 ulp, one Newton step brings it to rounding.
+// 1 / sqrt(x): rsqrtf is good to 2 ulp, one Newton step brings it to rounding (not from 0, the
+// result for infinity, which the step would make NaN).
 __device__ __forceinline__ float inv_sqrt(float x) {
   const float r = rsqrtf(x);
-  return r * (1.5f - 0.5f * x * r * r);
+  return r == 0.f ? 0.f : r * (1.5f - 0.5f * x * r * r);
 }
 
 template <int D, bool kInBf16, bool kOutBf16, int R, bool kInter>
@@ -131,14 +132,49 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
     load4<false>(p.rope, (size_t)row * p.rot + 4 * lane, c);
     load4<false>(p.rope, (size_t)row * p.rot + half + 4 * lane, s);
   }
-  // (all lanes: the sums cross the lanes of a group)
-  auto norm_turn = [&](float (&z)[8], const float (&w)[8], bool norm) {
+  const float* weight = is_q ? p.qw : p.kw;
+  float w[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) w[i] = 1.f;
+  if (weight) {
+    load4<false>(weight, e0, w);
+    load4<false>(weight, e1, w + 4);
+  }
+  // Factors of the norms, for all heads before anything depends on one (their shuffles overlap;
+  // all lanes, as the sums cross the lanes of a group).
+  const uint32_t k_end = p.H + p.Hk;
+  auto normed = [&](int r) { return weight && h0 + r < k_end; };
+  auto squares = [&](const float (&z)[8]) {
     float ss = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) ss += z[i] * z[i];
 #pragma unroll
     for (int o = L / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    const float f = norm ? inv_sqrt(ss * (1.0f / D) + p.eps) : 1.f;
+    return ss;
+  };
+  float f[R];
+  bool big = false;
+#pragma unroll
+  for (int r = 0; r < R; ++r) {
+    const float ss = squares(y[r]);
+    big |= normed(r) && ss == INFINITY;
+    f[r] = normed(r) ? inv_sqrt(ss * (1.0f / D) + p.eps) : 1.f;
+  }
+  // A sum past the largest number (elements from about 2^60): again with the row times 2^-70,
+  // which leaves y as it is. The squares then stay below 2^116; what they lose at the lower end,
+  // and eps, are nothing beside a sum of at least 2^-12 (for an eps below 2^90).
+  if (__any_sync(0xffffffffu, big)) {
+    constexpr float kDown = 1.0f / (1ull << 35) / (1ull << 35);
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      const bool down = normed(r) && f[r] == 0.f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[r][i] *= down ? kDown : 1.f;
+      const float ss = squares(y[r]);
+      if (down) f[r] = inv_sqrt(ss * (1.0f / D));
+    }
+  }
+  auto norm_turn = [&](float (&z)[8], const float (&w)[8], float f) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] *= f * w[i];
 #pragma unroll
@@ -151,25 +187,15 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
       d = turned ? d * c[i] + a0 * s[i] : d;
     }
   };
-  auto load_w = [&](const float* from, float (&w)[8]) {
-#pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = 1.f;
-    if (from) {
-      load4<false>(from, e0, w);
-      load4<false>(from, e1, w + 4);
-    }
-  };
   auto put = [&](void* dst, size_t at, const float (&z)[8]) {
     store4<kOutBf16>(dst, at + e0, z);
     store4<kOutBf16>(dst, at + e1, z + 4);
   };
-  float w[8];
-  load_w(is_q ? p.qw : p.kw, w);
   if (__all_sync(0xffffffffu, is_q)) {
     const size_t dst = ((size_t)t * p.H + h0) * D;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
-      norm_turn(y[r], w, p.qw != nullptr);
+      norm_turn(y[r], w, f[r]);
       if (live && r < cnt) put(p.q, dst + r * D, y[r]);
     }
     return;
@@ -187,14 +213,13 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
       slot = (((size_t)pg * p.Hk) << p.page_shift) + (pos & (p.page - 1));
     }
   }
-  const bool norm = (is_q ? p.qw : p.kw) != nullptr;
 #pragma unroll
   for (int r = 0; r < R; ++r) {
-    const uint32_t h = h0 + r, k_end = p.H + p.Hk;
+    const uint32_t h = h0 + r;
     float z[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) z[i] = y[r][i];
-    norm_turn(z, w, norm);
+    norm_turn(z, w, f[r]);
     if (!live || r >= cnt) continue;
     if (is_q) {
       put(p.q, ((size_t)t * p.H + h) * D, z);

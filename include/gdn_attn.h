@@ -111,7 +111,9 @@ size_t gdn_attn_workspace_size(const gdn_attn_desc* desc);
  *   page_table, k_cache, v_cache  where k and v are appended; all NULL: not appended
  *   q            [T, H, D] in out_dtype
  *   k, v         [T, Hk, D] in out_dtype; both NULL: not written
- * Norm, rotation and their sums are fp32, rounded once to out_dtype. Rows outside every
+ * Norm, rotation and their sums are fp32, rounded once to out_dtype; any finite row has a
+ * finite norm, elements past the rotated ones are not touched by the rotation, and an infinite
+ * element takes only its own head with it (where that is normed). Rows outside every
  * sequence are not written. A position past max_pos uses the table's last row
  * (GDN_DEV_BAD_LENGTH); a token whose place in the cache does not exist is not appended
  * (GDN_DEV_BAD_PAGE_TABLE for a page outside [0, n_pages), GDN_DEV_BAD_LENGTH for a

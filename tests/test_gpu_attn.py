@@ -695,6 +695,49 @@ def test_front_elements_that_do_not_turn_are_copied(D, rot, inter, x_dtype, out_
         close_front(y[..., :first], want[..., :first], out_dtype)
 
 
+@pytest.mark.parametrize("x_dtype", [BF, F32])
+@pytest.mark.parametrize("D, rot, inter", [(64, 32, True), (128, 64, False)])
+@pytest.mark.parametrize("mul", [1e18, 1e20, 3e29, 5e37])
+def test_front_norm_of_large_rows(mul, D, rot, inter, x_dtype):
+    """Rows whose squares, or whose sum of squares, pass the largest 32-bit number."""
+    check_front([3, 40], 4, 2, D, rot, inter, x_dtype=x_dtype, out_dtype=F32, mul=mul)
+
+
+@pytest.mark.parametrize("out_dtype", [BF, F32])
+def test_front_norm_of_one_large_element(out_dtype):
+    """Beside one large element the others go to nothing, in that head alone."""
+    g = torch.Generator().manual_seed(32)
+    H, Hk, D, T = 4, 2, 128, 9
+    x = randn(g, T, H + 2 * Hk, D, dtype=F32)
+    for t, big in enumerate((1e15, 1e19, 1e25, 3e38, -3e38)):
+        x[t, t % (H + Hk), 7 * t] = big
+    qw, kw = (1 + randn(g, D, dtype=F32, mul=0.2) for _ in range(2))
+    got = B.gdn_attn_front(x.view(T, -1).cuda(), H, Hk, D, qw.cuda(), kw.cuda(), out_dtype=out_dtype)
+    for y, want in zip(got, A.front(np64(x).reshape(T, -1), H, Hk, D, np64(qw), np64(kw))):
+        close_front(y, want, out_dtype)
+
+
+@pytest.mark.parametrize("bad", [float("inf"), -float("inf")])
+def test_front_norm_of_an_infinite_element(bad):
+    """x / sqrt(mean x^2 + eps) with one x infinite: NaN there, 0 elsewhere in that head; a
+    rotation carries the NaN to the element's partner."""
+    g = torch.Generator().manual_seed(33)
+    H, Hk, D, T, rot = 4, 2, 64, 5, 16
+    x = randn(g, T, H + 2 * Hk, D, dtype=F32)
+    x[1, 1, 40] = bad  # not rotated
+    x[2, H, 3] = bad   # rotated, with element 11
+    w = torch.ones(D)
+    q, k, v = B.gdn_attn_front(x.view(T, -1).cuda(), H, Hk, D, w.cuda(), w.cuda(),
+                               rope=rope_table(T, rot), out_dtype=F32)
+    gone = torch.zeros(D, dtype=torch.bool)
+    gone[40] = True
+    assert torch.equal(torch.isnan(q[1, 1]).cpu(), gone) and (q[1, 1].cpu()[~gone] == 0).all()
+    gone[:] = False
+    gone[[3, 11]] = True
+    assert torch.equal(torch.isnan(k[2, 0]).cpu(), gone) and (k[2, 0].cpu()[~gone] == 0).all()
+    assert torch.isnan(q).sum() == 1 and torch.isnan(k).sum() == 2 and torch.isfinite(v).all()
+
+
 def test_front_without_lengths_and_bad_places():
     g = torch.Generator().manual_seed(5)
     x = randn(g, 40, 4 * 64).cuda()
