@@ -495,6 +495,9 @@ def gdn_workspace_regions(desc: GdnDesc):
 
 
 # ---------------------------------------------------------------- softmax attention
+# A call with a `stream` of its own that allocates (outputs, workspace) takes the memory from the
+# current stream's: it then comes after what the current stream holds, and is refused where only one
+# of the two streams is being captured. With all of them given it waits for nothing.
 _attn_module = None
 
 

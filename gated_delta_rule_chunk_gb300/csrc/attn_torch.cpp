@@ -7,6 +7,7 @@
 #include <Python.h>
 
 #include <ATen/ops/empty.h>
+#include <c10/core/Event.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -105,33 +106,58 @@ int32_t i32(int64_t v) {
   return (int32_t)v;
 }
 
+// Whether a stream is being captured; -1 where that cannot be asked.
+int captured(cudaStream_t s) {
+  cudaStreamCaptureStatus status = cudaStreamCaptureStatusNone;
+  if (cudaStreamIsCapturing(s, &status) == cudaSuccess) return status != cudaStreamCaptureStatusNone;
+  (void)cudaGetLastError();
+  return -1;
+}
+
 // Makes the tensor's device current while the call runs, and finds the call's stream. What is
-// allocated comes from the current stream's memory; where the call runs in another one, `keep`
-// has it not go to new work, when it is given back, before that stream is done with it (a
-// workspace is given back when the call returns).
+// allocated comes from the current stream's memory, which that stream's queued work may still be
+// using. Where the call runs in another one, that stream first waits for the current one as it
+// stands (order; a call that allocates nothing does not wait), and the memory does not go to new
+// work, when it is given back, before that stream is done with it (a workspace is given back when
+// the call returns). Neither can be had between a captured stream and one that is not.
 struct Place {
   c10::cuda::CUDAGuard device;
-  c10::cuda::CUDAStream on;
+  c10::cuda::CUDAStream current, on;
   cudaStream_t stream;
   bool other;
+  mutable bool allocated = false;
   Place(PyObject* o, const at::Tensor& t)
-      : device(t.device()), on(c10::cuda::getCurrentCUDAStream(t.device().index())),
+      : device(t.device()), current(c10::cuda::getCurrentCUDAStream(t.device().index())), on(current),
         stream(on.stream()), other(false) {
     if (o == Py_None) return;
     stream = reinterpret_cast<cudaStream_t>((uintptr_t)number(o));
     other = stream != on.stream();
     if (other) on = c10::cuda::getStreamFromExternal(stream, t.device().index());
   }
-  at::Tensor keep(at::Tensor t) const {
+  at::Tensor make(at::IntArrayRef shape, at::ScalarType dtype, const at::Tensor& like) const {
+    if (other && !allocated) {
+      const int a = captured(current.stream()), b = captured(stream);
+      if (a != b || a < 0)
+        refuse(PyExc_ValueError, "one of the call's stream and the current stream is being captured "
+                                 "and the other is not: outputs and workspace must be given");
+    }
+    allocated = true;
+    at::Tensor t = at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device()));
     if (other) t.record_stream(on.unwrap());
     return t;
+  }
+  void order() const {
+    if (!other || !allocated) return;
+    c10::Event e(c10::DeviceType::CUDA);
+    e.record(current.unwrap());
+    e.block(on.unwrap());
   }
 };
 
 at::Tensor made(PyObject* o, const char* name, at::IntArrayRef shape, at::ScalarType dtype,
                 const at::Tensor& like, const Place& place) {
   const at::Tensor* t = tensor(o, name);
-  return t ? *t : place.keep(at::empty(shape, at::TensorOptions().dtype(dtype).device(like.device())));
+  return t ? *t : place.make(shape, dtype, like);
 }
 
 void argc(Py_ssize_t n, Py_ssize_t want) {
@@ -176,6 +202,7 @@ PyObject* front(PyObject*, PyObject* const* a, Py_ssize_t n) {
     k = made(a[17], "k", {T, Hk, D}, out, x, place);
     v = made(a[18], "v", {T, Hk, D}, out, x, place);
   }
+  place.order();
   const int rc = f_front(
       &d, px, static_cast<float*>(address(qw, "q_weight", kF32, {D})),
       static_cast<float*>(address(kw, "k_weight", kF32, {D})),
@@ -225,6 +252,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   at::Tensor out = made(a[6], "out", {T, H, D}, to, q, place), lse;
   const bool want_lse = PyObject_IsTrue(a[7]) || a[8] != Py_None;
   if (want_lse) lse = made(a[8], "lse", {T, H}, kF32, q, place);
+  place.order();
   const int rc = f_prefill(&d, pq, address(&k, "k", t, {T, Hk, D}), address(&v, "v", t, {T, Hk, D}),
                            static_cast<int32_t*>(address(cu, "cu_seqlens", kI32, {})),
                            (float)real(a[4]), address(&out, "out", to, {T, H, D}),
@@ -265,11 +293,11 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   } else {
     const size_t bytes = f_workspace(&d);
     if (bytes == 0) fail(f_check(&d), "gdn_attn_decode");
-    work = place.keep(
-        at::empty({(int64_t)bytes}, at::TensorOptions().dtype(at::kByte).device(q.device())));
+    work = place.make({(int64_t)bytes}, at::kByte, q);
   }
   d.workspace = address(&work, "workspace", work.scalar_type(), {});
   d.workspace_bytes = work.nbytes();
+  place.order();
   const int rc = f_decode(&d, pq, address(&kc, "k_cache", t, {pages, Hk, page, D}),
                           address(&vc, "v_cache", t, {pages, Hk, page, D}),
                           static_cast<int32_t*>(address(&table, "page_table", kI32, {N, cols})),

@@ -813,6 +813,103 @@ def test_memory_waits_for_the_calls_stream(call):
     assert not waiting()
 
 
+def stream_call(call):
+    """A call with its outputs to be allocated, or with them given: run(stream, **outputs), the
+    outputs' names and shapes, and the bytes of a workspace."""
+    g = torch.Generator().manual_seed(41)
+    x = randn(g, 8, 6 * 128).cuda()
+    q, k = (randn(g, 8, h, 128).cuda() for h in (4, 1))
+    kc = randn(g, 3, 1, 16, 128).cuda()
+    table = torch.zeros(8, 2, dtype=torch.int32, device="cuda")
+    kv = torch.full((8,), 20, dtype=torch.int32, device="cuda")
+    if call == "front":
+        return (lambda s, **kw: B.gdn_attn_front(x, 4, 1, 128, stream=s, **kw),
+                dict(q=(8, 4, 128), k=(8, 1, 128), v=(8, 1, 128)), 0)
+    if call == "prefill":
+        return lambda s, **kw: (B.gdn_attn_prefill(q, k, k, stream=s, **kw),), dict(out=(8, 4, 128)), 0
+    size = B.gdn_attn_workspace_size(B.make_attn_desc(8, 8, 4, 1, 128, page_size=16, n_pages=3, max_pages=2))
+    return (lambda s, **kw: (B.gdn_attn_decode(q, kc, kc, table, kv, stream=s, **kw),),
+            dict(out=(8, 4, 128)), size)
+
+
+@pytest.mark.parametrize("call", ["front", "prefill", "decode"])
+def test_memory_is_free_before_the_calls_stream_uses_it(call):
+    """Memory that the current stream's queued work still writes is given back and allocated
+    again by a call on another stream: the call comes after that work."""
+    run, shapes, size = stream_call(call)
+    want = run(None)
+    s, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    run(s)  # (first use of the stream)
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)  # about 0.2 s
+    tmp = [torch.empty(shape, dtype=BF, device="cuda") for shape in shapes.values()]
+    tmp += [torch.empty(size, dtype=torch.uint8, device="cuda")] if size else []
+    for t in tmp:
+        t.view(torch.uint8).fill_(255)
+    places = [t.data_ptr() for t in tmp]
+    del tmp, t
+    got = run(s)
+    assert not here.query() and not s.query()  # the sleep runs, and the call waits for it
+    torch.cuda.synchronize()
+    assert {t.data_ptr() for t in got} & set(places)
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("call", ["front", "prefill", "decode"])
+def test_a_call_that_allocates_nothing_waits_for_its_own_stream_only(call):
+    run, shapes, size = stream_call(call)
+    want = run(None)
+    given = {n: torch.zeros(shape, dtype=BF, device="cuda") for n, shape in shapes.items()}
+    if size:
+        given["workspace"] = torch.empty(size, dtype=torch.uint8, device="cuda")
+    s, here = torch.cuda.Stream(), torch.cuda.current_stream()
+    run(s, **given)
+    torch.cuda.synchronize()
+    for t in given.values():
+        t.zero_()
+    torch.cuda.synchronize()
+    torch.cuda._sleep(400_000_000)
+    got = run(s, **given)
+    s.synchronize()
+    assert not here.query()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+
+
+@pytest.mark.parametrize("call", ["front", "prefill", "decode"])
+def test_memory_between_captured_and_other_streams(call):
+    """A call on a stream that joined the capture is captured with what it allocates; where only
+    one of the two streams is captured, it is refused, unless all is given."""
+    run, shapes, size = stream_call(call)
+    want = run(None)
+    s, lone = torch.cuda.Stream(), torch.cuda.Stream()
+    x = torch.zeros(4, device="cuda")
+    graph, other = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        x += 1
+        s.wait_stream(torch.cuda.current_stream())
+        got = run(s)
+        torch.cuda.current_stream().wait_stream(s)
+        with pytest.raises(ValueError, match="captured"):
+            run(lone)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(want, got))
+    given = {n: torch.zeros(shape, dtype=BF, device="cuda") for n, shape in shapes.items()}
+    if size:
+        given["workspace"] = torch.empty(size, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    with torch.cuda.graph(other, stream=s):
+        with torch.cuda.stream(lone):
+            with pytest.raises(ValueError, match="captured"):
+                run(s)
+            run(s, **given)
+    other.replay()
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, given[n]) for a, n in zip(want, shapes))
+
+
 # ---------------------------------------------------------------- together
 def test_prompt_then_decode_equals_a_longer_prompt():
     """front + prefill of a prompt, then front + decode of the next tokens, give the rows that
