@@ -14,6 +14,8 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <initializer_list>
+
 #include "../../include/gdn_attn.h"
 
 namespace {
@@ -91,6 +93,22 @@ void* address(const at::Tensor* t, const char* name, at::ScalarType dtype, at::I
     throw python_error();
   }
   return t->data_ptr();
+}
+
+struct Named {
+  PyObject* o;
+  const char* name;
+};
+// Refuses tensors on another device than x: nothing below this would see that. (One that is on no
+// CUDA device has its own message in `address`.)
+void same_device(const at::Tensor& x, const char* x_name, std::initializer_list<Named> others) {
+  const c10::Device on = x.device();
+  for (const Named& n : others) {
+    const at::Tensor* t = tensor(n.o, n.name);
+    if (t && x.is_cuda() && t->is_cuda() && t->device() != on)
+      refuse(PyExc_ValueError, "%s is on %s, %s on %s", n.name, t->device().str().c_str(), x_name,
+             on.str().c_str());
+  }
 }
 
 int64_t num_seqs(const at::Tensor* cu) {
@@ -175,6 +193,9 @@ PyObject* front(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    *kv = tensor(a[10], "kv_lens"), *table = tensor(a[11], "page_table"),
                    *kc = tensor(a[12], "k_cache"), *vc = tensor(a[13], "v_cache"),
                    *status = tensor(a[19], "status"), *q_in = tensor(a[16], "q");
+  same_device(x, "x", {{a[4], "q_weight"}, {a[5], "k_weight"}, {a[7], "rope"}, {a[9], "cu_seqlens"},
+                       {a[10], "kv_lens"}, {a[11], "page_table"}, {a[12], "k_cache"},
+                       {a[13], "v_cache"}, {a[16], "q"}, {a[17], "k"}, {a[18], "v"}, {a[19], "status"}});
   const int64_t N = num_seqs(cu);
   const at::ScalarType out =
       dtype_or(a[15], kc ? kc->scalar_type() : q_in ? q_in->scalar_type() : x.scalar_type());
@@ -239,6 +260,8 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const at::Tensor &q = needed(a[0], "q", 3), &k = needed(a[1], "k", 3), &v = needed(a[2], "v", 3);
   const at::Tensor *cu = tensor(a[3], "cu_seqlens"), *status = tensor(a[9], "status"),
                    *out_in = tensor(a[6], "out");
+  same_device(q, "q", {{a[1], "k"}, {a[2], "v"}, {a[3], "cu_seqlens"}, {a[6], "out"}, {a[8], "lse"},
+                       {a[9], "status"}});
   const int64_t T = q.size(0), H = q.size(1), D = q.size(2), Hk = k.size(1);
   const at::ScalarType t = q.scalar_type(),
                        to = dtype_or(a[5], out_in ? out_in->scalar_type() : t);
@@ -271,6 +294,8 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    &kv = needed(a[4], "kv_lens", 1);
   if (q.dim() != 3 && q.dim() != 4)
     refuse(PyExc_ValueError, "q must have shape [N, H, D] or [N, n_q, H, D]");
+  same_device(q, "q", {{a[1], "k_cache"}, {a[2], "v_cache"}, {a[3], "page_table"}, {a[4], "kv_lens"},
+                       {a[8], "out"}, {a[10], "lse"}, {a[11], "workspace"}, {a[12], "status"}});
   const at::Tensor *status = tensor(a[12], "status"), *out_in = tensor(a[8], "out");
   const int64_t N = q.size(0), nq = q.dim() == 3 ? 1 : q.size(1), H = q.size(-2), D = q.size(-1);
   const int64_t pages = kc.size(0), Hk = kc.size(1), page = kc.size(2), cols = table.size(1);

@@ -154,6 +154,37 @@ def test_binding_refuses_cpu_tensors_and_shapes():
         B.gdn_attn_prefill(q, q, q)
 
 
+def two_device_cases():
+    """Each call with all its tensors on cuda:0 (stand-ins without memory: the refusal comes
+    before anything is allocated, enqueued or looked at), and one of them on cuda:1."""
+    bf, i32, f32 = torch.bfloat16, torch.int32, torch.float32
+    front = dict(x=((8, 6 * 128), bf), q_weight=((128,), f32), k_weight=((128,), f32),
+                 rope=((64, 32), f32), cu_seqlens=((3,), i32), kv_lens=((2,), i32),
+                 page_table=((2, 4), i32), k_cache=((5, 1, 16, 128), bf),
+                 v_cache=((5, 1, 16, 128), bf), q=((8, 4, 128), bf), k=((8, 1, 128), bf),
+                 v=((8, 1, 128), bf), status=((1,), i32))
+    prefill = dict(q=((8, 4, 128), bf), k=((8, 1, 128), bf), v=((8, 1, 128), bf),
+                   cu_seqlens=((3,), i32), out=((8, 4, 128), bf), lse=((8, 4), f32),
+                   status=((1,), i32))
+    decode = dict(q=((2, 4, 128), bf), k_cache=((5, 1, 16, 128), bf), v_cache=((5, 1, 16, 128), bf),
+                  page_table=((2, 4), i32), kv_lens=((2,), i32), out=((2, 4, 128), bf),
+                  lse=((2, 4), f32), workspace=((1 << 24,), torch.uint8), status=((1,), i32))
+    for call, shapes, rest in (("front", front, dict(H=4, Hk=1, D=128)), ("prefill", prefill, {}),
+                               ("decode", decode, {})):
+        for name in list(shapes)[1:]:
+            yield pytest.param(call, shapes, rest, name, id=f"{call}-{name}")
+
+
+@pytest.mark.parametrize("call, shapes, rest, away", list(two_device_cases()))
+def test_binding_refuses_tensors_of_another_device(call, shapes, rest, away):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    with FakeTensorMode():
+        a = {n: torch.empty(shape, dtype=dtype, device="cuda:1" if n == away else "cuda:0")
+             for n, (shape, dtype) in shapes.items()}
+    with pytest.raises(ValueError, match=f"{away} is on cuda:1"):
+        getattr(B, f"gdn_attn_{call}")(**a, **rest)
+
+
 # ---------------------------------------------------------------- rotary table
 def test_rope_table_plain():
     t = rope_table(50, 8, base=100.0, device="cpu")
