@@ -39,7 +39,8 @@ EXPORTED = ("gdn_check_desc", "gdn_nt_max", "gdn_workspace_size", "gdn_build_chu
             "gdn_debug_build", "gdn_test_debug_poison",
             "gdn_recurrent_fwd", "gdn_conv_front", "gdn_bwd_workspace_size", "gdn_chunk_bwd",
             "gdn_attn_check_desc", "gdn_attn_workspace_size", "gdn_attn_front",
-            "gdn_attn_prefill", "gdn_attn_decode", "gdn_test_attn_prefix", "gdn_test_attn_tiles")
+            "gdn_attn_prefill", "gdn_attn_decode", "gdn_test_attn_prefix", "gdn_test_attn_tiles",
+            "gdn_test_attn_timeout")
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
 GDN_ATTN_ROPE_INTERLEAVED = 1
 
@@ -130,6 +131,8 @@ def load_library(path: str = LIB_PATH):
         lib.gdn_test_attn_prefix.restype = None
         lib.gdn_test_attn_tiles.argtypes = [i32]
         lib.gdn_test_attn_tiles.restype = None
+        lib.gdn_test_attn_timeout.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
+        lib.gdn_test_attn_timeout.restype = None
         lib.gdn_attn_prefill.argtypes = [P(GdnAttnDesc), vp, vp, vp, vp, ctypes.c_float, vp, vp,
                                          vp]
         lib.gdn_attn_prefill.restype = ctypes.c_int
@@ -606,3 +609,9 @@ def gdn_test_attn_prefix(always: bool) -> None:
 def gdn_test_attn_tiles(tiles: int) -> None:
     """Testing hook: gdn_attn_prefill's work items hold 1 or 2 row tiles; 0: by its rule."""
     load_library().gdn_test_attn_tiles(tiles)
+
+
+def gdn_test_attn_timeout(polls: int, item: int = 0) -> None:
+    """Testing hook: with polls > 0 the tensor-core attention kernel waits that many polls, before
+    a CTA's `item`-th work item, for an event that never happens (GDN_DEV_TIMEOUT); 0 turns it off."""
+    load_library().gdn_test_attn_timeout(int(polls), int(item))

@@ -16,6 +16,14 @@ bool attn_prefix_always() { return g_prefix_always.load(std::memory_order_relaxe
 static std::atomic<int> g_prefill_tiles{0};
 int attn_prefill_tiles() { return g_prefill_tiles.load(std::memory_order_relaxed); }
 
+static std::atomic<uint32_t> g_wait_polls{0}, g_wait_item{0};
+void attn_test_timeout(AttnParams& p) {
+  if (const uint32_t polls = g_wait_polls.load(std::memory_order_relaxed)) {
+    p.polls = polls;
+    p.stall = g_wait_item.load(std::memory_order_relaxed) + 1;
+  }
+}
+
 }  // namespace gdn
 
 namespace {
@@ -65,6 +73,8 @@ AttnParams attn_params(const gdn_attn_desc& d, const void* q, const void* k, con
   p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d.D);  // also NaN
   p.out = out; p.lse = lse; p.status = d.status;
   p.out_bf16 = d.out_dtype == GDN_BF16;
+  p.polls = kAttnPolls;
+  attn_test_timeout(p);
   return p;
 }
 
@@ -78,6 +88,11 @@ void gdn_test_attn_prefix(int32_t always) {
 
 void gdn_test_attn_tiles(int32_t tiles) {
   g_prefill_tiles.store(tiles == 1 || tiles == 2 ? tiles : 0, std::memory_order_relaxed);
+}
+
+void gdn_test_attn_timeout(uint32_t polls, uint32_t item) {
+  g_wait_item.store(item, std::memory_order_relaxed);
+  g_wait_polls.store(polls, std::memory_order_relaxed);
 }
 
 int gdn_attn_check_desc(const gdn_attn_desc* desc) { return check_impl(desc); }

@@ -44,8 +44,14 @@ struct AttnParams {
   int32_t* status;                    // or null
   int out_bf16;
   int tiles;                          // prefill: row tiles of a work item, 1 or 2
+  uint32_t polls;                     // limit of an on-chip wait
+  uint32_t stall;                     // testing hook: item + 1 that waits for what never happens, or 0
 };
 
+// Polls of an on-chip wait before it gives up.
+constexpr uint32_t kAttnPolls = 1u << 22;
+// Testing hook (gdn_test_attn_timeout): sets polls and stall where it is on.
+void attn_test_timeout(AttnParams& p);
 // Testing hook (gdn_test_attn_prefix): a common prefix takes its own kernel at every size.
 bool attn_prefix_always();
 // Testing hook (gdn_test_attn_tiles): row tiles of a prompt's work items, 0: by the rule.

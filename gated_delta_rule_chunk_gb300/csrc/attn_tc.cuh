@@ -52,7 +52,6 @@ constexpr int kRows = 128;           // rows of a tile
 constexpr int kKeys = 128;           // keys of a tile
 constexpr int kAttnSeqs = 1024;      // sequences of one launch
 constexpr int kItems = 4;            // work items handed out ahead
-constexpr uint32_t kPolls = 1u << 22;
 constexpr float kGrow = 8.0f;
 
 struct AttnItem {
@@ -212,6 +211,7 @@ struct AttnBars {
   // buf_empty: the product with the weights in a score buffer is complete.
   uint64_t q_full[2], q_empty[2], s_full[2][kSet], p_full[2][kSet], o_full[2][kSet];
   uint64_t o_empty[2], buf_empty[3];
+  uint64_t idle[2];  // all products of an issuing warp are complete
   uint64_t item_full[kItems], item_empty[kItems];
   AttnItem item[kItems];
   uint32_t tmem;
@@ -220,11 +220,17 @@ struct AttnBars {
   int poison[8];
 };
 
-// A bounded wait: once one has run out, this thread waits for nothing any more.
+// A bounded wait. Once one has run out, the thread waits for nothing any more and goes on to its
+// next item, where its warp leaves; the others' waits run out in turn, and the call's results are
+// invalid. What must not happen is that a ring place is loaded again before its last copy has
+// landed (a barrier that counts bytes would be armed twice): so the load warp stops at its first
+// failure, and a place is not handed back (v_fixed, kv_empty, q_empty) by a thread that has given
+// up. Copies and products in flight are waited for before the CTA ends. (Not to issue products
+// after a failure would put a test into their stream: 4096 tokens 53.9 -> 70.5 us.)
 struct Waiter {
-  uint32_t limit = kPolls;
+  uint32_t limit;
   int32_t* status;
-  __device__ explicit Waiter(int32_t* s) : status(s) {}
+  __device__ Waiter(int32_t* s, uint32_t polls) : limit(polls), status(s) {}
   __device__ __forceinline__ bool ok() const { return limit != 0; }
   __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t phase) {
     if (mbar_try_wait(bar, phase & 1u)) return;
@@ -368,6 +374,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       }
     }
     for (int i = 0; i < 3; ++i) mbar_init(&B.buf_empty[i], 1);
+    for (int i = 0; i < 2; ++i) mbar_init(&B.idle[i], 1);
     for (int i = 0; i < kItems; ++i) {
       mbar_init(&B.item_full[i], 1);
       mbar_init(&B.item_empty[i], kBufs == 2 ? 14 : 15);  // load, MMA, 8 row warps, 4 V warps
@@ -421,7 +428,11 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = B.tmem;
-  Waiter wait(p.status);
+  Waiter wait(p.status, p.polls);
+  // Whether any lane of this warp has seen the last item, or has given up.
+  auto done = [&](const AttnItem& it) {
+    return __any_sync(0xffffffffu, !it.valid || !wait.ok()) != 0;
+  };
 
   // ------------------------------------------------------------------ rows
   if (warp < 8) {
@@ -438,7 +449,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       const AttnItem it = B.item[k % kItems];
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.item_empty[k % kItems]);
-      if (!it.valid || !wait.ok()) break;
+      if (done(it)) break;
       const int n = X ? it.nB : it.nA;
       const uint32_t first = seq0;
       seq0 += it.nA + it.nB;
@@ -637,11 +648,12 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         const AttnItem it = B.item[k % kItems];
         if constexpr (kPrefix) __syncwarp();
         if (lane == 0) mbar_arrive(&B.item_empty[k % kItems]);
-        if (!it.valid || !wait.ok()) break;
+        if (kPrefix ? done(it) : !it.valid || !wait.ok()) break;
         const int n = max(it.nA, it.nB);
         auto load_q = [&](int X) {
           if (X && it.nB == 0) return;
           wait(&B.q_empty[X], loads[X] + 1);
+          if (!wait.ok()) return;
           ++loads[X];
           if (lane != 0) return;
           mbar_expect_tx(&B.q_full[X], (uint32_t)(nt * p.G * D * 2));
@@ -659,6 +671,10 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         auto load_kv = [&](const CUtensorMap* tm, int j, bool raw) {
           const int st = slot % kStages;
           wait(&B.kv_empty[st], slot / kStages + 1);
+          if (kPrefix ? __any_sync(0xffffffffu, !wait.ok()) : !wait.ok()) {
+            wait.limit = 0;
+            return;
+          }
           ++slot;
           uint64_t* bar = raw ? &B.v_raw[st] : &B.kv_full[st];
           (raw ? raw_uses : kv_uses) ^= 1u << st;
@@ -694,16 +710,25 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           page = page_next;
         }
       }
-      if (!wait.ok()) {  // copies in flight end before the CTA does
+      // Copies in flight end before the CTA does (all have been waited for already, unless someone
+      // gave up).
+      if (lane == 0) {
+#pragma unroll 1
         for (uint32_t i = 0; i < kStages && i < slot; ++i) {
-          if ((is_raw >> i) & 1) mbar_wait(&B.v_raw[i], ((raw_uses >> i) & 1) ^ 1, kPolls);
-          else mbar_wait(&B.kv_full[i], ((kv_uses >> i) & 1) ^ 1, kPolls);
+          const bool r = (is_raw >> i) & 1;
+          mbar_wait(r ? &B.v_raw[i] : &B.kv_full[i], (((r ? raw_uses : kv_uses) >> i) & 1) ^ 1, kAttnPolls);
         }
+#pragma unroll 1
         for (int X = 0; X < 2; ++X)
-          if (loads[X]) mbar_wait(&B.q_full[X], (loads[X] - 1) & 1, kPolls);
+          if (loads[X]) mbar_wait(&B.q_full[X], (loads[X] - 1) & 1, kAttnPolls);
       }
     }
     // ---------------------------------------------------------------- products
+    // Nothing that this warp issued is still running when TMEM is freed.
+    auto finish = [&](uint32_t el, uint64_t* bar) {
+      mma_commit(el, bar);
+      if (!mbar_wait(bar, 0, kAttnPolls)) set_status(p.status, GDN_DEV_TIMEOUT);
+    };
     if (kBufs == 2 && warp == 9) {
       constexpr uint32_t kIdS = idesc_bf16_f32(128, kKeys);
       constexpr uint32_t kIdO = idesc_bf16_f32(128, D, false, true);
@@ -741,7 +766,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           mma_ss(el, tm + X * 128, q_lo + X * kT + (((d >> 6) * 16384 + (d & 63) * 2) >> 4), kQHi,
                  b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kKHi, kIdS, d > 0);
         mma_commit(el, &B.s_full[X][0]);
-        if (last) mma_commit(el, &B.q_empty[X]);
+        if (last) mma_commit(wait.ok() ? el : 0u, &B.q_empty[X]);
       };
       auto weigh = [&](auto x, uint32_t st, bool first, bool last) {  // O_X (+)= P_X V
         constexpr int X = decltype(x)::value;
@@ -766,8 +791,9 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       // The fields of item k that count here (no tiles: the end).
       auto item = [&](uint32_t k, int& a, int& b, int& mask0) {
         wait(&B.item_full[k % kItems], k / kItems);
+        if (p.stall == k + 1) wait(&B.idle[0], 0);
         const AttnItem& it = B.item[k % kItems];
-        const bool ok = it.valid && wait.ok();
+        const bool ok = !done(it);
         a = (int)uniform(ok ? it.nA : 0);
         b = (int)uniform(ok ? it.nB : 0);
         mask0 = (int)uniform(it.mask0);
@@ -786,7 +812,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           wait_q(1);
           scores(Bt, 0, nB == 1);
         }
-        mma_commit(el, &B.kv_empty[0]);
+        mma_commit(wait.ok() ? el : 0u, &B.kv_empty[0]);
       }
       for (uint32_t k = 1; nA; ++k) {
         const int n = max(nA, nB);
@@ -807,20 +833,21 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           }
           if (!end) wait_v(nst + 1, j + 1 >= mask0);
           if (j < nB) weigh(Bt, vst, j == 0, j == nB - 1);
-          mma_commit(el, &B.kv_empty[vst]);
+          mma_commit(wait.ok() ? el : 0u, &B.kv_empty[vst]);
           if (j + 1 < nB) {
             scores(Bt, nst, j + 2 == nB);
           } else if (end && b2) {
             wait_q(1);
             scores(Bt, nst, b2 == 1);
           }
-          if (k_next) mma_commit(el, &B.kv_empty[nst]);
+          if (k_next) mma_commit(wait.ok() ? el : 0u, &B.kv_empty[nst]);
           kst = nst;
         }
         nA = a2;
         nB = b2;
         mask0 = m2;
       }
+      finish(el, &B.idle[0]);
     }
     // Three score buffers: warp 9 issues Q K^T, warp 11 P V, in the same sequence.
     if (kBufs == 3 && (warp == 9 || warp == 11)) {
@@ -857,7 +884,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
                    b + (((d >> 6) * S::kHalf + (d & 63) * 2) >> 4), kKHi, idesc_bf16_f32(128, kKeys),
                    d > 0);
           mma_commit(el, &B.s_full[X][own[X]]);
-          if (j == n - 1) mma_commit(el, &B.q_empty[X]);
+          if (j == n - 1) mma_commit(wait.ok() ? el : 0u, &B.q_empty[X]);
         } else {
           if (first && masked) {
             wait(&B.v_fixed[st], fixes >> st);
@@ -882,7 +909,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           mma_commit(el, &B.buf_empty[buf]);
         }
         if (end) {  // the last product of this key tile
-          mma_commit(el, &B.kv_empty[st]);
+          mma_commit(wait.ok() ? el : 0u, &B.kv_empty[st]);
           st = st + 2 >= kStages ? st + 2 - kStages : st + 2;
         }
         if (++buf == kBufs) {
@@ -896,8 +923,9 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       };
       for (uint32_t k = 0;; ++k) {
         wait(&B.item_full[k % kItems], k / kItems);
+        if (qk && p.stall == k + 1) wait(&B.idle[0], 0);
         const AttnItem& it = B.item[k % kItems];
-        const bool ok = it.valid && wait.ok();
+        const bool ok = !done(it);
         const int nA = (int)uniform(ok ? it.nA : 0), nB = (int)uniform(ok ? it.nB : 0);
         const int mask0 = (int)uniform(it.mask0);
         arrive_one(el, &B.item_empty[k % kItems]);
@@ -907,6 +935,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
           if (j < nB) step(std::integral_constant<int, 1>{}, j, nB, j >= nA, true, j >= mask0);
         }
       }
+      finish(el, &B.idle[qk ? 0 : 1]);
     }
     // ---------------------------------------------------------------- work items
     if (warp == 10) {
@@ -925,13 +954,14 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         const int64_t idx = (int64_t)k * grid + ((k & 1) ? grid - 1 - b : b);
         const AttnItem it = items.get((int)min(idx, (int64_t)items.total), nt);
         wait(&B.item_empty[k % kItems], k / kItems + 1);
+        if (__any_sync(0xffffffffu, !wait.ok())) break;
         if (lane == 0) {
           B.item[k % kItems] = it;
           mbar_arrive(&B.item_full[k % kItems]);
         }
         __syncwarp();
         // a round dealt backwards may skip this CTA in the last, partial round only
-        if (!it.valid || !wait.ok()) break;
+        if (!it.valid) break;
       }
     }
     __syncwarp();
@@ -945,7 +975,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
       const AttnItem it = B.item[k % kItems];
       __syncwarp();
       if (lane == 0) mbar_arrive(&B.item_empty[k % kItems]);
-      if (!it.valid || !wait.ok()) break;
+      if (done(it)) break;
       const int n = max(it.nA, it.nB);
       for (int j = it.mask0; j < n; ++j) {
         const uint32_t st = (base + 2 * j + 1) % kStages;
@@ -992,7 +1022,7 @@ attn_tc_kernel(const AttnParams p, const PrefixParts parts,
         if (found) *reinterpret_cast<volatile int*>(&B.poison[k & 7]) = (int)k + 1;
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.v_fixed[st]);
+        if (lane == 0 && wait.ok()) mbar_arrive(&B.v_fixed[st]);
       }
       base += 2 * n;
     }

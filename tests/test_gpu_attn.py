@@ -910,6 +910,44 @@ def test_memory_between_captured_and_other_streams(call):
     assert all(torch.equal(a, given[n]) for a, n in zip(want, shapes))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("call", ["prefill", "decode"])
+@pytest.mark.parametrize("item", [0, 1, 2])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_next_call_right(call, D, item):
+    """The testing hook has the warp that issues the products wait, before a CTA's first, second
+    or third work item, for an event that never happens: the call returns with GDN_DEV_TIMEOUT,
+    and with the hook off the same call on the same buffers gives its results again."""
+    g = torch.Generator().manual_seed(51)
+    status = torch.full((1,), -1, dtype=torch.int32, device="cuda")
+    if call == "prefill":
+        q, k, v = (randn(g, 20000, h, D).cuda() for h in (16, 4, 4))
+        cu = torch.tensor([0, 7000, 7001, 20000], dtype=torch.int32, device="cuda")
+        run = lambda out: B.gdn_attn_prefill(q, k, v, cu, out=out, status=status)
+    else:
+        shared, N, Hk = 1024, 700, 4  # 700 items of the prefix: 175 pairs of row tiles x 4
+        kc, vc = (randn(g, 64, Hk, 64, D).cuda() for _ in range(2))
+        table = torch.randint(0, 64, (N, 20), generator=g, dtype=torch.int32)
+        table[:, :16] = table[0, :16]
+        q, table = randn(g, N, 4, 64, D).cuda(), table.cuda()
+        kv = (1024 + torch.randint(5, 250, (N,), generator=g)).to(torch.int32).cuda()
+        run = lambda out: B.gdn_attn_decode(q, kc, vc, table, kv, shared, out=out, status=status)
+    want = torch.zeros_like(q)
+    out = torch.zeros_like(q)
+    B.gdn_test_attn_prefix(True)
+    try:
+        run(want)
+        assert status.item() == 0
+        B.gdn_test_attn_timeout(256, item)
+        run(out)
+        assert status.item() & 8
+        B.gdn_test_attn_timeout(0)
+        run(out)
+        assert status.item() == 0 and torch.equal(out, want)
+    finally:
+        B.gdn_test_attn_timeout(0)
+        B.gdn_test_attn_prefix(False)
+
+
 # ---------------------------------------------------------------- together
 def test_prompt_then_decode_equals_a_longer_prompt():
     """front + prefill of a prompt, then front + decode of the next tokens, give the rows that
