@@ -49,7 +49,9 @@ class GdnError(RuntimeError):
     def __init__(self, status: int, what: str = ""):
         self.status = status
         msg = f"{what}: " if what else ""
-        super().__init__(f"{msg}libgdn status {status} ({status_string(status)})")
+        # (without loading the library: a missing one is reported from under load_library's lock)
+        text = status_string(status) if _lib is not None else "library not loaded"
+        super().__init__(f"{msg}libgdn status {status} ({text})")
 
 
 class GdnDesc(ctypes.Structure):
@@ -149,7 +151,7 @@ def load_library(path: str = LIB_PATH):
 
 def status_string(status: int) -> str:
     try:
-        return load_library().gdn_status_string(int(status)).decode()
+        return (_lib or load_library()).gdn_status_string(int(status)).decode()
     except Exception:
         return "unknown"
 

@@ -185,6 +185,28 @@ def test_binding_refuses_tensors_of_another_device(call, shapes, rest, away):
         getattr(B, f"gdn_attn_{call}")(**a, **rest)
 
 
+@pytest.mark.parametrize("what", ["library", "module"])
+def test_missing_builds_are_errors_at_once(what, lib, monkeypatch, tmp_path):
+    import threading
+    monkeypatch.setattr(B, "_lock", threading.Lock())
+    monkeypatch.setattr(B, "_attn_module", None)
+    monkeypatch.setattr(B, "_PKG", str(tmp_path))
+    monkeypatch.setattr(B.build, "MODULE", str(tmp_path / "_attn_torch.so")) if hasattr(B, "build") else None
+    if what == "library":
+        monkeypatch.setattr(B, "_lib", None)
+    seen = []
+
+    def call():
+        try:
+            B.load_library(str(tmp_path / "libgdn.so")) if what == "library" else B._attn()
+        except B.GdnError as e:
+            seen.append(str(e))
+    t = threading.Thread(target=call, daemon=True)
+    t.start()
+    t.join(10)
+    assert not t.is_alive() and len(seen) == 1 and "missing (build it" in seen[0]
+
+
 # ---------------------------------------------------------------- rotary table
 def test_rope_table_plain():
     t = rope_table(50, 8, base=100.0, device="cpu")
