@@ -17,6 +17,8 @@ from typing import Optional
 
 import torch
 
+from . import build
+
 _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
 
@@ -508,14 +510,17 @@ _attn_module = None
 
 def _attn():
     """The compiled marshalling of the attention calls (csrc/attn_torch.cpp), bound to the
-    loaded library. Raises if it has not been built."""
+    loaded library. Raises if it has not been built, or for another torch or Python."""
     global _attn_module
     lib = load_library()
     with _lock:
         if _attn_module is None:
-            path = os.path.join(_PKG, "_attn_torch.so")
+            path, abi = build.MODULE, build.module_abi()
             if not os.path.exists(path):
                 raise GdnError(-6, f"{path} is missing (build it with __graft_entry__.build())")
+            if build.module_built_for() != abi:
+                raise GdnError(-6, f"{path} was not built for {abi} (build it with "
+                                   "__graft_entry__.build())")
             spec = importlib.util.spec_from_file_location("_attn_torch", path)
             module = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(module)

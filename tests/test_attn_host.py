@@ -191,7 +191,7 @@ def test_missing_builds_are_errors_at_once(what, lib, monkeypatch, tmp_path):
     monkeypatch.setattr(B, "_lock", threading.Lock())
     monkeypatch.setattr(B, "_attn_module", None)
     monkeypatch.setattr(B, "_PKG", str(tmp_path))
-    monkeypatch.setattr(B.build, "MODULE", str(tmp_path / "_attn_torch.so")) if hasattr(B, "build") else None
+    monkeypatch.setattr(B.build, "MODULE", str(tmp_path / "_attn_torch.so"))
     if what == "library":
         monkeypatch.setattr(B, "_lib", None)
     seen = []
@@ -205,6 +205,63 @@ def test_missing_builds_are_errors_at_once(what, lib, monkeypatch, tmp_path):
     t.start()
     t.join(10)
     assert not t.is_alive() and len(seen) == 1 and "missing (build it" in seen[0]
+
+
+# ---------------------------------------------------------------- the compiled marshalling
+def test_module_of_another_torch_is_stale_and_refused(monkeypatch, lib):
+    """The module is built against one torch and one Python: with others in their place it is
+    built again, and until then not loaded."""
+    from gated_delta_rule_chunk_gb300 import build as M
+    assert M.module_up_to_date()
+    monkeypatch.setattr(M, "module_abi", lambda: "another torch")
+    assert not M.module_up_to_date()
+    monkeypatch.setattr(B, "_attn_module", None)
+    with pytest.raises(B.GdnError, match="build it"):
+        B.gdn_attn_prefill(None, None, None)
+
+
+@pytest.fixture
+def small_build(monkeypatch, tmp_path):
+    """build() of one small source into an empty folder."""
+    from gated_delta_rule_chunk_gb300 import build as M
+    src = tmp_path / "one.cu"
+    src.write_text('extern "C" int one() { return 1; }\n')
+    monkeypatch.setattr(M, "_sources", lambda: [str(src)])
+    for name, file in (("LIB", "libone.so"), ("BUILD", "_build"), ("MODULE", "_module.so"),
+                       ("MODULE_STAMP", "_module.abi")):
+        monkeypatch.setattr(M, name, str(tmp_path / file), raising=False)
+    return M, tmp_path
+
+
+def works(path):
+    return ctypes.CDLL(str(path)).one() == 1
+
+
+def test_library_is_built_without_torch(small_build, monkeypatch, capfd):
+    import sys
+    M, out = small_build
+    monkeypatch.setitem(sys.modules, "torch", None)
+    M.build()
+    assert works(out / "libone.so") and not (out / "_module.so").exists()
+    assert "torch" in capfd.readouterr().err
+    M.build()  # and again, with the library up to date
+
+
+def test_library_is_built_without_python_headers(small_build, monkeypatch, tmp_path):
+    M, out = small_build
+    monkeypatch.setattr(M.sysconfig, "get_paths", lambda: {"include": str(tmp_path / "none")})
+    M.build()
+    assert works(out / "libone.so") and not (out / "_module.so").exists()
+
+
+def test_module_that_does_not_compile_leaves_the_library(small_build, monkeypatch):
+    M, out = small_build
+    bad = out / "bad.cpp"
+    bad.write_text("#error no\n")
+    monkeypatch.setattr(M, "MODULE_SRC", str(bad))
+    with pytest.raises(RuntimeError, match="bad.cpp"):
+        M.build()
+    assert works(out / "libone.so") and not (out / "_module.so").exists()
 
 
 # ---------------------------------------------------------------- rotary table
