@@ -67,6 +67,12 @@ double real(PyObject* o) {
   return v;
 }
 
+bool truth(PyObject* o) {
+  const int v = PyObject_IsTrue(o);
+  if (v < 0) throw python_error();
+  return v != 0;
+}
+
 int32_t dtype_code(at::ScalarType t) {
   if (t == at::kFloat) return GDN_F32;
   if (t == at::kBFloat16) return GDN_BF16;
@@ -196,6 +202,7 @@ PyObject* front(PyObject*, PyObject* const* a, Py_ssize_t n) {
   same_device(x, "x", {{a[4], "q_weight"}, {a[5], "k_weight"}, {a[7], "rope"}, {a[9], "cu_seqlens"},
                        {a[10], "kv_lens"}, {a[11], "page_table"}, {a[12], "k_cache"},
                        {a[13], "v_cache"}, {a[16], "q"}, {a[17], "k"}, {a[18], "v"}, {a[19], "status"}});
+  const bool interleaved = truth(a[8]), dense = truth(a[14]);
   const int64_t N = num_seqs(cu);
   const at::ScalarType out =
       dtype_or(a[15], kc ? kc->scalar_type() : q_in ? q_in->scalar_type() : x.scalar_type());
@@ -211,13 +218,12 @@ PyObject* front(PyObject*, PyObject* const* a, Py_ssize_t n) {
   d.T = i32(T); d.N = i32(N); d.H = i32(H); d.Hk = i32(Hk); d.D = i32(D);
   d.page_size = i32(page); d.n_pages = i32(pages); d.max_pages = i32(cols);
   d.rot_dim = rope ? i32(rope->size(1)) : 0; d.max_pos = rope ? i32(rope->size(0)) : 0;
-  d.flags = PyObject_IsTrue(a[8]) ? GDN_ATTN_ROPE_INTERLEAVED : 0;
+  d.flags = interleaved ? GDN_ATTN_ROPE_INTERLEAVED : 0;
   d.norm_eps = (float)real(a[6]);
   d.status = static_cast<int32_t*>(address(status, "status", kI32, {}));
   const void* px = address(&x, "x", x.scalar_type(), {T, (H + 2 * Hk) * D});
   const at::Tensor *qw = tensor(a[4], "q_weight"), *kw = tensor(a[5], "k_weight");
   const Place place(a[20], x);
-  const bool dense = PyObject_IsTrue(a[14]);
   at::Tensor q = made(a[16], "q", {T, H, D}, out, x, place), k, v;
   if (dense) {
     k = made(a[17], "k", {T, Hk, D}, out, x, place);
@@ -262,6 +268,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
                    *out_in = tensor(a[6], "out");
   same_device(q, "q", {{a[1], "k"}, {a[2], "v"}, {a[3], "cu_seqlens"}, {a[6], "out"}, {a[8], "lse"},
                        {a[9], "status"}});
+  const bool return_lse = truth(a[7]), want_lse = return_lse || a[8] != Py_None;
   const int64_t T = q.size(0), H = q.size(1), D = q.size(2), Hk = k.size(1);
   const at::ScalarType t = q.scalar_type(),
                        to = dtype_or(a[5], out_in ? out_in->scalar_type() : t);
@@ -273,7 +280,6 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const void* pq = address(&q, "q", t, {});
   const Place place(a[10], q);
   at::Tensor out = made(a[6], "out", {T, H, D}, to, q, place), lse;
-  const bool want_lse = PyObject_IsTrue(a[7]) || a[8] != Py_None;
   if (want_lse) lse = made(a[8], "lse", {T, H}, kF32, q, place);
   place.order();
   const int rc = f_prefill(&d, pq, address(&k, "k", t, {T, Hk, D}), address(&v, "v", t, {T, Hk, D}),
@@ -282,7 +288,7 @@ PyObject* prefill(PyObject*, PyObject* const* a, Py_ssize_t n) {
                            static_cast<float*>(address(want_lse ? &lse : nullptr, "lse", kF32, {T, H})),
                            place.stream);
   if (rc != GDN_OK) fail(rc, "gdn_attn_prefill");
-  return with_lse(out, PyObject_IsTrue(a[7]) ? &lse : nullptr);
+  return with_lse(out, return_lse ? &lse : nullptr);
   END_HANDLE_TH_ERRORS
 }
 
@@ -297,6 +303,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   same_device(q, "q", {{a[1], "k_cache"}, {a[2], "v_cache"}, {a[3], "page_table"}, {a[4], "kv_lens"},
                        {a[8], "out"}, {a[10], "lse"}, {a[11], "workspace"}, {a[12], "status"}});
   const at::Tensor *status = tensor(a[12], "status"), *out_in = tensor(a[8], "out");
+  const bool return_lse = truth(a[9]), want_lse = return_lse || a[10] != Py_None;
   const int64_t N = q.size(0), nq = q.dim() == 3 ? 1 : q.size(1), H = q.size(-2), D = q.size(-1);
   const int64_t pages = kc.size(0), Hk = kc.size(1), page = kc.size(2), cols = table.size(1);
   const at::ScalarType t = q.scalar_type(),
@@ -311,7 +318,6 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const Place place(a[13], q);
   at::Tensor out = made(a[8], "out", q.sizes(), to, q, place), lse, work;
   const at::IntArrayRef rows = q.sizes().slice(0, q.dim() - 1);
-  const bool want_lse = PyObject_IsTrue(a[9]) || a[10] != Py_None;
   if (want_lse) lse = made(a[10], "lse", rows, kF32, q, place);
   if (const at::Tensor* w = tensor(a[11], "workspace")) {
     work = *w;
@@ -331,7 +337,7 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
                           static_cast<float*>(address(want_lse ? &lse : nullptr, "lse", kF32, rows)),
                           place.stream);
   if (rc != GDN_OK) fail(rc, "gdn_attn_decode");
-  return with_lse(out, PyObject_IsTrue(a[9]) ? &lse : nullptr);
+  return with_lse(out, return_lse ? &lse : nullptr);
   END_HANDLE_TH_ERRORS
 }
 

@@ -185,6 +185,25 @@ def test_binding_refuses_tensors_of_another_device(call, shapes, rest, away):
         getattr(B, f"gdn_attn_{call}")(**a, **rest)
 
 
+@pytest.mark.parametrize("call, flag", [("front", "interleaved"), ("front", "output_kv"),
+                                        ("prefill", "return_lse"), ("decode", "return_lse")])
+def test_flags_without_a_truth_value_are_errors(call, flag):
+    """(stand-ins without memory: the error comes before anything is allocated or enqueued)"""
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    class Neither:
+        def __bool__(self):
+            raise ZeroDivisionError
+    with FakeTensorMode():
+        x = torch.empty(8, 6 * 128, dtype=torch.bfloat16, device="cuda:0")
+        q, k = (torch.empty(8, h, 128, dtype=torch.bfloat16, device="cuda:0") for h in (4, 1))
+        kc = torch.empty(5, 1, 16, 128, dtype=torch.bfloat16, device="cuda:0")
+        table, kv = (torch.empty(n, dtype=torch.int32, device="cuda:0") for n in ((8, 4), (8,)))
+    args = dict(front=(x, 4, 1, 128), prefill=(q, k, k), decode=(q, kc, kc, table, kv))[call]
+    with pytest.raises(ZeroDivisionError):
+        getattr(B, f"gdn_attn_{call}")(*args, **{flag: Neither()})
+
+
 @pytest.mark.parametrize("what", ["library", "module"])
 def test_missing_builds_are_errors_at_once(what, lib, monkeypatch, tmp_path):
     import threading
