@@ -32,9 +32,9 @@
 //
 // Bound: at D = 128 the chain of a step (scores, weights, products; 2,600 cycles, 2,048 of them
 // MMAs); short prompts by the start and the output of an item, about 2.3 steps. Measured
-// (GB300): 16384 tokens x 32 heads 1.27 ms (1,730 TFLOP/s; 1.39 ms under the power limit), 4096
-// x 16 heads 52 us (1,320 TFLOP/s), 8 ragged prompts x 32 heads 62.1 us (968 TFLOP/s), 4001 x 16
-// heads of 64 39.6 us (828 TFLOP/s).
+// (GB300): 16384 tokens x 32 heads 1.25 to 1.27 ms (1,740 TFLOP/s; 1.39 ms under the power limit),
+// 4096 x 16 heads 51.3 us (1,340 TFLOP/s), 8 ragged prompts x 32 heads 62.5 us (963 TFLOP/s), 4001
+// x 16 heads of 64 40.1 us (819 TFLOP/s).
 #pragma once
 
 #include <cuda.h>

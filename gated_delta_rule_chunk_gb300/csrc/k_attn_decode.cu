@@ -20,8 +20,8 @@
 // replaced when outgrown by 2^8, as in attn_tc.cuh; rounded to bf16 for the second product,
 // summed in fp32 before that.
 //
-// Measured (GB300): 64 sequences of up to 8192 keys 148.5 to 152 us (6.8 TB/s), one of 8191 keys
-// 10.0 us, 64 behind 16384 shared keys 53 to 58 us.
+// Measured (GB300): 64 sequences of up to 8192 keys 148.5 to 153 us (6.8 TB/s), one of 8191 keys
+// 10.1 us, 64 behind 16384 shared keys 53 to 58 us.
 #include "attn_tc.cuh"
 
 namespace gdn {
@@ -613,8 +613,8 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   // them in WM row tiles at warp-MMA speed. What counts is how many keys that is, of either head
   // size. Measured (GB300; thousands of keys read again, with / without the prefix kernel):
   // 84 17.7 / 14.3 us, 129 15.4 / 15.0, 172 27.3 / 24.7, 188 17.9 / 20.4, 224 17.7 / 21.5,
-  // 429 17.4 / 29.9; D = 64: 157 20.9 / 20.7, 237 15.1 / 18.1, 396 15.6 / 24.1; four row tiles
-  // behind a short prefix: 199 24.3 / 20.8.
+  // 429 17.4 / 29.9; D = 64: 157 20.9 / 20.7, 237 15.1 / 18.1, 396 15.6 / 24.1. One point is on
+  // the wrong side of the rule: four row tiles behind a short prefix, 199, 24.3 / 20.8.
   const int R = p.nq * p.G, WM = R <= 16 ? 1 : R <= 32 ? 2 : 4;
   const int64_t again = (int64_t)(p.N - 1) * p.common * p.Hk * WM;
   p.shared = p.n_pages > 0 && p.N > 1 && (again >= 180000 || attn_prefix_always())

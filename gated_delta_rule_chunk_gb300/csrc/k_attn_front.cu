@@ -13,9 +13,9 @@
 // group takes R heads of one token, all loaded before anything waits, with one lookup of the
 // token's sequence, position and page and one load of its cos/sin. Bound: HBM for long
 // prompts; latency (cu_seqlens -> kv_lens -> page table and rotary row -> store, x loaded
-// meanwhile) for a decode step. Measured (GB300): 8 prompts to 2048 in 32 bits 27.0 us (6.3 TB/s),
-// 4096 tokens in bf16 with dense and cached k and v 11.3 us (4.1 TB/s, issue-bound), one token
-// 2.4 us.
+// meanwhile) for a decode step. Measured (GB300): 8 prompts to 2048 in 32 bits 27.3 us (6.2 TB/s),
+// 4096 tokens in bf16 with dense and cached k and v 12.1 us (3.9 TB/s: 8-byte accesses and their
+// latency at 16 warps an SM), one token 2.3 us.
 #include "attn_common.cuh"
 
 namespace gdn {
@@ -242,7 +242,7 @@ bool launch(const AttnFrontParams& p, cudaStream_t s) {
   const int per_block = kThreads / (D / 8);
   const int64_t rows = (int64_t)p.T * (p.H + 2 * p.Hk);
   // Two heads per lane group where there is work for all SMs, so that the lookups serve both
-  // (4096 tokens x 20 heads: 11.3 us; one head 15.2 us, four 11.9 us, eight 14.9 us); one head
+  // (4096 tokens x 20 heads: 12.1 us; one head 15.8 us, four 13.3 us, eight 15.1 us); one head
   // where there is not, as in a decode step.
   const bool wide = rows >= 8 * 152 * 16;
   const int64_t items = wide ? (int64_t)p.T * ((p.H + 1) / 2 + p.Hk) : rows;
