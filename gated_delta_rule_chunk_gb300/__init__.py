@@ -13,6 +13,8 @@ __all__ = [
     "gdn_chunk_fwd", "gdn_build_chunk_indices", "gdn_workspace_size",
     "gdn_read_status", "gdn_status_string", "GdnError", "load_library",
     "gdn_attn_front", "gdn_attn_prefill", "gdn_attn_decode", "gdn_attn_workspace_size",
+    "gdn_attn_append8", "gdn_attn_prefill_weights", "gdn_attn_evict",
+    "gdn_attn_decode_cache_workspace_size", "gdn_attn_prefill_weights_workspace_size",
     "rope_table",
 ]
 

@@ -42,7 +42,10 @@ EXPORTED = ("gdn_check_desc", "gdn_nt_max", "gdn_workspace_size", "gdn_build_chu
             "gdn_recurrent_fwd", "gdn_conv_front", "gdn_bwd_workspace_size", "gdn_chunk_bwd",
             "gdn_attn_check_desc", "gdn_attn_workspace_size", "gdn_attn_front",
             "gdn_attn_prefill", "gdn_attn_decode", "gdn_test_attn_prefix", "gdn_test_attn_tiles",
-            "gdn_test_attn_timeout")
+            "gdn_test_attn_timeout", "gdn_attn_front_axes", "gdn_attn_append8",
+            "gdn_attn_decode_cache", "gdn_attn_decode_cache_workspace_size",
+            "gdn_attn_prefill_weights", "gdn_attn_prefill_weights_workspace_size",
+            "gdn_attn_evict")
 GDN_NOALLOC_SCRATCH_BYTES = 64 << 20
 GDN_ATTN_ROPE_INTERLEAVED = 1
 
@@ -137,6 +140,21 @@ def load_library(path: str = LIB_PATH):
         lib.gdn_test_attn_tiles.restype = None
         lib.gdn_test_attn_timeout.argtypes = [ctypes.c_uint32, ctypes.c_uint32]
         lib.gdn_test_attn_timeout.restype = None
+        f32 = ctypes.c_float
+        lib.gdn_attn_front_axes.argtypes = [P(GdnAttnDesc)] + [vp] * 7 + [i32] + [vp] * 8
+        lib.gdn_attn_front_axes.restype = ctypes.c_int
+        lib.gdn_attn_append8.argtypes = [P(GdnAttnDesc)] + [vp] * 10
+        lib.gdn_attn_append8.restype = ctypes.c_int
+        lib.gdn_attn_decode_cache.argtypes = [P(GdnAttnDesc)] + [vp] * 7 + [i32, f32] + [vp] * 4
+        lib.gdn_attn_decode_cache.restype = ctypes.c_int
+        lib.gdn_attn_decode_cache_workspace_size.argtypes = [P(GdnAttnDesc), i32]
+        lib.gdn_attn_decode_cache_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_attn_prefill_weights.argtypes = [P(GdnAttnDesc)] + [vp] * 5 + [i32, f32, vp, vp]
+        lib.gdn_attn_prefill_weights.restype = ctypes.c_int
+        lib.gdn_attn_prefill_weights_workspace_size.argtypes = [P(GdnAttnDesc)]
+        lib.gdn_attn_prefill_weights_workspace_size.restype = ctypes.c_size_t
+        lib.gdn_attn_evict.argtypes = [P(GdnAttnDesc)] + [vp] * 8 + [i32] * 3 + [vp] * 3
+        lib.gdn_attn_evict.restype = ctypes.c_int
         lib.gdn_attn_prefill.argtypes = [P(GdnAttnDesc), vp, vp, vp, vp, ctypes.c_float, vp, vp,
                                          vp]
         lib.gdn_attn_prefill.restype = ctypes.c_int
@@ -526,7 +544,10 @@ def _attn():
             spec.loader.exec_module(module)
             module.init(GdnError, *(ctypes.cast(f, ctypes.c_void_p).value for f in (
                 lib.gdn_attn_front, lib.gdn_attn_prefill, lib.gdn_attn_decode,
-                lib.gdn_attn_workspace_size, lib.gdn_attn_check_desc)))
+                lib.gdn_attn_workspace_size, lib.gdn_attn_check_desc, lib.gdn_attn_front_axes,
+                lib.gdn_attn_append8, lib.gdn_attn_decode_cache,
+                lib.gdn_attn_decode_cache_workspace_size, lib.gdn_attn_prefill_weights,
+                lib.gdn_attn_prefill_weights_workspace_size, lib.gdn_attn_evict)))
             _attn_module = module
         return _attn_module
 
@@ -548,6 +569,15 @@ def gdn_attn_workspace_size(desc: GdnAttnDesc) -> int:
     return int(load_library().gdn_attn_workspace_size(ctypes.byref(desc)))
 
 
+def gdn_attn_decode_cache_workspace_size(desc: GdnAttnDesc, with_weights: bool) -> int:
+    return int(load_library().gdn_attn_decode_cache_workspace_size(ctypes.byref(desc),
+                                                                   1 if with_weights else 0))
+
+
+def gdn_attn_prefill_weights_workspace_size(desc: GdnAttnDesc) -> int:
+    return int(load_library().gdn_attn_prefill_weights_workspace_size(ctypes.byref(desc)))
+
+
 def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
                    q_weight: Optional[torch.Tensor] = None,
                    k_weight: Optional[torch.Tensor] = None, norm_eps: float = 0.0,
@@ -559,7 +589,8 @@ def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
                    output_kv: bool = True, out_dtype: Optional[torch.dtype] = None,
                    q: Optional[torch.Tensor] = None, k: Optional[torch.Tensor] = None,
                    v: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None,
-                   stream=None):
+                   stream=None, positions: Optional[torch.Tensor] = None,
+                   rope_axes: Optional[torch.Tensor] = None):
     """Front end of an attention layer through the C ABI.
 
     x [T, (H + 2 Hk) * D] (fp32 or bf16), channels q | k | v. Per head of q and k: RMS norm
@@ -571,11 +602,16 @@ def gdn_attn_front(x: torch.Tensor, H: int, Hk: int, D: int,
     out_dtype (fp32 or bf16) defaults to the cache's, else to x's. Returns (q [T, H, D], k,
     v [T, Hk, D]), the last two None when output_kv is false; q, k, v may be given. `status`,
     if given, is one int32 on the device that receives the device status word.
+
+    With positions (int32 [n_axes, T], n_axes up to 8), pair i turns by the table's row
+    positions[rope_axes[i], t] (rope_axes uint8 [rope.shape[1] / 2]; None: all by the first) in
+    place of the token's place in the cache: axes of time, row and column for images and video,
+    or positions after an eviction.
     """
     return (_attn_module or _attn()).front(
         x, H, Hk, D, q_weight, k_weight, norm_eps, rope, interleaved, cu_seqlens, kv_lens,
         page_table, k_cache, v_cache, output_kv, out_dtype, q, k, v, status,
-        None if stream is None else stream.cuda_stream)
+        None if stream is None else stream.cuda_stream, positions, rope_axes)
 
 
 def gdn_attn_prefill(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor,
@@ -596,16 +632,76 @@ def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     scale: Optional[float] = None, out_dtype: Optional[torch.dtype] = None,
                     out: Optional[torch.Tensor] = None, return_lse: bool = False,
                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
-                    status: Optional[torch.Tensor] = None, stream=None):
+                    status: Optional[torch.Tensor] = None, stream=None,
+                    k_scale: Optional[torch.Tensor] = None, v_scale: Optional[torch.Tensor] = None,
+                    weights: Optional[torch.Tensor] = None):
     """Decode attention over the paged cache through the C ABI: q [N, H, D] (one token a
     sequence) or [N, n_q, H, D] bf16; k_cache, v_cache [n_pages, Hk, page_size, D] bf16;
     page_table int32 [N, max_pages]; kv_lens int32 [N], the call's tokens included. The first
     shared_len tokens (a multiple of page_size) are the same pages for every sequence and are
     read once for all. `workspace` (uint8, gdn_attn_workspace_size bytes) is allocated when
-    not given. Returns out with q's shape, or (out, lse) when return_lse."""
+    not given. Returns out with q's shape, or (out, lse) when return_lse.
+
+    With k_scale and v_scale (fp32 [n_pages, Hk, page_size / 16]) the caches are in 8 bits
+    (torch.float8_e4m3fn, see gdn_attn_append8). With `weights` (fp32 [n_pages, Hk, page_size])
+    each key's softmax weights, summed over the call's rows and its group's query heads, are added
+    there; the call's own tokens are set to theirs (shared_len must be 0 then). A workspace is
+    gdn_attn_decode_cache_workspace_size bytes with either."""
     return (_attn_module or _attn()).decode(
         q, k_cache, v_cache, page_table, kv_lens, shared_len, scale, out_dtype, out, return_lse,
-        lse, workspace, status, None if stream is None else stream.cuda_stream)
+        lse, workspace, status, None if stream is None else stream.cuda_stream, k_scale, v_scale,
+        weights)
+
+
+def gdn_attn_append8(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor,
+                     v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                     page_table: torch.Tensor, kv_lens: Optional[torch.Tensor] = None,
+                     cu_seqlens: Optional[torch.Tensor] = None,
+                     status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """Appends k and v [T, Hk, D] (bf16 or fp32, as gdn_attn_front returns them) to a cache in 8
+    bits through the C ABI: k_cache, v_cache torch.float8_e4m3fn [n_pages, Hk, page_size, D],
+    k_scale, v_scale fp32 [n_pages, Hk, page_size / 16], a power of two for each 16 tokens and
+    head. page_table int32 [N, max_pages]; kv_lens int32 [N], the call's tokens included (None:
+    they are the sequence's first); cu_seqlens int32 [N + 1] or None (one sequence). A block's
+    scale grows with its tokens, whose elements are then rounded again."""
+    (_attn_module or _attn()).append8(
+        k, v, k_cache, v_cache, k_scale, v_scale, page_table, kv_lens, cu_seqlens, status,
+        None if stream is None else stream.cuda_stream)
+
+
+def gdn_attn_prefill_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor,
+                             weights: torch.Tensor, page_table: torch.Tensor,
+                             cu_seqlens: Optional[torch.Tensor] = None, window: int = 0,
+                             scale: Optional[float] = None,
+                             workspace: Optional[torch.Tensor] = None,
+                             status: Optional[torch.Tensor] = None, stream=None) -> None:
+    """The weight that prompts' rows give their keys, through the C ABI: q [T, H, D], k
+    [T, Hk, D] bf16 and lse fp32 [T, H] of gdn_attn_prefill; weights fp32 [n_pages, Hk, page_size]
+    is set, at the places that page_table int32 [N, max_pages] gives the prompts' tokens (the first
+    of their sequences), to the sum of their softmax weights over all rows (window = 0) or the last
+    `window` rows of each prompt, and over the query heads of the group."""
+    (_attn_module or _attn()).prefill_weights(
+        q, k, lse, weights, page_table, cu_seqlens, window, scale, workspace, status,
+        None if stream is None else stream.cuda_stream)
+
+
+def gdn_attn_evict(k_cache: torch.Tensor, v_cache: torch.Tensor, weights: torch.Tensor,
+                   page_table: torch.Tensor, kv_lens: torch.Tensor, new_table: torch.Tensor,
+                   keep: int, recent: int = 0, k_scale: Optional[torch.Tensor] = None,
+                   v_scale: Optional[torch.Tensor] = None,
+                   new_lens: Optional[torch.Tensor] = None, kept: Optional[torch.Tensor] = None,
+                   status: Optional[torch.Tensor] = None, stream=None):
+    """Cuts sequences to `keep` tokens through the C ABI: the last `recent` ones and, per key head,
+    those of largest weight among the others (equal weights: the lower index), copied in their
+    order, with their weights, to the pages of new_table int32 [N, new_max_pages], which must be
+    pages that no sequence of the call uses. k_cache, v_cache [n_pages, Hk, page_size, D] bf16, or
+    torch.float8_e4m3fn with k_scale and v_scale; weights fp32 [n_pages, Hk, page_size]; page_table
+    int32 [N, max_pages]; kv_lens int32 [N]. Returns (new_lens int32 [N], which may be given as
+    kv_lens itself, and kept int32 [N, Hk, keep]: the places that the tokens had, -1 past the new
+    length)."""
+    return (_attn_module or _attn()).evict(
+        k_cache, v_cache, weights, page_table, kv_lens, new_table, keep, recent, k_scale, v_scale,
+        new_lens, kept, status, None if stream is None else stream.cuda_stream)
 
 
 def gdn_test_attn_prefix(always: bool) -> None:

@@ -13,6 +13,8 @@ struct AttnFrontParams {
   const float* qw;          // [D] or null
   const float* kw;          // [D] or null
   const float* rope;        // [max_pos, rot] or null
+  const int32_t* positions; // [n_axes, T] or null: the place in the sequence
+  const uint8_t* axes;      // [rot / 2] or null: all by the first axis
   const int32_t* cu;        // [N + 1] or null
   const int32_t* kv_lens;   // [N] or null
   const int32_t* table;     // [N, max_pages] or null
@@ -24,7 +26,54 @@ struct AttnFrontParams {
   int32_t* status;          // or null
   float eps;
   int in_bf16, out_bf16, interleaved;
+  int n_axes;
 };
+
+struct AttnAppend8Params {
+  int T, N, Hk, D, page, page_shift, n_pages, max_pages;
+  int span;                 // rows that a warp looks through for the first of a block, 1 or 16
+  const void* k;
+  const void* v;
+  const int32_t* cu;        // [N + 1] or null
+  const int32_t* kv_lens;   // [N] or null
+  const int32_t* table;     // [N, max_pages]
+  uint8_t* kc;
+  uint8_t* vc;
+  float* ks;
+  float* vs;
+  int32_t* status;          // or null
+  int in_bf16;
+};
+
+struct AttnWeightsParams {
+  int T, N, H, Hk, G, D, page, page_shift, n_pages, max_pages, window;
+  const __nv_bfloat16* q;
+  const __nv_bfloat16* k;
+  const float* lse;         // [T, H]
+  const int32_t* cu;        // [N + 1] or null
+  const int32_t* table;     // [N, max_pages]
+  float scale;
+  float* weights;           // [n_pages, Hk, page]
+  int32_t* status;          // or null
+};
+
+struct AttnEvictParams {
+  int N, Hk, D, page, page_shift, n_pages, max_pages, new_max, keep, recent;
+  int row;                  // bytes of a key
+  char* kc;
+  char* vc;
+  float* ks;                // or null: bf16
+  float* vs;
+  float* weights;
+  const int32_t* table;     // [N, max_pages]
+  const int32_t* kv_lens;   // [N]
+  const int32_t* new_table; // [N, new_max]
+  int32_t* new_lens;        // [N], may be kv_lens
+  int32_t* kept;            // [N, Hk, keep]
+  int32_t* status;          // or null
+};
+
+constexpr int kBlock8 = 16;  // tokens of an 8-bit cache that share a scale
 
 struct AttnParams {
   int T, N, H, Hk, G, D;              // G = H / Hk
@@ -35,6 +84,9 @@ struct AttnParams {
   const __nv_bfloat16* q;
   const __nv_bfloat16* k;             // [T, Hk, D] or the cache
   const __nv_bfloat16* v;
+  const float* ks;                    // decode, cache in 8 bits: its scales, or null
+  const float* vs;
+  float* weights;                     // decode: [n_pages, Hk, page] or null
   const int32_t* cu;                  // prefill: [N + 1] or null
   const int32_t* table;               // decode
   const int32_t* kv_lens;             // decode
@@ -61,6 +113,12 @@ bool launch_attn_front(const AttnFrontParams& p, cudaStream_t s);
 bool launch_attn_prefill(const AttnParams& p, cudaStream_t s);
 bool launch_attn_decode(const AttnParams& p, void* workspace, cudaStream_t s);
 size_t attn_decode_workspace(int T, int N, int H, int Hk, int D);
+bool launch_attn_decode_cache(const AttnParams& p, void* workspace, cudaStream_t s);
+size_t attn_decode_cache_workspace(int T, int N, int H, int Hk, int D, int64_t max_keys, bool weights);
+bool launch_attn_append8(const AttnAppend8Params& p, cudaStream_t s);
+bool launch_attn_prefill_weights(const AttnWeightsParams& p, void* workspace, cudaStream_t s);
+size_t attn_prefill_weights_workspace(int T, int N, int H, int Hk, int D);
+bool launch_attn_evict(const AttnEvictParams& p, cudaStream_t s);
 
 // Decode: the keys of sequence n, and those that its new token i sees.
 __device__ __forceinline__ int seq_len(const AttnParams& p, int n) {
@@ -68,6 +126,30 @@ __device__ __forceinline__ int seq_len(const AttnParams& p, int n) {
 }
 __device__ __forceinline__ int keys_seen(const AttnParams& p, int n, int i) {
   return max(seq_len(p, n) - p.nq + i + 1, 0);
+}
+
+// Sequence n of token t and its [cu[n], cu[n + 1]); n = -1 outside every sequence. The guess
+// n = t is right in a decode step (one token each), where it saves the search's loads.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int N, int T, int t, int& b, int& e) {
+  if (!cu) {
+    b = 0;
+    e = T;
+    return 0;
+  }
+  int n = min(t, N - 1);
+  b = cu[n];
+  e = cu[n + 1];
+  if (b <= t && t < e) return n;
+  int lo = 0, hi = N;  // the last entry <= t lies in [lo, hi]
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (cu[m] <= t) lo = m;
+    else hi = m - 1;
+  }
+  if (lo >= N) return -1;
+  b = cu[lo];
+  e = cu[lo + 1];
+  return b <= t && t < e && b >= 0 && e <= T ? lo : -1;
 }
 
 // One lane's D / 32 output columns of row `row` (a [rows, D] array).

@@ -48,30 +48,6 @@ __device__ __forceinline__ void store4(void* x, size_t at, const float* y) {
   }
 }
 
-// Sequence n of token t and its [cu[n], cu[n + 1]); n = -1 outside every sequence. The guess
-// n = t is right in a decode step (one token each), where it saves the search's loads.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int N, int T, int t, int& b, int& e) {
-  if (!cu) {
-    b = 0;
-    e = T;
-    return 0;
-  }
-  int n = min(t, N - 1);
-  b = cu[n];
-  e = cu[n + 1];
-  if (b <= t && t < e) return n;
-  int lo = 0, hi = N;  // the last entry <= t lies in [lo, hi]
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (cu[m] <= t) lo = m;
-    else hi = m - 1;
-  }
-  if (lo >= N) return -1;
-  b = cu[lo];
-  e = cu[lo + 1];
-  return b <= t && t < e && b >= 0 && e <= T ? lo : -1;
-}
-
 // 1 / sqrt(x): rsqrtf is good to 2 ulp, one Newton step brings it to rounding (not from 0, the
 // result for infinity, which the step would make NaN).
 __device__ __forceinline__ float inv_sqrt(float x) {
@@ -79,7 +55,7 @@ __device__ __forceinline__ float inv_sqrt(float x) {
   return r == 0.f ? 0.f : r * (1.5f - 0.5f * x * r * r);
 }
 
-template <int D, bool kInBf16, bool kOutBf16, int R, bool kInter>
+template <int D, bool kInBf16, bool kOutBf16, int R, bool kInter, bool kAxes>
 __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontParams p) {
   constexpr int L = D / 8;  // lanes of a head row
   // A token's chunks of R heads: first the query heads', then those of the keys and values, so
@@ -126,7 +102,20 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
 
   // cos and sin of this lane's pairs
   float c[4] = {1.f, 1.f, 1.f, 1.f}, s[4] = {0.f, 0.f, 0.f, 0.f};
-  if (live && turned) {
+  if (kAxes && live && turned) {
+    uint32_t ax = 0;  // the axes of the lane's four pairs, a byte each
+    if (p.axes) ax = *reinterpret_cast<const uint32_t*>(p.axes + 4 * lane);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int a = (ax >> (8 * i)) & 255;
+      const int at = p.positions[(size_t)min(a, p.n_axes - 1) * p.T + t];
+      if (a >= p.n_axes || at < 0 || at >= p.max_pos) set_status(p.status, GDN_DEV_BAD_LENGTH);
+      const size_t row = (size_t)min(max(at, 0), p.max_pos - 1) * p.rot + 4 * lane + i;
+      c[i] = p.rope[row];
+      s[i] = p.rope[row + half];
+    }
+  }
+  if (!kAxes && live && turned) {
     if (pos < 0 || pos >= p.max_pos) set_status(p.status, GDN_DEV_BAD_LENGTH);
     const int64_t row = pos < 0 ? 0 : pos < p.max_pos ? pos : p.max_pos - 1;
     load4<false>(p.rope, (size_t)row * p.rot + 4 * lane, c);
@@ -237,7 +226,7 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
   }
 }
 
-template <int D, bool kInBf16, bool kOutBf16, bool kInter>
+template <int D, bool kInBf16, bool kOutBf16, bool kInter, bool kAxes>
 bool launch(const AttnFrontParams& p, cudaStream_t s) {
   const int per_block = kThreads / (D / 8);
   const int64_t rows = (int64_t)p.T * (p.H + 2 * p.Hk);
@@ -247,21 +236,25 @@ bool launch(const AttnFrontParams& p, cudaStream_t s) {
   const bool wide = rows >= 8 * 152 * 16;
   const int64_t items = wide ? (int64_t)p.T * ((p.H + 1) / 2 + p.Hk) : rows;
   const int64_t blocks = (items + per_block - 1) / per_block;
-  const auto kernel = wide ? attn_front_kernel<D, kInBf16, kOutBf16, 2, kInter>
-                           : attn_front_kernel<D, kInBf16, kOutBf16, 1, kInter>;
+  const auto kernel = wide ? attn_front_kernel<D, kInBf16, kOutBf16, 2, kInter, kAxes>
+                           : attn_front_kernel<D, kInBf16, kOutBf16, 1, kInter, kAxes>;
   return launch_pdl(kernel, dim3((unsigned)blocks), dim3(kThreads), 0, s, p) == cudaSuccess;
 }
 
-template <int D, bool kInter>
+template <int D, bool kInter, bool kAxes>
 bool launch_t(const AttnFrontParams& p, cudaStream_t s) {
   if (p.in_bf16)
-    return p.out_bf16 ? launch<D, true, true, kInter>(p, s) : launch<D, true, false, kInter>(p, s);
-  return p.out_bf16 ? launch<D, false, true, kInter>(p, s) : launch<D, false, false, kInter>(p, s);
+    return p.out_bf16 ? launch<D, true, true, kInter, kAxes>(p, s)
+                      : launch<D, true, false, kInter, kAxes>(p, s);
+  return p.out_bf16 ? launch<D, false, true, kInter, kAxes>(p, s)
+                    : launch<D, false, false, kInter, kAxes>(p, s);
 }
 
 template <int D>
 bool launch_d(const AttnFrontParams& p, cudaStream_t s) {
-  return p.interleaved ? launch_t<D, true>(p, s) : launch_t<D, false>(p, s);
+  if (p.positions)
+    return p.interleaved ? launch_t<D, true, true>(p, s) : launch_t<D, false, true>(p, s);
+  return p.interleaved ? launch_t<D, true, false>(p, s) : launch_t<D, false, false>(p, s);
 }
 
 }  // namespace

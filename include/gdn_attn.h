@@ -11,6 +11,11 @@
  *   decode    the same for the last tokens of each sequence, over keys and values
  *             held in pages; the first shared_len tokens may be the same pages for
  *             all sequences and are then read once for all
+ *   append    keys and values rounded to 8 bits into a cache with a scale for each 16
+ *             tokens and key head, which decode reads as well
+ *   weights   what each key gathers of the rows' softmax weights, while decoding and
+ *             from a prompt's rows
+ *   evict     each sequence cut to its last tokens and those of largest weight
  *
  * Conventions are those of gdn.h: device pointers owned by the caller, work
  * enqueued on `stream`, no allocation, no synchronization, nothing read back, so
@@ -25,6 +30,10 @@
  *                                          log, scale included; -inf for a row that
  *                                          sees no key
  *   k_cache, v_cache  [n_pages, Hk, page_size, D]
+ *                     in 8 bits: e4m3 (one byte an element), with
+ *   k_scale, v_scale  [n_pages, Hk, page_size / 16] fp32: an element is its e4m3 value
+ *                     times the scale of its token's block of 16 tokens
+ *   weights           [n_pages, Hk, page_size] fp32: what each key of the cache has gathered
  *   page_table        [N, max_pages] int32: sequence n's token t is held by page
  *                     page_table[n, t / page_size] at row t % page_size
  *   kv_lens           [N] int32: tokens of each sequence in the cache, the call's
@@ -126,6 +135,43 @@ int gdn_attn_front(const gdn_attn_desc* desc, const void* x, const float* q_weig
                    void* k_cache, void* v_cache, cudaStream_t stream);
 
 /*
+ * The front end with positions of their own: rotary positions of several axes (time, row and
+ * column of an image's or a video's tokens), or positions that are not places in the cache
+ * (behind images, after an eviction).
+ *   positions    [n_axes, T] int32, n_axes 1 to 8
+ *   rope_axes    [rot_dim / 2] uint8: pair i turns by the table's row positions[rope_axes[i], t];
+ *                NULL: all by the first
+ * The token's place in the cache stays kv_lens[n] - len_n + t. A position outside [0, max_pos)
+ * uses the table's nearest row (GDN_DEV_BAD_LENGTH), an axis outside [0, n_axes) the last axis
+ * (GDN_DEV_BAD_LENGTH). rot_dim must not be 0. Everything else as for gdn_attn_front.
+ */
+int gdn_attn_front_axes(const gdn_attn_desc* desc, const void* x, const float* q_weight,
+                        const float* k_weight, const float* rope, const int32_t* cu_seqlens,
+                        const int32_t* kv_lens, const int32_t* positions, int32_t n_axes,
+                        const uint8_t* rope_axes, const int32_t* page_table, void* q, void* k,
+                        void* v, void* k_cache, void* v_cache, cudaStream_t stream);
+
+/*
+ * Appends keys and values to a cache in 8 bits.
+ *   k, v         [T, Hk, D] in in_dtype (what gdn_attn_front returns)
+ *   kv_lens      [N], the call's tokens included; token t of sequence n goes to place
+ *                kv_lens[n] - len_n + t. NULL: t
+ * A block of 16 tokens is scaled by the least power of two s, 2^-100 or more, with max|x| <=
+ * 448 s over its new tokens of one key head (infinities and NaN, which are held as NaN, aside);
+ * elements are x / s rounded to nearest even. Where the block holds earlier tokens of the
+ * sequence, s is at least the scale that it has, and if s grows, their elements are rounded
+ * again to the new scale: powers of two lose nothing there but what gets below 2^-6 s. The
+ * result is the same for any split of the tokens into calls, but for that second rounding.
+ * Rows of the block past the sequence's end are left as they are. Tokens with no place in the
+ * cache are not appended (status bits as for gdn_attn_front). A page in which two sequences of
+ * the call have tokens: undefined values in that page.
+ */
+int gdn_attn_append8(const gdn_attn_desc* desc, const void* k, const void* v,
+                     const int32_t* cu_seqlens, const int32_t* kv_lens, const int32_t* page_table,
+                     void* k_cache, void* v_cache, float* k_scale, float* v_scale,
+                     cudaStream_t stream);
+
+/*
  * Causal attention of packed prompts over their own keys and values.
  *   q [T, H, D], k, v [T, Hk, D]  bf16
  *   scale        <= 0 or NaN selects 1/sqrt(D)
@@ -156,6 +202,67 @@ int gdn_attn_prefill(const gdn_attn_desc* desc, const void* q, const void* k, co
 int gdn_attn_decode(const gdn_attn_desc* desc, const void* q, const void* k_cache,
                     const void* v_cache, const int32_t* page_table, const int32_t* kv_lens,
                     int32_t shared_len, float scale, void* out, float* lse, cudaStream_t stream);
+
+/*
+ * gdn_attn_decode over a cache in bf16 or in 8 bits, and with the weight that each key gets.
+ *   k_scale, v_scale  with them the cache is in 8 bits (any scales that are 0 or more, not only
+ *                     gdn_attn_append8's); both NULL: bf16. Elements that are NaN, and scales of
+ *                     keys past a sequence's length, have no influence where they are not seen.
+ *   weights           NULL, or where the softmax weights go: to each key of a sequence is added
+ *                     their sum over the call's rows and the query heads of its group (fp32);
+ *                     to the call's own tokens nothing is added, they are set to it. With
+ *                     weights, shared_len must be 0. A page of two sequences gathers from both,
+ *                     in any order; a page that does not exist gathers nothing.
+ * The workspace is gdn_attn_decode_cache_workspace_size bytes: with weights it holds the scores of
+ * all max_pages * page_size keys too. A cache in 8 bits takes no pass of its own for a common
+ * prefix; every sequence reads it (mostly from L2).
+ */
+int gdn_attn_decode_cache(const gdn_attn_desc* desc, const void* q, const void* k_cache,
+                          const void* v_cache, const float* k_scale, const float* v_scale,
+                          const int32_t* page_table, const int32_t* kv_lens, int32_t shared_len,
+                          float scale, void* out, float* lse, float* weights, cudaStream_t stream);
+size_t gdn_attn_decode_cache_workspace_size(const gdn_attn_desc* desc, int32_t with_weights);
+
+/*
+ * The weight that a prompt's rows give its keys: weights[key j] = sum over the rows i >= j and
+ * the query heads of the group of exp(scale * q_i . k_j - lse_i), set (not added) for all keys of
+ * each prompt, which are the first tokens of their sequences.
+ *   q [T, H, D], k [T, Hk, D]  bf16;  lse [T, H] fp32 as gdn_attn_prefill returns it
+ *   window       0: all rows; w > 0: the last w rows of each prompt only
+ * cu_seqlens as for gdn_attn_prefill. A key with no place in the cache is left out
+ * (GDN_DEV_BAD_LENGTH, GDN_DEV_BAD_PAGE_TABLE). A page of two sequences: undefined values there.
+ * The workspace is gdn_attn_prefill_weights_workspace_size bytes.
+ */
+int gdn_attn_prefill_weights(const gdn_attn_desc* desc, const void* q, const void* k,
+                             const float* lse, const int32_t* cu_seqlens,
+                             const int32_t* page_table, int32_t window, float scale,
+                             float* weights, cudaStream_t stream);
+size_t gdn_attn_prefill_weights_workspace_size(const gdn_attn_desc* desc);
+
+/*
+ * Cuts each sequence to at most `keep` tokens: its last `recent` ones and, of the others, for
+ * each key head those of largest weight (of equal weights the lower index; NaN counts as larger
+ * than all numbers). They are copied in their order to the places 0, 1, .. of the pages of
+ * new_table, with their weights; the sequence's old pages stay as they are, and may be shared.
+ * A sequence of at most `keep` tokens is copied whole.
+ *   k_scale, v_scale  with them the cache is in 8 bits: a new block's scale is the largest of its
+ *                     tokens' scales, and elements of smaller scales are rounded again. Both NULL:
+ *                     bf16
+ *   new_table    [N, new_max_pages] int32; its pages must not be among the call's old ones, nor
+ *                named twice (values in pages that are: undefined)
+ *   keep         1 to new_max_pages * page_size;  recent 0 to keep
+ *   new_lens     [N] int32, the lengths after the call; it may be kv_lens itself
+ *   kept         [N, Hk, keep] int32, the places that the tokens had; -1 past new_lens[n]
+ * Tokens differ from head to head, so a place holds several tokens; rotary positions are in the
+ * keys already. T, H and dtypes of desc are not looked at beyond gdn_attn_check_desc. Keys and
+ * values of a page outside [0, n_pages) are zeros of weight 0, and what would go to such a page
+ * goes nowhere (GDN_DEV_BAD_PAGE_TABLE).
+ */
+int gdn_attn_evict(const gdn_attn_desc* desc, void* k_cache, void* v_cache, float* k_scale,
+                   float* v_scale, float* weights, const int32_t* page_table,
+                   const int32_t* kv_lens, const int32_t* new_table, int32_t new_max_pages,
+                   int32_t keep, int32_t recent, int32_t* new_lens, int32_t* kept,
+                   cudaStream_t stream);
 
 /*
  * Testing hook. gdn_attn_decode gives a common prefix its own pass only where that pays (many
