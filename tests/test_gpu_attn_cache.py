@@ -8,6 +8,11 @@ Tolerances, derived before the first run:
   - attention: each weight may be rounded to bf16 (relative 2^-8 at most), which moves an output
     by at most 2^-8 sum_j w_ij |v_j|; scores and exp add less than 2^-11 of the same sum at these
     inputs. A bf16 output adds 2^-8 |o|. lse: 1e-3 as for the bf16 cache.
+    Over a cache in 8 bits, weight times scale, w_j s_j, is rounded to fp16 against a reference r of
+    its row: relatively by 2^-12 (within the 2^-8 above), or, where it becomes subnormal, by 2^-25 r.
+    r is set to 2^-7 of the largest w_j s_j so far and only grows, so that r <= 2^-7 max_j w_j s_j,
+    and an output moves by at most 2^-32 max_j(w_j s_j) sum_j |e_j|, e_j being the e4m3 value: it
+    counts where the keys of large weight have a value of 0.
   - weights: fp32 throughout. A score is off by at most (D + 8) 2^-24 scale sum |q k|, a row's lse by
     as much, and exp of their difference by that amount relatively, and 2^-19 for exp itself and the
     sums. A sum that is added to rounds by 2^-24 of it.
@@ -198,15 +203,35 @@ def test_append_places_that_do_not_exist():
 
 
 # ---------------------------------------------------------------- decode
-def close(out, lse, ref, mag, ref_lse):
+def close(out, lse, ref, mag, ref_lse, floor=0.0):
     o = np64(out).reshape(ref.shape)
-    tol = REL * mag + (2.0 ** -8 * np.abs(ref) if out.dtype == BF else 0.0) + 1e-6 * mag
+    tol = REL * mag + (2.0 ** -8 * np.abs(ref) if out.dtype == BF else 0.0) + 1e-6 * mag + floor
     bad = ~(np.abs(o - ref) <= tol)
     assert not bad.any(), (np.argwhere(bad)[:5], o[bad][:5], ref[bad][:5], tol[bad][:5])
     got, want = np64(lse).reshape(ref_lse.shape), ref_lse
     assert np.array_equal(np.isneginf(got), np.isneginf(want))
     fin = np.isfinite(want)
     assert np.abs(got[fin] - want[fin]).max(initial=0.0) <= 1e-3
+
+
+def fp16_floor(q, keys, vb, vs, table, lens, shared=0, scale=None):
+    """2^-32 max_j(w_j s_j) sum_j |e_j| for rows q [N, n_q, H, D] over keys' values, bytes and scales."""
+    N, nq, H, D = q.shape
+    Hk, page = keys.shape[1:3]
+    e = np.abs(C.VALUES[vb.numpy()])
+    s = np.repeat(vs.double().numpy(), 16, 2)[..., None]
+    floor = np.zeros(q.shape)
+    for n in range(N):
+        length = min(max(lens[n], 0), table.shape[1] * page)
+        last = np.arange(length - nq, length)
+        for h in range(H):
+            k, ev, sv = (A.gather(x, table.numpy(), n, length, h * Hk // H, page, shared) for x in (keys, e, s))
+            w = C.row_weights(q[n, :, h], k, last, D ** -0.5 if scale is None else scale)
+            for i in range(nq):
+                seen = max(last[i] + 1, 0)
+                if seen:
+                    floor[n, i, h] = 2.0 ** -32 * (w[i, :seen] * sv[:seen, 0]).max() * ev[:seen].sum(0)
+    return floor
 
 
 def weight_slack(q, keys, D, scale):
@@ -246,7 +271,8 @@ def run_decode(lens, H, Hk, D, page, nq=1, bits=8, weights=False, seed=0, mul=1.
     assert status.item() == 0
     q4 = np64(q).reshape(N, nq, H, D)
     ref, mag, rl = A.decode(q4, kv, vv, table.numpy(), lens, shared, scale)
-    close(out, lse, ref, mag, rl)
+    floor = fp16_floor(q4, kv, vb, vs, table, lens, shared, scale) if bits == 8 else 0.0
+    close(out, lse, ref, mag, rl, floor)
     if weights:
         want = C.decode_weights(q4, kv, table.numpy(), lens, w.numpy(), scale)
         seen = [kv[int(table[n, j // page]), :, j % page] for n in range(N) for j in range(lens[n])]
@@ -438,7 +464,8 @@ def test_decode_pages_that_do_not_exist(bits, weights):
                                  v_scale=cuda(vs), weights=w_dev)
     assert status.item() == 64 | 128
     ref, mag, rl = A.decode(np64(q)[:, None], kv, vv, table.numpy(), lens)
-    close(out, lse, ref, mag, rl)
+    floor = fp16_floor(np64(q)[:, None], kv, vb, vs, table, lens) if bits == 8 else 0.0
+    close(out, lse, ref, mag, rl, floor)
     if weights:  # (the page that a sequence names three times gathers three times, in any order)
         want = C.decode_weights(np64(q)[:2, None], kv, table.numpy()[:2], lens[:2], w.numpy())
         assert np.abs(np64(w_dev)[:3] - want[:3]).max() < 1e-4
@@ -460,7 +487,8 @@ def test_decode8_cache_past_32_bit_offsets():
                                  return_lse=True, k_scale=ks, v_scale=ks, weights=w)
     v = values8(b, s)
     t = table.numpy() - (n_pages - 4)
-    close(out, lse, *A.decode(np64(q)[:, None], v, v, t, [400]))
+    floor = fp16_floor(np64(q)[:, None], v, b, s, torch.from_numpy(t), [400])
+    close(out, lse, *A.decode(np64(q)[:, None], v, v, t, [400]), floor)
     want = C.decode_weights(np64(q)[:, None], v, t, [400], np.zeros((4, Hk, page)))
     assert np.abs(np64(w[-4:]) - want).max() < 1e-4 and w[:-4].abs().max() == 0
     x = randn(g, 16, Hk, D)
