@@ -154,8 +154,8 @@ int decode_impl(const gdn_attn_desc* desc, const void* q, const void* k_cache, c
   p.table = page_table; p.kv_lens = kv_lens;
   p.ks = k_scale; p.vs = v_scale; p.weights = weights;
   if (!clear_status(d.status, stream)) return GDN_ERR_LAUNCH_FAILED;
-  if (!(k_scale || weights ? launch_attn_decode_cache(p, d.workspace, stream)
-                           : launch_attn_decode(p, d.workspace, stream)))
+  if (!(k_scale ? launch_attn_decode8(p, d.workspace, stream)
+                : launch_attn_decode(p, d.workspace, stream)))
     return GDN_ERR_LAUNCH_FAILED;
   return cudaPeekAtLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH_FAILED;
 }

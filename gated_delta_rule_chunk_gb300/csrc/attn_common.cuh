@@ -113,7 +113,8 @@ bool launch_attn_front(const AttnFrontParams& p, cudaStream_t s);
 bool launch_attn_prefill(const AttnParams& p, cudaStream_t s);
 bool launch_attn_decode(const AttnParams& p, void* workspace, cudaStream_t s);
 size_t attn_decode_workspace(int T, int N, int H, int Hk, int D);
-bool launch_attn_decode_cache(const AttnParams& p, void* workspace, cudaStream_t s);
+constexpr int kDecode8Ctas = 3;  // of an SM, over a cache in 8 bits
+bool launch_attn_decode8(const AttnParams& p, void* workspace, cudaStream_t s);
 size_t attn_decode_cache_workspace(int T, int N, int H, int Hk, int D, int64_t max_keys, bool weights);
 bool launch_attn_append8(const AttnAppend8Params& p, cudaStream_t s);
 bool launch_attn_prefill_weights(const AttnWeightsParams& p, void* workspace, cudaStream_t s);

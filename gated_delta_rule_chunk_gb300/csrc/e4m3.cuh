@@ -17,14 +17,19 @@ __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
 }
 
-// The two low bytes as fp16 values (exact).
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t x) {
-  const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)x, __NV_E4M3);
-  return (uint32_t)h.x | (uint32_t)h.y << 16;
+// Four bytes as two pairs of fp16 values (exact). (Through cuda_fp8.h's types the halves of a
+// pair were taken apart and put together again, an instruction or two each.)
+__device__ __forceinline__ void e4m3x4_to_f16x4(uint32_t x, uint32_t& lo, uint32_t& hi) {
+  asm("{\n .reg .b16 a, b;\n mov.b32 {a, b}, %2;\n cvt.rn.f16x2.e4m3x2 %0, a;\n"
+      " cvt.rn.f16x2.e4m3x2 %1, b;\n}\n"
+      : "=r"(lo), "=r"(hi)
+      : "r"(x));
 }
+// The two low bytes.
 __device__ __forceinline__ float2 e4m3x2_to_float2(uint32_t x) {
-  const uint32_t h = e4m3x2_to_f16x2(x);
-  return __half22float2(*reinterpret_cast<const __half2*>(&h));
+  uint32_t lo, hi;
+  e4m3x4_to_f16x4(x & 0xFFFFu, lo, hi);
+  return __half22float2(*reinterpret_cast<const __half2*>(&lo));
 }
 
 }  // namespace gdn

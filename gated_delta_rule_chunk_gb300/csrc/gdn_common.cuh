@@ -311,6 +311,9 @@ bool encode_2d_tmap(void* tmap, const void* base, bool bf16, int cols, int rows,
 // from the second on) with the 128-byte swizzle, zeros outside.
 bool encode_bf16_tmap(void* tmap, const void* base, int rank, const uint64_t* dims,
                       const uint64_t* strides, const uint32_t* box);
+// The same for bytes, rows of 64 or 128 (swizzled by as many).
+bool encode_u8_tmap(void* tmap, const void* base, int rank, const uint64_t* dims,
+                    const uint64_t* strides, const uint32_t* box);
 // SMs of the current device (152 where it cannot be asked, as on a host without one).
 int num_sms();
 // Same over an fp32 state [rows, 128]: box 32 rows x 32 elements, 128-byte swizzle.
