@@ -17,10 +17,10 @@ static std::atomic<int> g_prefill_tiles{0};
 int attn_prefill_tiles() { return g_prefill_tiles.load(std::memory_order_relaxed); }
 
 static std::atomic<uint32_t> g_wait_polls{0}, g_wait_item{0};
-void attn_test_timeout(AttnParams& p) {
-  if (const uint32_t polls = g_wait_polls.load(std::memory_order_relaxed)) {
-    p.polls = polls;
-    p.stall = g_wait_item.load(std::memory_order_relaxed) + 1;
+void attn_test_timeout(uint32_t& polls, uint32_t& stall) {
+  if (const uint32_t n = g_wait_polls.load(std::memory_order_relaxed)) {
+    polls = n;
+    stall = g_wait_item.load(std::memory_order_relaxed) + 1;
   }
 }
 
@@ -74,7 +74,7 @@ AttnParams attn_params(const gdn_attn_desc& d, const void* q, const void* k, con
   p.out = out; p.lse = lse; p.status = d.status;
   p.out_bf16 = d.out_dtype == GDN_BF16;
   p.polls = kAttnPolls;
-  attn_test_timeout(p);
+  attn_test_timeout(p.polls, p.stall);
   return p;
 }
 
@@ -305,6 +305,8 @@ int gdn_attn_prefill_weights(const gdn_attn_desc* desc, const void* q, const voi
   p.lse = lse; p.cu = cu_seqlens; p.table = page_table;
   p.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)d.D);  // also NaN
   p.weights = weights; p.status = d.status;
+  p.polls = kAttnPolls;
+  attn_test_timeout(p.polls, p.stall);
   if (!clear_status(d.status, stream)) return GDN_ERR_LAUNCH_FAILED;
   if (!launch_attn_prefill_weights(p, d.workspace, stream)) return GDN_ERR_LAUNCH_FAILED;
   return cudaPeekAtLastError() == cudaSuccess ? GDN_OK : GDN_ERR_LAUNCH_FAILED;

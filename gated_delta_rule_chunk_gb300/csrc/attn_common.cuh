@@ -55,6 +55,7 @@ struct AttnWeightsParams {
   float scale;
   float* weights;           // [n_pages, Hk, page]
   int32_t* status;          // or null
+  uint32_t polls, stall;    // as in AttnParams
 };
 
 struct AttnEvictParams {
@@ -103,7 +104,7 @@ struct AttnParams {
 // Polls of an on-chip wait before it gives up.
 constexpr uint32_t kAttnPolls = 1u << 22;
 // Testing hook (gdn_test_attn_timeout): sets polls and stall where it is on.
-void attn_test_timeout(AttnParams& p);
+void attn_test_timeout(uint32_t& polls, uint32_t& stall);
 // Testing hook (gdn_test_attn_prefix): a common prefix takes its own kernel at every size.
 bool attn_prefix_always();
 // Testing hook (gdn_test_attn_tiles): row tiles of a prompt's work items, 0: by the rule.

@@ -1,72 +1,527 @@
 // The weight that a prompt's rows give its keys: w_j = sum over the rows i >= j of the window and
-// the query heads of the group of exp(scale q_i . k_j - lse_i). One warp per key and key head.
-#include "attn_common.cuh"
+// the query heads of the group of exp(scale q_i . k_j - lse_i), on the tensor cores.
+//
+// With the keys as the rows of the product, S^T = K Q^T, a key's scores are one lane of TMEM and
+// its sum is one thread's: no exchange between threads, and no weights are stored. A step is 128
+// query rows (tokens of one head) against a pair of key tiles, A and B, of 128 keys, so that a Q
+// tile is read once for both: two M = 128, N = 128 products, 2 x 16384 exponentials.
+//   warps 0-3, 4-7  one thread per key of A, B: 2^(c s - lse2) of its 128 columns, summed in fp32, four
+//                   partial sums a step
+//   warp 8          TMA loads: a pair's K tiles (two pairs), a ring of Q tiles
+//   warp 9          issues the MMAs; a step's scores are in one of two TMEM buffers a tile
+//   warp 10         the rows' -lse * log2(e), from two steps ahead, into shared memory
+// The steps of all (sequence, key head, key pair) items form one list, and each SM takes an equal
+// contiguous part of it: causal items are of any length, and one prompt is spread over the GPU. An
+// item that spans CTAs leaves partial sums in the workspace, which reduce_kernel adds in the order
+// of the rows, so that results do not depend on timing.
+// Columns that a key does not count (rows before it or before the window, past the sequence's end)
+// are selected away in the tiles that have any; a row there may hold anything.
+//
+// Bound: the products and the exponentials alike, 1,076 and 1,024 cycles a step.
+#include "attn_tc.cuh"
 
 namespace gdn {
 
 namespace {
 
+constexpr int kTile = 128;        // keys of a tile, rows of a step
+constexpr int kThreads = 11 * 32;
+constexpr float kLog2e = 1.44269504088896340736f;
+
 template <int D>
-__global__ void __launch_bounds__(128) prefill_weights_kernel(const AttnWeightsParams p) {
-  constexpr int E = D / 32;
-  const uint32_t item = blockIdx.x * 4 + (threadIdx.x >> 5);
-  const int lane = threadIdx.x & 31, t = item / p.Hk, hk = item - t * p.Hk;
-  pdl_wait();
-  if (t >= p.T) return;
-  // entries clamped to [0, T] and raised to the largest before them
-  int n = 0, b = 0, e = p.T;
-  if (p.cu) {
-    e = min(max(p.cu[0], 0), p.T);
-    for (n = 0; n < p.N; ++n) {
-      b = e;
-      e = max(b, min(p.cu[n + 1], p.T));
-      if (item == 0 && lane == 0 && (p.cu[n] < (n ? p.cu[n - 1] : 0) || p.cu[n + 1] < p.cu[n] ||
-                                     p.cu[n + 1] > p.T))
-        set_status(p.status, GDN_DEV_BAD_CU_SEQLENS);
-      if (item != 0 && b <= t && t < e) break;
+struct WeightsSmem {
+  static constexpr int kBytesTile = kTile * D * 2;
+  static constexpr int kStages = D == 128 ? 2 : 4;          // Q tiles
+  static constexpr int kK = 0;                              // two pairs of K tiles
+  static constexpr int kQ = 4 * kBytesTile;
+  static constexpr int kLse = kQ + kStages * kBytesTile;    // [2][128]
+  static constexpr int kBars = kLse + 2 * kTile * 4;
+  static constexpr int kBytes = kBars + 256 + 1024;         // + alignment of the tiles
+};
+
+template <int kStages>
+struct WeightsBars {
+  uint64_t k_full[2], k_empty[2], q_full[kStages], q_empty[kStages];
+  uint64_t s_full[2][2], s_empty[2][2];  // [tile][buffer]
+  uint64_t lse_full[2], idle, never;
+  uint32_t tmem;
+};
+
+// The workspace.
+struct WeightsParts {
+  int64_t* first;  // [N + 1] number of each sequence's first step
+  int2* seq;       // [N] sanitized (first row, length)
+  float* part;     // [2 * grid][256] an item's sums in a CTA: of its first item, of its last
+};
+
+// Steps of a sequence: nt row tiles, of which the window begins in tile w.
+struct Shape {
+  int len, row0, nt, w;
+  __device__ Shape(const AttnWeightsParams& p, int len_) : len(len_) {
+    row0 = p.window > 0 && p.window < len ? len - p.window : 0;
+    nt = (len + kTile - 1) / kTile;
+    w = row0 / kTile;
+  }
+  __device__ int first_row_tile(int pair) const { return max(2 * pair, w); }
+  // steps of one head in the pairs before `pair`
+  __device__ int64_t before(int pair) const {
+    const int k0 = (w + 1) / 2;
+    if (pair <= k0) return (int64_t)pair * (nt - w);
+    return (int64_t)k0 * (nt - w) + (int64_t)(pair - k0) * (nt - pair + 1 - k0);
+  }
+  __device__ int pairs() const { return (nt + 1) / 2; }
+  // the pair that step u (of one key head, all its query heads) is in
+  __device__ int pair_of(int64_t u, int G) const {
+    int lo = 0, hi = pairs() - 1;
+    while (lo < hi) {
+      const int m = (lo + hi + 1) >> 1;
+      if (before(m) * G <= u) lo = m;
+      else hi = m - 1;
     }
-    if (item == 0)
-      for (n = 0, e = min(max(p.cu[0], 0), p.T); n < p.N; ++n) {
-        b = e;
-        e = max(b, min(p.cu[n + 1], p.T));
-        if (b <= t && t < e) break;
+    return lo;
+  }
+};
+
+// A place in the list of steps.
+struct StepCursor {
+  int64_t u;
+  int n, hk, pair, rt, g;
+  int base, end, next;  // rows of the sequence, and the next entry of cu_seqlens
+  Shape shape;
+  __device__ explicit StepCursor(const AttnWeightsParams& p) : shape(p, 0) {}
+  __device__ int bound(const AttnWeightsParams& p, int i) const {
+    return i <= p.N ? min(max(p.cu[i], 0), p.T) : p.T;
+  }
+  __device__ bool starts_item() const { return g == 0 && rt == shape.first_row_tile(pair); }
+  __device__ bool ends_item(const AttnWeightsParams& p) const {
+    return g == p.G - 1 && rt == shape.nt - 1;
+  }
+  __device__ void advance(const AttnWeightsParams& p) {
+    ++u;
+    if (++g < p.G) return;
+    g = 0;
+    if (++rt < shape.nt) return;
+    if (++pair >= shape.pairs()) {
+      pair = 0;
+      if (++hk >= p.Hk) {
+        hk = 0;
+        do {
+          if (++n >= p.N) return;
+          base = end;
+          end = max(base, next);
+          next = bound(p, n + 2);
+          shape = Shape(p, end - base);
+        } while (shape.len == 0);
       }
-    if (n == p.N) return;
-  }
-  const int j = t - b;
-  if ((j >> p.page_shift) >= p.max_pages) {
-    if (lane == 0) set_status(p.status, GDN_DEV_BAD_LENGTH);
-    return;
-  }
-  const int page = p.table[(size_t)n * p.max_pages + (j >> p.page_shift)];
-  if (page < 0 || page >= p.n_pages) {
-    if (lane == 0) set_status(p.status, GDN_DEV_BAD_PAGE_TABLE);
-    return;
-  }
-  float k[E], sum = 0.f;
-  for (int x = 0; x < E; ++x)
-    k[x] = __bfloat162float(p.k[((size_t)t * p.Hk + hk) * D + lane * E + x]);
-  const int first = p.window ? max(t, e - p.window) : t;
-  for (int i = first; i < e; ++i)
-    for (int g = 0; g < p.G; ++g) {
-      const size_t row = (size_t)i * p.H + hk * p.G + g;
-      float s = 0.f;
-      for (int x = 0; x < E; ++x) s += k[x] * __bfloat162float(p.q[row * D + lane * E + x]);
-      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      sum += expf(s * p.scale - p.lse[row]);
     }
-  if (lane == 0)
-    p.weights[(((size_t)page * p.Hk + hk) << p.page_shift) + (j & (p.page - 1))] = sum;
+    rt = shape.first_row_tile(pair);
+  }
+};
+
+__device__ __forceinline__ int64_t steps_of(const AttnWeightsParams& p, int len) {
+  const Shape s(p, len);
+  return s.before(s.pairs()) * p.G * p.Hk;
+}
+
+// CTA blockIdx.x's steps [at.u, u1), found by a warp; whether it has any. The scribe writes what
+// reduce_kernel needs.
+__device__ __forceinline__ bool find_steps(const AttnWeightsParams& p, const WeightsParts& w,
+                                           StepCursor& at, int64_t& u1, bool scribe) {
+  const int lane = threadIdx.x & 31;
+  int64_t U = 0, u0 = 0;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    int64_t before = 0;
+    int carry = 0;
+#pragma unroll 1
+    for (int n0 = 0; n0 < p.N; n0 += 32) {
+      const int n = n0 + lane;
+      int b = 0, e = 0;
+      if (n < p.N) {
+        b = p.cu ? min(max(p.cu[n], 0), p.T) : 0;
+        e = p.cu ? min(max(p.cu[n + 1], 0), p.T) : p.T;
+        if (scribe && pass == 0 && p.cu && (p.cu[n] < 0 || p.cu[n + 1] < p.cu[n] || p.cu[n + 1] > p.T))
+          set_status(p.status, GDN_DEV_BAD_CU_SEQLENS);
+      }
+      b = max(b, carry);  // raised to the largest entry before it
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, b, o);
+        if (lane >= o) b = max(b, x);
+      }
+      e = n < p.N ? max(b, e) : b;
+      const int64_t c = n < p.N ? steps_of(p, e - b) : 0;
+      int64_t inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += x;
+      }
+      const int64_t first = before + inc - c;
+      if (pass == 0 && scribe && n < p.N) {
+        w.first[n] = first;
+        w.seq[n] = make_int2(b, e - b);
+      }
+      if (pass == 1) {
+        const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && u0 >= first && u0 < first + c);
+        if (hit) {
+          const int src = __ffs(hit) - 1;
+          at.n = n0 + src;
+          at.base = __shfl_sync(0xffffffffu, b, src);
+          at.end = __shfl_sync(0xffffffffu, e, src);
+          at.u = __shfl_sync(0xffffffffu, first, src);
+          break;
+        }
+      }
+      before += __shfl_sync(0xffffffffu, inc, 31);
+      carry = __shfl_sync(0xffffffffu, e, 31);
+    }
+    if (pass == 0) {
+      U = before;
+      if (scribe && lane == 0) w.first[p.N] = U;
+      const int64_t grid = min((int64_t)gridDim.x, U);
+      if ((int64_t)blockIdx.x >= grid) return false;
+      u0 = U * blockIdx.x / grid;
+      u1 = U * (blockIdx.x + 1) / grid;
+    }
+  }
+  at.next = p.cu ? at.bound(p, at.n + 2) : p.T;
+  at.shape = Shape(p, at.end - at.base);
+  const int64_t head = at.shape.before(at.shape.pairs()) * p.G;
+  int64_t r = u0 - at.u;
+  at.hk = (int)(r / head);
+  r -= at.hk * head;
+  at.pair = at.shape.pair_of(r, p.G);
+  r -= at.shape.before(at.pair) * p.G;
+  at.rt = at.shape.first_row_tile(at.pair) + (int)(r / p.G);
+  at.g = (int)(r % p.G);
+  at.u = u0;
+  return true;
+}
+
+// Where the weight of key `key` of sequence n goes; null where its place does not exist.
+__device__ __forceinline__ float* weight_at(const AttnWeightsParams& p, int n, int hk, int key) {
+  if ((key >> p.page_shift) >= p.max_pages) {
+    set_status(p.status, GDN_DEV_BAD_LENGTH);
+    return nullptr;
+  }
+  const int page = p.table[(size_t)n * p.max_pages + (key >> p.page_shift)];
+  if (page < 0 || page >= p.n_pages) {
+    set_status(p.status, GDN_DEV_BAD_PAGE_TABLE);
+    return nullptr;
+  }
+  return p.weights + ((((size_t)page * p.Hk + hk) << p.page_shift) + (key & (p.page - 1)));
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
+                  const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
+  using S = WeightsSmem<D>;
+  constexpr int kStages = S::kStages;
+  extern __shared__ char raw_smem[];
+  char* smem = raw_smem + (-smem_u32(raw_smem) & 1023u);
+  auto& B = *reinterpret_cast<WeightsBars<kStages>*>(smem + S::kBars);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (warp == 9) {
+    if (lane == 0) {
+      for (int i = 0; i < 2; ++i) {
+        mbar_init(&B.k_full[i], 1);
+        mbar_init(&B.k_empty[i], 1);
+        mbar_init(&B.lse_full[i], 1);
+        for (int x = 0; x < 2; ++x) {
+          mbar_init(&B.s_full[x][i], 1);
+          mbar_init(&B.s_empty[x][i], 4);
+        }
+      }
+      for (int i = 0; i < kStages; ++i) {
+        mbar_init(&B.q_full[i], 1);
+        mbar_init(&B.q_empty[i], 1);
+      }
+      mbar_init(&B.idle, 1);
+      mbar_init(&B.never, 1);
+      mbar_init_fence();
+      prefetch_tmap(&tm_q);
+      prefetch_tmap(&tm_k);
+    }
+    __syncwarp();
+    tmem_alloc(&B.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = B.tmem;
+  pdl_wait();
+  StepCursor at(p);
+  int64_t u1 = 0;
+  pdl_release();
+  const bool any = find_steps(p, parts, at, u1, blockIdx.x == 0 && warp == 0);
+  Waiter wait(p.status, p.polls);
+  // The warp gives up as one.
+  auto good = [&] {
+    const bool ok = __all_sync(0xffffffffu, wait.ok());
+    if (!ok) wait.limit = 0;
+    return ok;
+  };
+  if (any && warp < 8) {
+    // ---------------------------------------------------------------- exponentials and sums
+    const int X = warp >> 2, of_tile = (warp & 3) * 32 + lane;
+    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const float* lse = reinterpret_cast<const float*>(smem + S::kLse);
+    const float c = p.scale * kLog2e;
+    const float2 c2 = make_float2(c, c);
+    float sum = 0.f;
+    bool from_start = at.starts_item();
+    int slot = 0;
+    for (uint32_t s = 0; at.u < u1; ++s, at.advance(p)) {
+      const uint32_t b = s & 1;
+      const int kt = 2 * at.pair + X, r0 = at.rt * kTile, key = kt * kTile + of_tile;
+      const Shape& q = at.shape;
+      wait(&B.lse_full[b], s >> 1);
+      wait(&B.s_full[X][b], s >> 1);
+      if (!good()) break;
+      tc_fence_after();
+      if (at.rt >= kt && kt < q.nt) {
+        const uint32_t t = tmem + lanes + X * 256 + b * 128;
+        const float4* nl = reinterpret_cast<const float4*>(lse + b * kTile);
+        const bool masked = at.rt == kt || r0 < q.row0 || r0 + kTile > q.len;
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        float v[2][32];
+        tmem_ld32(t, v[0]);
+        if (!masked) {
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            tmem_ld_wait();
+            if (ch < 3) tmem_ld32(t + 32 * (ch + 1), v[(ch + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              const float4 m = nl[ch * 8 + i];
+              const float* y = v[ch & 1] + 4 * i;
+              const float2 x0 = fma2(make_float2(y[0], y[1]), c2, make_float2(m.x, m.y));
+              const float2 x1 = fma2(make_float2(y[2], y[3]), c2, make_float2(m.z, m.w));
+              acc[0] = add2(acc[0], make_float2(ex2(x0.x), ex2(x0.y)));
+              acc[1] = add2(acc[1], make_float2(ex2(x1.x), ex2(x1.y)));
+            }
+          }
+        } else {
+          const int lo = max(key, q.row0) - r0, hi = q.len - r0;  // columns that count
+#pragma unroll
+          for (int ch = 0; ch < 4; ++ch) {
+            tmem_ld_wait();
+            if (ch < 3) tmem_ld32(t + 32 * (ch + 1), v[(ch + 1) & 1]);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) {
+              const int col = ch * 32 + i;
+              const float y = ex2(fmaf(v[ch & 1][i], c, lse[b * kTile + col]));
+              float& a = i & 1 ? acc[i >> 1 & 1].y : acc[i >> 1 & 1].x;
+              a += col >= lo && col < hi ? y : 0.f;
+            }
+          }
+        }
+        sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&B.s_empty[X][b]);
+      const bool ends = at.ends_item(p);
+      if (ends || at.u + 1 == u1) {
+        if (ends && from_start) {
+          if (key < q.len)
+            if (float* to = weight_at(p, at.n, at.hk, key)) *to = sum;
+        } else {
+          parts.part[(size_t)(2 * blockIdx.x + slot) * 256 + X * kTile + of_tile] = sum;
+        }
+        sum = 0.f;
+        from_start = true;
+        slot = 1;
+      }
+    }
+  } else if (any && warp == 8) {
+    // ---------------------------------------------------------------- loads
+    if (lane == 0) {
+      uint32_t items = 0, steps = 0;
+      for (bool begins = true; at.u < u1; ++steps) {
+        if (begins) {
+          const uint32_t k = items & 1;
+          wait(&B.k_empty[k], (items >> 1) + 1);
+          if (!wait.ok()) break;
+          const bool two = 2 * at.pair + 1 < at.shape.nt;
+          mbar_expect_tx(&B.k_full[k], S::kBytesTile * (two ? 2 : 1));
+          for (int x = 0; x < (two ? 2 : 1); ++x)
+            for (int d = 0; d < D; d += 64)
+              tma_load_3d(smem + S::kK + (2 * k + x) * S::kBytesTile + d * 256, &tm_k, d, at.hk,
+                          at.base + (2 * at.pair + x) * kTile, &B.k_full[k]);
+          ++items;
+        }
+        const uint32_t st = steps % kStages;
+        wait(&B.q_empty[st], steps / kStages + 1);
+        if (!wait.ok()) break;
+        mbar_expect_tx(&B.q_full[st], S::kBytesTile);
+        for (int d = 0; d < D; d += 64)
+          tma_load_3d(smem + S::kQ + st * S::kBytesTile + d * 256, &tm_q, d, at.hk * p.G + at.g,
+                      at.base + at.rt * kTile, &B.q_full[st]);
+        begins = at.ends_item(p);
+        at.advance(p);
+      }
+      // Copies in flight end before the CTA does (all have been waited for already, unless someone
+      // gave up).
+      for (uint32_t i = 0; i < 2 && i < items; ++i)
+        mbar_wait(&B.k_full[i], ((items - 1 - i) / 2) & 1, kAttnPolls);
+      for (uint32_t i = 0; i < kStages && i < steps; ++i)
+        mbar_wait(&B.q_full[i], ((steps - 1 - i) / kStages) & 1, kAttnPolls);
+    }
+  } else if (any && warp == 9) {
+    // ---------------------------------------------------------------- products
+    constexpr uint32_t kId = idesc_bf16_f32(128, kTile), kT = S::kBytesTile >> 4;
+    constexpr uint32_t kHi = (1u << 14) | (2u << 29) | (1024 >> 4);
+    const uint32_t k_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kK), 16, 1024));
+    const uint32_t q_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024));
+    const uint32_t el = elect_one(), tm = uniform(tmem);
+    uint32_t items = 0;
+    bool begins = true;
+    for (uint32_t s = 0; at.u < u1; ++s) {
+      const uint32_t st = s % kStages, b = s & 1, k = items & 1;
+      if (begins) wait(&B.k_full[k], items >> 1);
+      wait(&B.q_full[st], s / kStages);
+      if (p.stall && s + 1 == p.stall) wait(&B.never, 0);  // testing hook
+      if (!good()) break;
+      const bool ends = at.ends_item(p);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        wait(&B.s_empty[x][b], (s >> 1) + 1);
+        if (!good()) break;
+        tc_fence_after();
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          const uint32_t off = (i >> 2) * (kTile * 128 >> 4) + (i & 3) * 2;
+          mma_ss(el, tm + x * 256 + b * 128, k_lo + (2 * k + x) * kT + off, kHi, q_lo + st * kT + off,
+                 kHi, kId, i > 0);
+        }
+        mma_commit(el, &B.s_full[x][b]);
+      }
+      if (!wait.ok()) break;
+      mma_commit(el, &B.q_empty[st]);
+      if (ends) {
+        mma_commit(el, &B.k_empty[k]);
+        ++items;
+      }
+      begins = ends;
+      at.advance(p);
+    }
+    // Nothing that this warp issued is still running when TMEM is freed.
+    mma_commit(el, &B.idle);
+    if (!mbar_wait(&B.idle, 0, kAttnPolls)) set_status(p.status, GDN_DEV_TIMEOUT);
+  } else if (any && warp == 10) {
+    // ---------------------------------------------------------------- the rows' denominators
+    float* lse = reinterpret_cast<float*>(smem + S::kLse);
+    float v[2][4];
+    StepCursor ahead = at;
+    auto fetch = [&](float (&y)[4]) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int row = ahead.rt * kTile + i * 32 + lane;
+        y[i] = 0.f;
+        if (ahead.u < u1 && row < ahead.shape.len)
+          y[i] = p.lse[(size_t)(ahead.base + row) * p.H + ahead.hk * p.G + ahead.g];
+      }
+      if (ahead.u < u1) ahead.advance(p);
+    };
+    fetch(v[0]);
+    fetch(v[1]);
+    bool ok = true;
+    for (uint32_t s = 0; ok && at.u + s < u1; s += 2) {
+#pragma unroll
+      for (uint32_t b = 0; b < 2; ++b) {
+        if (at.u + s + b >= u1) break;
+        for (int x = 0; x < 2; ++x) wait(&B.s_empty[x][b], (s >> 1) + 1);
+        if (!good()) {
+          ok = false;
+          break;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) lse[b * kTile + i * 32 + lane] = -kLog2e * v[b][i];
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.lse_full[b]);
+        fetch(v[b]);
+      }
+    }
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+// The sums of the items that span CTAs: block i those of the item that the end of CTA i's part cuts,
+// if it began there.
+__global__ void __launch_bounds__(256) reduce_kernel(const AttnWeightsParams p, const WeightsParts w) {
+  pdl_wait();
+  const int64_t U = w.first[p.N], grid = min((int64_t)gridDim.x + 1, U);
+  const int64_t cta = blockIdx.x;
+  if (cta + 1 >= grid) return;
+  const int64_t u0 = U * cta / grid, cut = U * (cta + 1) / grid;
+  int lo = 0, hi = p.N - 1;  // the last sequence that begins at or before the cut
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (w.first[m] <= cut) lo = m;
+    else hi = m - 1;
+  }
+  const int n = lo;
+  const Shape s(p, w.seq[n].y);
+  const int64_t head = s.before(s.pairs()) * p.G, r = cut - w.first[n];
+  const int hk = (int)(r / head), pair = s.pair_of(r - hk * head, p.G);
+  const int64_t first = w.first[n] + hk * head + s.before(pair) * p.G;
+  const int64_t last = w.first[n] + hk * head + s.before(pair + 1) * p.G;
+  if (first >= cut || first < u0) return;
+  float sum = w.part[(2 * cta + (first == u0 ? 0 : 1)) * 256 + threadIdx.x];
+  for (int64_t i = cta + 1; U * i / grid < last; ++i) sum += w.part[2 * i * 256 + threadIdx.x];
+  const int key = pair * 256 + threadIdx.x;
+  if (key >= s.len) return;
+  if (float* to = weight_at(p, n, hk, key)) *to = sum;
+}
+
+struct WeightsLayout {
+  size_t first, seq, part, total;
+};
+WeightsLayout layout(int N) {
+  WeightsLayout L{};
+  L.seq = align_up(sizeof(int64_t) * ((size_t)N + 1), 256);
+  L.part = align_up(L.seq + sizeof(int2) * N, 256);
+  L.total = L.part + sizeof(float) * 512 * num_sms();
+  return L;
+}
+
+template <int D>
+bool launch(const AttnWeightsParams& p, void* workspace, cudaStream_t s) {
+  const WeightsLayout L = layout(p.N);
+  char* ws = static_cast<char*>(workspace);
+  const WeightsParts w{reinterpret_cast<int64_t*>(ws), reinterpret_cast<int2*>(ws + L.seq),
+                       reinterpret_cast<float*>(ws + L.part)};
+  const uint32_t box[3] = {64, 1, kTile};
+  const uint64_t dim_q[3] = {D, (uint64_t)p.H, (uint64_t)p.T}, str_q[2] = {D * 2, (uint64_t)p.H * D * 2};
+  const uint64_t dim_k[3] = {D, (uint64_t)p.Hk, (uint64_t)p.T}, str_k[2] = {D * 2, (uint64_t)p.Hk * D * 2};
+  CUtensorMap tm_q, tm_k;
+  if (!encode_bf16_tmap(&tm_q, p.q, 3, dim_q, str_q, box) ||
+      !encode_bf16_tmap(&tm_k, p.k, 3, dim_k, str_k, box))
+    return false;
+  constexpr int smem = WeightsSmem<D>::kBytes;
+  ensure_smem_limit(reinterpret_cast<const void*>(weights_tc_kernel<D>), smem);
+  const int grid = num_sms();
+  if (launch_pdl(weights_tc_kernel<D>, dim3(grid), dim3(kThreads), smem, s, p, w, tm_q, tm_k) !=
+      cudaSuccess)
+    return false;
+  return grid == 1 ||
+         launch_pdl(reduce_kernel, dim3(grid - 1), dim3(256), 0, s, p, w) == cudaSuccess;
 }
 
 }  // namespace
 
-size_t attn_prefill_weights_workspace(int T, int N, int H, int Hk, int D) { return 256; }
+size_t attn_prefill_weights_workspace(int T, int N, int H, int Hk, int D) { return layout(N).total; }
 
 bool launch_attn_prefill_weights(const AttnWeightsParams& p, void* workspace, cudaStream_t s) {
-  const auto kernel = p.D == 128 ? prefill_weights_kernel<128> : prefill_weights_kernel<64>;
-  const int64_t blocks = ((int64_t)p.T * p.Hk + 3) / 4;
-  return launch_pdl(kernel, dim3((unsigned)blocks), dim3(128), 0, s, p) == cudaSuccess;
+  return p.D == 128 ? launch<128>(p, workspace, s) : launch<64>(p, workspace, s);
 }
 
 }  // namespace gdn
