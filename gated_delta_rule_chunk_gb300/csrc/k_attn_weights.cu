@@ -128,62 +128,62 @@ __device__ __forceinline__ int64_t steps_of(const AttnWeightsParams& p, int len)
 __device__ __forceinline__ bool find_steps(const AttnWeightsParams& p, const WeightsParts& w,
                                            StepCursor& at, int64_t& u1, bool scribe) {
   const int lane = threadIdx.x & 31;
-  int64_t U = 0, u0 = 0;
+  int64_t U = 0, u0 = -1;
+  // The sequences 32 at a time, twice: for the number of steps, then for u0's sequence; a batch of
+  // no more is looked at once.
 #pragma unroll 1
-  for (int pass = 0; pass < 2; ++pass) {
-    int64_t before = 0;
-    int carry = 0;
-#pragma unroll 1
-    for (int n0 = 0; n0 < p.N; n0 += 32) {
-      const int n = n0 + lane;
-      int b = 0, e = 0;
-      if (n < p.N) {
-        b = p.cu ? min(max(p.cu[n], 0), p.T) : 0;
-        e = p.cu ? min(max(p.cu[n + 1], 0), p.T) : p.T;
-        if (scribe && pass == 0 && p.cu && (p.cu[n] < 0 || p.cu[n + 1] < p.cu[n] || p.cu[n + 1] > p.T))
-          set_status(p.status, GDN_DEV_BAD_CU_SEQLENS);
-      }
-      b = max(b, carry);  // raised to the largest entry before it
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, b, o);
-        if (lane >= o) b = max(b, x);
-      }
-      e = n < p.N ? max(b, e) : b;
-      const int64_t c = n < p.N ? steps_of(p, e - b) : 0;
-      int64_t inc = c;
-#pragma unroll
-      for (int o = 1; o < 32; o <<= 1) {
-        const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
-        if (lane >= o) inc += x;
-      }
-      const int64_t first = before + inc - c;
-      if (pass == 0 && scribe && n < p.N) {
-        w.first[n] = first;
-        w.seq[n] = make_int2(b, e - b);
-      }
-      if (pass == 1) {
-        const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && u0 >= first && u0 < first + c);
-        if (hit) {
-          const int src = __ffs(hit) - 1;
-          at.n = n0 + src;
-          at.base = __shfl_sync(0xffffffffu, b, src);
-          at.end = __shfl_sync(0xffffffffu, e, src);
-          at.u = __shfl_sync(0xffffffffu, first, src);
-          break;
-        }
-      }
-      before += __shfl_sync(0xffffffffu, inc, 31);
-      carry = __shfl_sync(0xffffffffu, e, 31);
+  for (int n0 = 0, carry = 0;;) {
+    const int n = n0 + lane;
+    int b = 0, e = 0;
+    if (n < p.N) {
+      const int b_in = p.cu ? p.cu[n] : 0, e_in = p.cu ? p.cu[n + 1] : p.T;
+      if (scribe && u0 < 0 && (b_in < 0 || e_in < b_in || e_in > p.T))
+        set_status(p.status, GDN_DEV_BAD_CU_SEQLENS);
+      b = min(max(b_in, 0), p.T);
+      e = min(max(e_in, 0), p.T);
     }
-    if (pass == 0) {
-      U = before;
-      if (scribe && lane == 0) w.first[p.N] = U;
-      const int64_t grid = min((int64_t)gridDim.x, U);
+    b = max(b, carry);  // raised to the largest entry before it
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(0xffffffffu, b, o);
+      if (lane >= o) b = max(b, x);
+    }
+    e = n < p.N ? max(b, e) : b;
+    const int64_t c = n < p.N ? steps_of(p, e - b) : 0;
+    int64_t inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t x = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += x;
+    }
+    const int64_t first = U + inc - c;
+    const bool count = u0 < 0, last = n0 + 32 >= p.N;
+    if (count && scribe && n < p.N) {
+      w.first[n] = first;
+      w.seq[n] = make_int2(b, e - b);
+    }
+    const int64_t after = U + __shfl_sync(0xffffffffu, inc, 31);
+    if (count && last) {
+      if (scribe && lane == 0) w.first[p.N] = after;
+      const int64_t grid = min((int64_t)gridDim.x, after);
       if ((int64_t)blockIdx.x >= grid) return false;
-      u0 = U * blockIdx.x / grid;
-      u1 = U * (blockIdx.x + 1) / grid;
+      u0 = after * blockIdx.x / grid;
+      u1 = after * (blockIdx.x + 1) / grid;
     }
+    if (!count || (last && p.N <= 32)) {
+      const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && u0 >= first && u0 < first + c);
+      if (hit) {
+        const int src = __ffs(hit) - 1;
+        at.n = n0 + src;
+        at.base = __shfl_sync(0xffffffffu, b, src);
+        at.end = __shfl_sync(0xffffffffu, e, src);
+        at.u = __shfl_sync(0xffffffffu, first, src);
+        break;
+      }
+    }
+    U = last ? 0 : after;
+    carry = last ? 0 : __shfl_sync(0xffffffffu, e, 31);
+    n0 = last ? 0 : n0 + 32;
   }
   at.next = p.cu ? at.bound(p, at.n + 2) : p.T;
   at.shape = Shape(p, at.end - at.base);
@@ -285,37 +285,42 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
       if (at.rt >= kt && kt < q.nt) {
         const uint32_t t = tmem + lanes + X * 256 + b * 128;
         const float4* nl = reinterpret_cast<const float4*>(lse + b * kTile);
-        const bool masked = at.rt == kt || r0 < q.row0 || r0 + kTile > q.len;
+        // columns [lo, hi) count for this key; [lo0, hi) for the warp's first, [lo1, hi) for its last
+        const int lo = max(key, q.row0) - r0, hi = q.len - r0;
+        const int lo0 = __shfl_sync(0xffffffffu, lo, 0), lo1 = __shfl_sync(0xffffffffu, lo, 31);
         float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
         float v[2][32];
         tmem_ld32(t, v[0]);
-        if (!masked) {
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            tmem_ld_wait();
-            if (ch < 3) tmem_ld32(t + 32 * (ch + 1), v[(ch + 1) & 1]);
+        for (int ch = 0; ch < 4; ++ch) {
+          tmem_ld_wait();
+          if (ch < 3) tmem_ld32(t + 32 * (ch + 1), v[(ch + 1) & 1]);
+          const int c0 = ch * 32;
+          if (c0 + 32 <= lo0 || c0 >= hi) continue;
+          if (c0 >= lo1 && c0 + 32 <= hi) {
+            // stage by stage: loads, sums, exponentials, none waiting for one just issued
+            float4 m[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) m[i] = nl[ch * 8 + i];
+            float2 x[16];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              const float4 m = nl[ch * 8 + i];
               const float* y = v[ch & 1] + 4 * i;
-              const float2 x0 = fma2(make_float2(y[0], y[1]), c2, make_float2(m.x, m.y));
-              const float2 x1 = fma2(make_float2(y[2], y[3]), c2, make_float2(m.z, m.w));
-              acc[0] = add2(acc[0], make_float2(ex2(x0.x), ex2(x0.y)));
-              acc[1] = add2(acc[1], make_float2(ex2(x1.x), ex2(x1.y)));
+              x[2 * i] = fma2(make_float2(y[0], y[1]), c2, make_float2(m[i].x, m[i].y));
+              x[2 * i + 1] = fma2(make_float2(y[2], y[3]), c2, make_float2(m[i].z, m[i].w));
             }
-          }
-        } else {
-          const int lo = max(key, q.row0) - r0, hi = q.len - r0;  // columns that count
 #pragma unroll
-          for (int ch = 0; ch < 4; ++ch) {
-            tmem_ld_wait();
-            if (ch < 3) tmem_ld32(t + 32 * (ch + 1), v[(ch + 1) & 1]);
+            for (int i = 0; i < 16; ++i) x[i] = make_float2(ex2(x[i].x), ex2(x[i].y));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) acc[i & 1] = add2(acc[i & 1], x[i]);
+          } else {
+            const uint32_t counts = (lo <= c0 ? 0xffffffffu : lo >= c0 + 32 ? 0u : 0xffffffffu << (lo - c0)) &
+                                    (hi >= c0 + 32 ? 0xffffffffu : (1u << (hi - c0)) - 1);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const int col = ch * 32 + i;
-              const float y = ex2(fmaf(v[ch & 1][i], c, lse[b * kTile + col]));
+              const float y = ex2(fmaf(v[ch & 1][i], c, lse[b * kTile + c0 + i]));
               float& a = i & 1 ? acc[i >> 1 & 1].y : acc[i >> 1 & 1].x;
-              a += col >= lo && col < hi ? y : 0.f;
+              a += counts >> i & 1u ? y : 0.f;
             }
           }
         }
