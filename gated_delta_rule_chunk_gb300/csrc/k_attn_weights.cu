@@ -5,11 +5,15 @@
 // its sum is one thread's: no exchange between threads, and no weights are stored. A step is 128
 // query rows (tokens of one head) against a pair of key tiles, A and B, of 128 keys, so that a Q
 // tile is read once for both: two M = 128, N = 128 products, 2 x 16384 exponentials.
-//   warps 0-3, 4-7  one thread per key of A, B: 2^(c s - lse2) of its 128 columns, summed in fp32, four
-//                   partial sums a step
+//   warps 0-3, 4-7  one thread per key of A, B: 2^(c s) of its 128 columns, summed in fp32, four partial
+//                   sums a step
 //   warp 8          TMA loads: a pair's K tiles (two pairs), a ring of Q tiles
 //   warp 9          issues the MMAs; a step's scores are in one of two TMEM buffers a tile
-//   warp 10         the rows' -lse * log2(e), from two steps ahead, into shared memory
+//   warp 10         the rows' -lse / scale as 16 more elements of the product's depth: three bf16 parts
+//                   (24 bits) against ones, so that the scores come out as s - lse / scale. (Read by
+//                   the threads instead, 128 values a step each, they took as much of shared memory's
+//                   bandwidth as the products' operands, which take nearly all of it: 2,300 cycles
+//                   a step.)
 // The steps of all (sequence, key head, key pair) items form one list, and each SM takes an equal
 // contiguous part of it: causal items are of any length, and one prompt is spread over the GPU. An
 // item that spans CTAs leaves partial sums in the workspace, which reduce_kernel adds in the order
@@ -24,6 +28,16 @@ namespace gdn {
 
 namespace {
 
+// Two fp32 products in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n .reg .b64 x, y, w;\n mov.b64 x, {%2, %3};\n mov.b64 y, {%4, %5};\n"
+      " mul.rn.f32x2 w, x, y;\n mov.b64 {%0, %1}, w;\n}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+
 constexpr int kTile = 128;        // keys of a tile, rows of a step
 constexpr int kThreads = 11 * 32;
 constexpr float kLog2e = 1.44269504088896340736f;
@@ -34,8 +48,9 @@ struct WeightsSmem {
   static constexpr int kStages = D == 128 ? 2 : 4;          // Q tiles
   static constexpr int kK = 0;                              // two pairs of K tiles
   static constexpr int kQ = 4 * kBytesTile;
-  static constexpr int kLse = kQ + kStages * kBytesTile;    // [2][128]
-  static constexpr int kBars = kLse + 2 * kTile * 4;
+  static constexpr int kLse = kQ + kStages * kBytesTile;    // [kStages][128 rows of 16], no swizzle
+  static constexpr int kOnes = kLse + kStages * kTile * 32;
+  static constexpr int kBars = kOnes + kTile * 32;
   static constexpr int kBytes = kBars + 256 + 1024;         // + alignment of the tiles
 };
 
@@ -43,7 +58,7 @@ template <int kStages>
 struct WeightsBars {
   uint64_t k_full[2], k_empty[2], q_full[kStages], q_empty[kStages];
   uint64_t s_full[2][2], s_empty[2][2];  // [tile][buffer]
-  uint64_t lse_full[2], idle, never;
+  uint64_t lse_full[kStages], idle, never;
   uint32_t tmem;
 };
 
@@ -228,7 +243,6 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
       for (int i = 0; i < 2; ++i) {
         mbar_init(&B.k_full[i], 1);
         mbar_init(&B.k_empty[i], 1);
-        mbar_init(&B.lse_full[i], 1);
         for (int x = 0; x < 2; ++x) {
           mbar_init(&B.s_full[x][i], 1);
           mbar_init(&B.s_empty[x][i], 4);
@@ -237,6 +251,7 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
       for (int i = 0; i < kStages; ++i) {
         mbar_init(&B.q_full[i], 1);
         mbar_init(&B.q_empty[i], 1);
+        mbar_init(&B.lse_full[i], 1);
       }
       mbar_init(&B.idle, 1);
       mbar_init(&B.never, 1);
@@ -248,6 +263,14 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
     tmem_alloc(&B.tmem, 512);
     tmem_relinquish();
   }
+  // The operands of the denominators: element k of row r at (r / 8) 256 + (k / 8) 128 + (r % 8) 16 + 2 (k % 8)
+  // bytes; the keys' side is three ones a row, the rows' side is written step by step.
+  for (int i = threadIdx.x; i < (kStages + 1) * kTile * 2; i += kThreads) {
+    const bool ones = i >= kStages * kTile * 2 && (i >> 3 & 1) == 0;
+    *reinterpret_cast<uint4*>(smem + S::kLse + i * 16) = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0)
+                                                              : make_uint4(0, 0, 0, 0);
+  }
+  fence_async_smem();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -268,7 +291,6 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
     // ---------------------------------------------------------------- exponentials and sums
     const int X = warp >> 2, of_tile = (warp & 3) * 32 + lane;
     const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-    const float* lse = reinterpret_cast<const float*>(smem + S::kLse);
     const float c = p.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
     float sum = 0.f;
@@ -278,13 +300,11 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
       const uint32_t b = s & 1;
       const int kt = 2 * at.pair + X, r0 = at.rt * kTile, key = kt * kTile + of_tile;
       const Shape& q = at.shape;
-      wait(&B.lse_full[b], s >> 1);
       wait(&B.s_full[X][b], s >> 1);
       if (!good()) break;
       tc_fence_after();
       if (at.rt >= kt && kt < q.nt) {
         const uint32_t t = tmem + lanes + X * 256 + b * 128;
-        const float4* nl = reinterpret_cast<const float4*>(lse + b * kTile);
         // columns [lo, hi) count for this key; [lo0, hi) for the warp's first, [lo1, hi) for its last
         const int lo = max(key, q.row0) - r0, hi = q.len - r0;
         const int lo0 = __shfl_sync(0xffffffffu, lo, 0), lo1 = __shfl_sync(0xffffffffu, lo, 31);
@@ -298,27 +318,17 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
           const int c0 = ch * 32;
           if (c0 + 32 <= lo0 || c0 >= hi) continue;
           if (c0 >= lo1 && c0 + 32 <= hi) {
-            // stage by stage: loads, sums, exponentials, none waiting for one just issued
-            float4 m[8];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) m[i] = nl[ch * 8 + i];
-            float2 x[16];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float* y = v[ch & 1] + 4 * i;
-              x[2 * i] = fma2(make_float2(y[0], y[1]), c2, make_float2(m[i].x, m[i].y));
-              x[2 * i + 1] = fma2(make_float2(y[2], y[3]), c2, make_float2(m[i].z, m[i].w));
+            for (int i = 0; i < 16; ++i) {
+              const float2 x = mul2(make_float2(v[ch & 1][2 * i], v[ch & 1][2 * i + 1]), c2);
+              acc[i & 1] = add2(acc[i & 1], make_float2(ex2(x.x), ex2(x.y)));
             }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) x[i] = make_float2(ex2(x[i].x), ex2(x[i].y));
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[i & 1] = add2(acc[i & 1], x[i]);
           } else {
             const uint32_t counts = (lo <= c0 ? 0xffffffffu : lo >= c0 + 32 ? 0u : 0xffffffffu << (lo - c0)) &
                                     (hi >= c0 + 32 ? 0xffffffffu : (1u << (hi - c0)) - 1);
 #pragma unroll
             for (int i = 0; i < 32; ++i) {
-              const float y = ex2(fmaf(v[ch & 1][i], c, lse[b * kTile + c0 + i]));
+              const float y = ex2(v[ch & 1][i] * c);
               float& a = i & 1 ? acc[i >> 1 & 1].y : acc[i >> 1 & 1].x;
               a += counts >> i & 1u ? y : 0.f;
             }
@@ -382,6 +392,9 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
     constexpr uint32_t kHi = (1u << 14) | (2u << 29) | (1024 >> 4);
     const uint32_t k_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kK), 16, 1024));
     const uint32_t q_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024));
+    const uint32_t ones_lo = uniform((uint32_t)sdesc_kmajor(smem_addr(smem + S::kOnes), 128, 256));
+    const uint32_t lse_lo = uniform((uint32_t)sdesc_kmajor(smem_addr(smem + S::kLse), 128, 256));
+    constexpr uint32_t kFlat = (1u << 14) | (256 >> 4);  // no swizzle
     const uint32_t el = elect_one(), tm = uniform(tmem);
     uint32_t items = 0;
     bool begins = true;
@@ -389,6 +402,7 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
       const uint32_t st = s % kStages, b = s & 1, k = items & 1;
       if (begins) wait(&B.k_full[k], items >> 1);
       wait(&B.q_full[st], s / kStages);
+      wait(&B.lse_full[st], s / kStages);
       if (p.stall && s + 1 == p.stall) wait(&B.never, 0);  // testing hook
       if (!good()) break;
       const bool ends = at.ends_item(p);
@@ -403,6 +417,7 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
           mma_ss(el, tm + x * 256 + b * 128, k_lo + (2 * k + x) * kT + off, kHi, q_lo + st * kT + off,
                  kHi, kId, i > 0);
         }
+        mma_ss(el, tm + x * 256 + b * 128, ones_lo, kFlat, lse_lo + st * (kTile * 32 >> 4), kFlat, kId, 1);
         mma_commit(el, &B.s_full[x][b]);
       }
       if (!wait.ok()) break;
@@ -419,8 +434,8 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
     if (!mbar_wait(&B.idle, 0, kAttnPolls)) set_status(p.status, GDN_DEV_TIMEOUT);
   } else if (any && warp == 10) {
     // ---------------------------------------------------------------- the rows' denominators
-    float* lse = reinterpret_cast<float*>(smem + S::kLse);
-    float v[2][4];
+    const float down = -1.0f / p.scale;
+    float v[kStages][4];
     StepCursor ahead = at;
     auto fetch = [&](float (&y)[4]) {
 #pragma unroll
@@ -432,23 +447,32 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
       }
       if (ahead.u < u1) ahead.advance(p);
     };
-    fetch(v[0]);
-    fetch(v[1]);
-    bool ok = true;
-    for (uint32_t s = 0; ok && at.u + s < u1; s += 2) {
 #pragma unroll
-      for (uint32_t b = 0; b < 2; ++b) {
-        if (at.u + s + b >= u1) break;
-        for (int x = 0; x < 2; ++x) wait(&B.s_empty[x][b], (s >> 1) + 1);
+    for (int i = 0; i < kStages; ++i) fetch(v[i]);
+    const int64_t n = u1 - at.u;
+    bool ok = true;
+    for (uint32_t s = 0; ok && s < n; s += kStages) {
+#pragma unroll
+      for (uint32_t st = 0; st < kStages; ++st) {
+        if (s + st >= n) break;
+        wait(&B.q_empty[st], s / kStages + 1);
         if (!good()) {
           ok = false;
           break;
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lse[b * kTile + i * 32 + lane] = -kLog2e * v[b][i];
+        for (int i = 0; i < 4; ++i) {
+          const int r = i * 32 + lane;
+          const float x = v[st][i] * down;
+          const float hi = __bfloat162float(__float2bfloat16_rn(x));
+          const float y = isfinite(hi) ? x - hi : 0.f, mid = __bfloat162float(__float2bfloat16_rn(y));
+          *reinterpret_cast<uint4*>(smem + S::kLse + st * kTile * 32 + (r >> 3) * 256 + (r & 7) * 16) =
+              make_uint4(pack_bf16(hi, mid), pack_bf16(y - mid, 0.f), 0, 0);
+        }
+        fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.lse_full[b]);
-        fetch(v[b]);
+        if (lane == 0) mbar_arrive(&B.lse_full[st]);
+        fetch(v[st]);
       }
     }
   }
