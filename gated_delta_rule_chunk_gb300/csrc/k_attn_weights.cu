@@ -5,11 +5,12 @@
 // its sum is one thread's: no exchange between threads, and no weights are stored. A step is 128
 // query rows (tokens of one head) against a pair of key tiles, A and B, of 128 keys, so that a Q
 // tile is read once for both: two M = 128, N = 128 products, 2 x 16384 exponentials.
-//   warps 0-3, 4-7  one thread per key of A, B: 2^(c s) of its 128 columns, summed in fp32, four partial
-//                   sums a step
-//   warp 8          TMA loads: a pair's K tiles (two pairs), a ring of Q tiles
-//   warp 9          issues the MMAs; a step's scores are in one of two TMEM buffers a tile
-//   warp 10         the rows' -lse / scale as 16 more elements of the product's depth: three bf16 parts
+//   warps 0-7, 8-15 two threads per key of A, B: 2^(c s) of 64 of its 128 columns each, summed in fp32,
+//                   four partial sums a step. (With one thread a key, eight warps, the exponentials'
+//                   latency shows: 405 cycles for 32 columns, 256 of them the unit's.)
+//   warp 16         TMA loads: a pair's K tiles (two pairs), a ring of Q tiles
+//   warp 17         issues the MMAs; a step's scores are in one of two TMEM buffers a tile
+//   warp 18         the rows' -lse / scale as 16 more elements of the product's depth: three bf16 parts
 //                   (24 bits) against ones, so that the scores come out as s - lse / scale. (Read by
 //                   the threads instead, 128 values a step each, they took as much of shared memory's
 //                   bandwidth as the products' operands, which take nearly all of it: 2,300 cycles
@@ -38,27 +39,40 @@ __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
   return d;
 }
 
+// Whether the phase with this parity is complete; does not wait.
+__device__ __forceinline__ bool mbar_test(uint64_t* bar, uint32_t phase) {
+  uint32_t ok;
+  asm volatile(
+      "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+      " selp.u32 %0, 1, 0, p;\n}\n"
+      : "=r"(ok)
+      : "r"(smem_addr(bar)), "r"(phase)
+      : "memory");
+  return ok != 0;
+}
+
 constexpr int kTile = 128;        // keys of a tile, rows of a step
-constexpr int kThreads = 11 * 32;
+constexpr int kThreads = 19 * 32;
 constexpr float kLog2e = 1.44269504088896340736f;
 
 template <int D>
 struct WeightsSmem {
   static constexpr int kBytesTile = kTile * D * 2;
-  static constexpr int kStages = D == 128 ? 2 : 4;          // Q tiles
+  static constexpr int kStages = 2;                         // Q tiles
   static constexpr int kK = 0;                              // two pairs of K tiles
   static constexpr int kQ = 4 * kBytesTile;
   static constexpr int kLse = kQ + kStages * kBytesTile;    // [kStages][128 rows of 16], no swizzle
   static constexpr int kOnes = kLse + kStages * kTile * 32;
-  static constexpr int kBars = kOnes + kTile * 32;
+  static constexpr int kSums = kOnes + kTile * 32;          // [2][128], from the one half to the other
+  static constexpr int kBars = kSums + 2 * kTile * 4;
   static constexpr int kBytes = kBars + 256 + 1024;         // + alignment of the tiles
 };
 
-template <int kStages>
+// Step s uses the Q tile, the denominators and the score buffers s % 2: what it read is free, and
+// its scores are there, when its products are complete (s_full).
 struct WeightsBars {
-  uint64_t k_full[2], k_empty[2], q_full[kStages], q_empty[kStages];
-  uint64_t s_full[2][2], s_empty[2][2];  // [tile][buffer]
-  uint64_t lse_full[kStages], idle, never;
+  uint64_t k_full[2], k_empty[2], q_full[2], lse_full[2], s_full[2], s_empty[2];
+  uint64_t sum_full[2], sum_empty[2], idle, never;
   uint32_t tmem;
 };
 
@@ -99,7 +113,6 @@ struct Shape {
 
 // A place in the list of steps.
 struct StepCursor {
-  int64_t u;
   int n, hk, pair, rt, g;
   int base, end, next;  // rows of the sequence, and the next entry of cu_seqlens
   Shape shape;
@@ -108,14 +121,12 @@ struct StepCursor {
     return i <= p.N ? min(max(p.cu[i], 0), p.T) : p.T;
   }
   __device__ bool starts_item() const { return g == 0 && rt == shape.first_row_tile(pair); }
-  __device__ bool ends_item(const AttnWeightsParams& p) const {
-    return g == p.G - 1 && rt == shape.nt - 1;
+  // steps from here to the item's end
+  __device__ uint32_t left(const AttnWeightsParams& p) const {
+    return (uint32_t)(shape.nt - rt) * p.G - g;
   }
-  __device__ void advance(const AttnWeightsParams& p) {
-    ++u;
-    if (++g < p.G) return;
+  __device__ void next_item(const AttnWeightsParams& p) {
     g = 0;
-    if (++rt < shape.nt) return;
     if (++pair >= shape.pairs()) {
       pair = 0;
       if (++hk >= p.Hk) {
@@ -131,6 +142,11 @@ struct StepCursor {
     }
     rt = shape.first_row_tile(pair);
   }
+  __device__ void advance(const AttnWeightsParams& p) {
+    if (++g < p.G) return;
+    g = 0;
+    if (++rt >= shape.nt) next_item(p);
+  }
 };
 
 __device__ __forceinline__ int64_t steps_of(const AttnWeightsParams& p, int len) {
@@ -138,12 +154,13 @@ __device__ __forceinline__ int64_t steps_of(const AttnWeightsParams& p, int len)
   return s.before(s.pairs()) * p.G * p.Hk;
 }
 
-// CTA blockIdx.x's steps [at.u, u1), found by a warp; whether it has any. The scribe writes what
+// The first of CTA blockIdx.x's steps and their number, found by a warp. The scribe writes what
 // reduce_kernel needs.
-__device__ __forceinline__ bool find_steps(const AttnWeightsParams& p, const WeightsParts& w,
-                                           StepCursor& at, int64_t& u1, bool scribe) {
+__device__ __forceinline__ uint32_t find_steps(const AttnWeightsParams& p, const WeightsParts& w,
+                                               StepCursor& at, bool scribe) {
   const int lane = threadIdx.x & 31;
-  int64_t U = 0, u0 = -1;
+  int64_t U = 0, u0 = -1, r = 0;
+  uint32_t steps = 0;
   // The sequences 32 at a time, twice: for the number of steps, then for u0's sequence; a batch of
   // no more is looked at once.
 #pragma unroll 1
@@ -181,9 +198,9 @@ __device__ __forceinline__ bool find_steps(const AttnWeightsParams& p, const Wei
     if (count && last) {
       if (scribe && lane == 0) w.first[p.N] = after;
       const int64_t grid = min((int64_t)gridDim.x, after);
-      if ((int64_t)blockIdx.x >= grid) return false;
+      if ((int64_t)blockIdx.x >= grid) return 0;
       u0 = after * blockIdx.x / grid;
-      u1 = after * (blockIdx.x + 1) / grid;
+      steps = (uint32_t)(after * (blockIdx.x + 1) / grid - u0);
     }
     if (!count || (last && p.N <= 32)) {
       const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && u0 >= first && u0 < first + c);
@@ -192,7 +209,7 @@ __device__ __forceinline__ bool find_steps(const AttnWeightsParams& p, const Wei
         at.n = n0 + src;
         at.base = __shfl_sync(0xffffffffu, b, src);
         at.end = __shfl_sync(0xffffffffu, e, src);
-        at.u = __shfl_sync(0xffffffffu, first, src);
+        r = u0 - __shfl_sync(0xffffffffu, first, src);
         break;
       }
     }
@@ -203,15 +220,13 @@ __device__ __forceinline__ bool find_steps(const AttnWeightsParams& p, const Wei
   at.next = p.cu ? at.bound(p, at.n + 2) : p.T;
   at.shape = Shape(p, at.end - at.base);
   const int64_t head = at.shape.before(at.shape.pairs()) * p.G;
-  int64_t r = u0 - at.u;
   at.hk = (int)(r / head);
   r -= at.hk * head;
   at.pair = at.shape.pair_of(r, p.G);
   r -= at.shape.before(at.pair) * p.G;
   at.rt = at.shape.first_row_tile(at.pair) + (int)(r / p.G);
   at.g = (int)(r % p.G);
-  at.u = u0;
-  return true;
+  return steps;
 }
 
 // Where the weight of key `key` of sequence n goes; null where its place does not exist.
@@ -233,25 +248,17 @@ __global__ void __launch_bounds__(kThreads, 1)
 weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
                   const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k) {
   using S = WeightsSmem<D>;
-  constexpr int kStages = S::kStages;
   extern __shared__ char raw_smem[];
   char* smem = raw_smem + (-smem_u32(raw_smem) & 1023u);
-  auto& B = *reinterpret_cast<WeightsBars<kStages>*>(smem + S::kBars);
+  auto& B = *reinterpret_cast<WeightsBars*>(smem + S::kBars);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  if (warp == 9) {
+  if (warp == 17) {
     if (lane == 0) {
       for (int i = 0; i < 2; ++i) {
-        mbar_init(&B.k_full[i], 1);
-        mbar_init(&B.k_empty[i], 1);
-        for (int x = 0; x < 2; ++x) {
-          mbar_init(&B.s_full[x][i], 1);
-          mbar_init(&B.s_empty[x][i], 4);
-        }
-      }
-      for (int i = 0; i < kStages; ++i) {
-        mbar_init(&B.q_full[i], 1);
-        mbar_init(&B.q_empty[i], 1);
-        mbar_init(&B.lse_full[i], 1);
+        for (uint64_t* one : {B.k_full, B.k_empty, B.q_full, B.lse_full, B.s_full}) mbar_init(one + i, 1);
+        mbar_init(&B.s_empty[i], 16);
+        mbar_init(&B.sum_full[i], 4);
+        mbar_init(&B.sum_empty[i], 4);
       }
       mbar_init(&B.idle, 1);
       mbar_init(&B.never, 1);
@@ -265,8 +272,8 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
   }
   // The operands of the denominators: element k of row r at (r / 8) 256 + (k / 8) 128 + (r % 8) 16 + 2 (k % 8)
   // bytes; the keys' side is three ones a row, the rows' side is written step by step.
-  for (int i = threadIdx.x; i < (kStages + 1) * kTile * 2; i += kThreads) {
-    const bool ones = i >= kStages * kTile * 2 && (i >> 3 & 1) == 0;
+  for (int i = threadIdx.x; i < 3 * kTile * 2; i += kThreads) {
+    const bool ones = i >= 2 * kTile * 2 && (i >> 3 & 1) == 0;
     *reinterpret_cast<uint4*>(smem + S::kLse + i * 16) = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0, 0)
                                                               : make_uint4(0, 0, 0, 0);
   }
@@ -276,89 +283,127 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
   tc_fence_after();
   const uint32_t tmem = B.tmem;
   pdl_wait();
-  StepCursor at(p);
-  int64_t u1 = 0;
   pdl_release();
-  const bool any = find_steps(p, parts, at, u1, blockIdx.x == 0 && warp == 0);
+  StepCursor at(p);
+  const uint32_t steps = find_steps(p, parts, at, blockIdx.x == 0 && warp == 0);
   Waiter wait(p.status, p.polls);
-  // The warp gives up as one.
+  // A warp gives up as one, at the next such point; up to it works on whatever is there.
   auto good = [&] {
     const bool ok = __all_sync(0xffffffffu, wait.ok());
     if (!ok) wait.limit = 0;
     return ok;
   };
-  if (any && warp < 8) {
+  if (steps > 0 && warp < 16) {
     // ---------------------------------------------------------------- exponentials and sums
-    const int X = warp >> 2, of_tile = (warp & 3) * 32 + lane;
-    const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+    const int X = warp >> 3, half = warp >> 2 & 1, of_tile = (warp & 3) * 32 + lane;
+    float* other = reinterpret_cast<float*>(smem + S::kSums) + X * kTile + of_tile;
+    const uint32_t t = tmem + ((uint32_t)((warp & 3) * 32) << 16) + X * 256 + half * 64;
     const float c = p.scale * kLog2e;
     const float2 c2 = make_float2(c, c);
-    float sum = 0.f;
     bool from_start = at.starts_item();
-    int slot = 0;
-    for (uint32_t s = 0; at.u < u1; ++s, at.advance(p)) {
-      const uint32_t b = s & 1;
-      const int kt = 2 * at.pair + X, r0 = at.rt * kTile, key = kt * kTile + of_tile;
+    uint32_t s = 0, items = 0;
+    float v[2][16];
+    bool loaded = false;  // v[0] is being loaded for step s
+    for (uint32_t left = steps; left > 0;) {
       const Shape& q = at.shape;
-      wait(&B.s_full[X][b], s >> 1);
-      if (!good()) break;
-      tc_fence_after();
-      if (at.rt >= kt && kt < q.nt) {
-        const uint32_t t = tmem + lanes + X * 256 + b * 128;
-        // columns [lo, hi) count for this key; [lo0, hi) for the warp's first, [lo1, hi) for its last
-        const int lo = max(key, q.row0) - r0, hi = q.len - r0;
-        const int lo0 = __shfl_sync(0xffffffffu, lo, 0), lo1 = __shfl_sync(0xffffffffu, lo, 31);
-        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-        float v[2][32];
-        tmem_ld32(t, v[0]);
+      const int kt = 2 * at.pair + X, key = kt * kTile + of_tile;
+      float sum = 0.f;
+      bool ends = false;
+      while (left > 0 && !ends) {
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};  // of a row tile's steps
+        // Columns [lo, hi) of this half count for the key; [lo0, hi) for the warp's first key,
+        // [lo1, hi) for its last.
+        const int r0 = at.rt * kTile + half * 64;
+        const int lo = max(key, q.row0) - r0, hi = at.rt >= kt && kt < q.nt ? q.len - r0 : INT_MIN;
+        const int lo0 = max(key - lane, q.row0) - r0, lo1 = max(key - lane + 31, q.row0) - r0;
+        auto chunk = [&](const float (&y)[16], int c0) {
+          if (c0 + 16 <= lo0 || c0 >= hi) return;
+          if (c0 >= lo1 && c0 + 16 <= hi) {
 #pragma unroll
-        for (int ch = 0; ch < 4; ++ch) {
-          tmem_ld_wait();
-          if (ch < 3) tmem_ld32(t + 32 * (ch + 1), v[(ch + 1) & 1]);
-          const int c0 = ch * 32;
-          if (c0 + 32 <= lo0 || c0 >= hi) continue;
-          if (c0 >= lo1 && c0 + 32 <= hi) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float2 x = mul2(make_float2(v[ch & 1][2 * i], v[ch & 1][2 * i + 1]), c2);
+            for (int i = 0; i < 8; ++i) {
+              const float2 x = mul2(make_float2(y[2 * i], y[2 * i + 1]), c2);
               acc[i & 1] = add2(acc[i & 1], make_float2(ex2(x.x), ex2(x.y)));
             }
-          } else {
-            const uint32_t counts = (lo <= c0 ? 0xffffffffu : lo >= c0 + 32 ? 0u : 0xffffffffu << (lo - c0)) &
-                                    (hi >= c0 + 32 ? 0xffffffffu : (1u << (hi - c0)) - 1);
-#pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float y = ex2(v[ch & 1][i] * c);
-              float& a = i & 1 ? acc[i >> 1 & 1].y : acc[i >> 1 & 1].x;
-              a += counts >> i & 1u ? y : 0.f;
-            }
+            return;
           }
+          const uint32_t counts =
+              (lo <= c0 ? 0xffffu : lo >= c0 + 16 ? 0u : 0xffffu << (lo - c0)) &
+              (hi >= c0 + 16 ? 0xffffu : (1u << (hi - c0)) - 1);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float x = ex2(y[i] * c);
+            float& a = i & 1 ? acc[i >> 1 & 1].y : acc[i >> 1 & 1].x;
+            a += counts >> i & 1u ? x : 0.f;
+          }
+        };
+        const uint32_t todo = min((uint32_t)(p.G - at.g), left), end = s + todo;
+        for (; s < end; ++s) {
+          const uint32_t b = s & 1;
+          if (!loaded) {
+            wait(&B.s_full[b], s >> 1);
+            tc_fence_after();
+            tmem_ld16(t + b * 128, v[0]);
+          }
+#pragma unroll
+          for (int ch = 0; ch < 3; ++ch) {
+            tmem_ld_wait();
+            tmem_ld16(t + b * 128 + 16 * (ch + 1), v[(ch + 1) & 1]);
+            chunk(v[ch & 1], 16 * ch);
+          }
+          tmem_ld_wait();
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&B.s_empty[b]);
+          // The next step's first columns come while this one's last are worked on, where they are
+          // there.
+          loaded = s + 1 < steps &&
+                   __all_sync(0xffffffffu, mbar_test(&B.s_full[b ^ 1], ((s + 1) >> 1) & 1));
+          if (loaded) {
+            tc_fence_after();
+            tmem_ld16(t + (b ^ 1) * 128, v[0]);
+          }
+          chunk(v[1], 48);
         }
         sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-      }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&B.s_empty[X][b]);
-      const bool ends = at.ends_item(p);
-      if (ends || at.u + 1 == u1) {
-        if (ends && from_start) {
-          if (key < q.len)
-            if (float* to = weight_at(p, at.n, at.hk, key)) *to = sum;
-        } else {
-          parts.part[(size_t)(2 * blockIdx.x + slot) * 256 + X * kTile + of_tile] = sum;
+        left -= todo;
+        at.g += (int)todo;
+        if (at.g == p.G) {
+          at.g = 0;
+          ends = ++at.rt == q.nt;
         }
-        sum = 0.f;
-        from_start = true;
-        slot = 1;
+        if (!good()) break;
       }
+      // The end of the item, or of the CTA's part of it.
+      if (half == 1) {
+        wait(&B.sum_empty[X], items + 1);
+        *other = sum;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.sum_full[X]);
+      } else {
+        wait(&B.sum_full[X], items);
+        sum += *other;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&B.sum_empty[X]);
+        if (!ends || !from_start) {
+          parts.part[(size_t)(2 * blockIdx.x + (items > 0)) * 256 + X * kTile + of_tile] = sum;
+        } else if (key < q.len) {
+          if (float* to = weight_at(p, at.n, at.hk, key)) *to = sum;
+        }
+      }
+      if (!good()) break;
+      ++items;
+      from_start = true;
+      if (ends) at.next_item(p);
     }
-  } else if (any && warp == 8) {
+  } else if (steps > 0 && warp == 16) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {
-      uint32_t items = 0, steps = 0;
-      for (bool begins = true; at.u < u1; ++steps) {
-        if (begins) {
+      uint32_t items = 0, in_item = 0, s = 0;  // in_item: steps to come of the item
+      for (; s < steps; ++s, --in_item, at.advance(p)) {
+        const uint32_t b = s & 1;
+        if (in_item == 0) {
           const uint32_t k = items & 1;
+          in_item = at.left(p);
           wait(&B.k_empty[k], (items >> 1) + 1);
           if (!wait.ok()) break;
           const bool two = 2 * at.pair + 1 < at.shape.nt;
@@ -369,110 +414,112 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
                           at.base + (2 * at.pair + x) * kTile, &B.k_full[k]);
           ++items;
         }
-        const uint32_t st = steps % kStages;
-        wait(&B.q_empty[st], steps / kStages + 1);
+        wait(&B.s_full[b], (s >> 1) + 1);
         if (!wait.ok()) break;
-        mbar_expect_tx(&B.q_full[st], S::kBytesTile);
+        mbar_expect_tx(&B.q_full[b], S::kBytesTile);
         for (int d = 0; d < D; d += 64)
-          tma_load_3d(smem + S::kQ + st * S::kBytesTile + d * 256, &tm_q, d, at.hk * p.G + at.g,
-                      at.base + at.rt * kTile, &B.q_full[st]);
-        begins = at.ends_item(p);
-        at.advance(p);
+          tma_load_3d(smem + S::kQ + b * S::kBytesTile + d * 256, &tm_q, d, at.hk * p.G + at.g,
+                      at.base + at.rt * kTile, &B.q_full[b]);
       }
       // Copies in flight end before the CTA does (all have been waited for already, unless someone
       // gave up).
       for (uint32_t i = 0; i < 2 && i < items; ++i)
         mbar_wait(&B.k_full[i], ((items - 1 - i) / 2) & 1, kAttnPolls);
-      for (uint32_t i = 0; i < kStages && i < steps; ++i)
-        mbar_wait(&B.q_full[i], ((steps - 1 - i) / kStages) & 1, kAttnPolls);
+      for (uint32_t i = 0; i < 2 && i < s; ++i)
+        mbar_wait(&B.q_full[i], ((s - 1 - i) / 2) & 1, kAttnPolls);
     }
-  } else if (any && warp == 9) {
+  } else if (steps > 0 && warp == 17) {
     // ---------------------------------------------------------------- products
     constexpr uint32_t kId = idesc_bf16_f32(128, kTile), kT = S::kBytesTile >> 4;
     constexpr uint32_t kHi = (1u << 14) | (2u << 29) | (1024 >> 4);
+    constexpr uint32_t kFlat = (1u << 14) | (256 >> 4);  // no swizzle
     const uint32_t k_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kK), 16, 1024));
     const uint32_t q_lo = uniform((uint32_t)sdesc_sw128(smem_addr(smem + S::kQ), 16, 1024));
     const uint32_t ones_lo = uniform((uint32_t)sdesc_kmajor(smem_addr(smem + S::kOnes), 128, 256));
     const uint32_t lse_lo = uniform((uint32_t)sdesc_kmajor(smem_addr(smem + S::kLse), 128, 256));
-    constexpr uint32_t kFlat = (1u << 14) | (256 >> 4);  // no swizzle
     const uint32_t el = elect_one(), tm = uniform(tmem);
-    uint32_t items = 0;
-    bool begins = true;
-    for (uint32_t s = 0; at.u < u1; ++s) {
-      const uint32_t st = s % kStages, b = s & 1, k = items & 1;
-      if (begins) wait(&B.k_full[k], items >> 1);
-      wait(&B.q_full[st], s / kStages);
-      wait(&B.lse_full[st], s / kStages);
-      if (p.stall && s + 1 == p.stall) wait(&B.never, 0);  // testing hook
-      if (!good()) break;
-      const bool ends = at.ends_item(p);
+    // Straight-line, two steps at a time, so that operands are constants from uniform registers: with
+    // the buffers as variables a step's issue took 1,300 cycles. Each wait costs about 100 even
+    // where it need not, each commit 130: so one of each for both tiles.
+    uint32_t left = steps, items = 0, in_item = 0, k_pair = k_lo;
+    for (uint32_t turn = 0; left > 0; ++turn) {
 #pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        wait(&B.s_empty[x][b], (s >> 1) + 1);
-        if (!good()) break;
+      for (uint32_t b = 0; b < 2; ++b) {
+        if (left == 0) break;
+        if (in_item == 0) {
+          in_item = at.left(p);
+          at.next_item(p);
+          wait(&B.k_full[items & 1], items >> 1);
+          k_pair = uniform(k_lo + (items & 1) * 2 * kT);
+        }
+        wait(&B.q_full[b], turn);
+        wait(&B.lse_full[b], turn);
+        wait(&B.s_empty[b], turn + 1);
+        if (p.stall && turn * 2 + b + 1 == p.stall) wait(&B.never, 0);  // testing hook
         tc_fence_after();
 #pragma unroll
-        for (int i = 0; i < D / 16; ++i) {
-          const uint32_t off = (i >> 2) * (kTile * 128 >> 4) + (i & 3) * 2;
-          mma_ss(el, tm + x * 256 + b * 128, k_lo + (2 * k + x) * kT + off, kHi, q_lo + st * kT + off,
-                 kHi, kId, i > 0);
+        for (uint32_t x = 0; x < 2; ++x) {
+#pragma unroll
+          for (int i = 0; i < D / 16; ++i) {
+            const uint32_t off = (i >> 2) * (kTile * 128 >> 4) + (i & 3) * 2;
+            mma_ss(el, tm + x * 256 + b * 128, k_pair + x * kT + off, kHi, q_lo + b * kT + off, kHi, kId,
+                   i > 0);
+          }
+          mma_ss(el, tm + x * 256 + b * 128, ones_lo, kFlat, lse_lo + b * (kTile * 32 >> 4), kFlat, kId, 1);
         }
-        mma_ss(el, tm + x * 256 + b * 128, ones_lo, kFlat, lse_lo + st * (kTile * 32 >> 4), kFlat, kId, 1);
-        mma_commit(el, &B.s_full[x][b]);
+        mma_commit(el, &B.s_full[b]);
+        if (--in_item == 0) {
+          mma_commit(el, &B.k_empty[items & 1]);
+          ++items;
+        }
+        --left;
       }
-      if (!wait.ok()) break;
-      mma_commit(el, &B.q_empty[st]);
-      if (ends) {
-        mma_commit(el, &B.k_empty[k]);
-        ++items;
-      }
-      begins = ends;
-      at.advance(p);
+      if (!good()) break;
     }
     // Nothing that this warp issued is still running when TMEM is freed.
     mma_commit(el, &B.idle);
     if (!mbar_wait(&B.idle, 0, kAttnPolls)) set_status(p.status, GDN_DEV_TIMEOUT);
-  } else if (any && warp == 10) {
+  } else if (steps > 0 && warp == 18) {
     // ---------------------------------------------------------------- the rows' denominators
     const float down = -1.0f / p.scale;
-    float v[kStages][4];
-    StepCursor ahead = at;
+    float v[2][4];  // of the next two steps
+    uint32_t fetched = 0;
     auto fetch = [&](float (&y)[4]) {
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int row = ahead.rt * kTile + i * 32 + lane;
+        const int row = at.rt * kTile + i * 32 + lane;
         y[i] = 0.f;
-        if (ahead.u < u1 && row < ahead.shape.len)
-          y[i] = p.lse[(size_t)(ahead.base + row) * p.H + ahead.hk * p.G + ahead.g];
+        if (fetched < steps && row < at.shape.len)
+          y[i] = p.lse[(size_t)(at.base + row) * p.H + at.hk * p.G + at.g];
       }
-      if (ahead.u < u1) ahead.advance(p);
+      if (fetched++ < steps) at.advance(p);
     };
+    fetch(v[0]);
+    fetch(v[1]);
+    uint32_t left = steps;
+    for (uint32_t turn = 0; left > 0; ++turn) {
 #pragma unroll
-    for (int i = 0; i < kStages; ++i) fetch(v[i]);
-    const int64_t n = u1 - at.u;
-    bool ok = true;
-    for (uint32_t s = 0; ok && s < n; s += kStages) {
-#pragma unroll
-      for (uint32_t st = 0; st < kStages; ++st) {
-        if (s + st >= n) break;
-        wait(&B.q_empty[st], s / kStages + 1);
+      for (uint32_t b = 0; b < 2; ++b) {
+        if (left == 0) break;
+        wait(&B.s_full[b], turn + 1);
         if (!good()) {
-          ok = false;
+          left = 0;
           break;
         }
+        --left;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
           const int r = i * 32 + lane;
-          const float x = v[st][i] * down;
+          const float x = v[b][i] * down;
           const float hi = __bfloat162float(__float2bfloat16_rn(x));
           const float y = isfinite(hi) ? x - hi : 0.f, mid = __bfloat162float(__float2bfloat16_rn(y));
-          *reinterpret_cast<uint4*>(smem + S::kLse + st * kTile * 32 + (r >> 3) * 256 + (r & 7) * 16) =
+          *reinterpret_cast<uint4*>(smem + S::kLse + b * kTile * 32 + (r >> 3) * 256 + (r & 7) * 16) =
               make_uint4(pack_bf16(hi, mid), pack_bf16(y - mid, 0.f), 0, 0);
         }
         fence_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive(&B.lse_full[st]);
-        fetch(v[st]);
+        if (lane == 0) mbar_arrive(&B.lse_full[b]);
+        fetch(v[b]);
       }
     }
   }
@@ -480,7 +527,7 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
-  if (warp == 9) tmem_dealloc(tmem, 512);
+  if (warp == 17) tmem_dealloc(tmem, 512);
 }
 
 // The sums of the items that span CTAs: block i those of the item that the end of CTA i's part cuts,
