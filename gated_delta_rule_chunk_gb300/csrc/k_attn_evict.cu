@@ -1,10 +1,16 @@
 // Eviction: the tokens of a sequence that stay (select_kernel), and their copies (move_kernel).
 //
 // The choice is per sequence and key head: the k = keep - recent largest weights among the first
-// len - recent tokens, of equal ones those of lower index. A CTA finds the k-th largest weight by
-// its bits, 8 at a time from the top (a histogram of the values that agree so far, then the bin in
-// which the k-th lies), and goes through the tokens once more in their order: larger ones stay,
-// and of the equal ones the first that are still wanted.
+// len - recent tokens, of equal ones those of lower index. A CTA holds the weights in registers, as
+// integers of the same order, and finds the k-th largest bit by bit from the top: a bit is set where
+// at least k values reach the number with it. A round is a comparison a value and one barrier (about
+// 150 cycles), and the rounds end early once exactly k values reach the number. A thread's values
+// are consecutive tokens, so that one scan over the threads gives the places in the result: larger
+// values stay, and of those equal to the k-th the first that are still wanted. Bound: the rounds,
+// a few microseconds; a histogram of 8 bits a pass took ten times as long, as weights share their
+// exponents and most of a warp's additions went to one counter.
+// Rows longer than the registers of a CTA hold (kThreads * 32 tokens) are read again each round, 8
+// bits a round, in select_long_kernel.
 //
 // The copies are rows of 64 to 256 bytes from anywhere to consecutive places. A warp takes 16
 // places of K or of V, all rows loaded side by side.
@@ -15,7 +21,8 @@ namespace gdn {
 
 namespace {
 
-constexpr int kSelect = 512;
+constexpr int kSelect = 1024;  // threads of a selection
+constexpr int kList = 512;      // values that one warp goes on with
 constexpr int kMoveWarps = 4;
 
 // Bits whose unsigned order is that of the numbers; NaN above all, both zeros the same.
@@ -29,25 +36,161 @@ __device__ __forceinline__ int evict_len(const AttnEvictParams& p, int n) {
   return min(max(p.kv_lens[n], 0), p.max_pages << p.page_shift);
 }
 
-__global__ void __launch_bounds__(kSelect) select_kernel(const AttnEvictParams p) {
+// What a selection does before it looks at weights: the lists of sequences that stay whole, the
+// last tokens. Returns whether there is nothing left to do.
+__device__ __forceinline__ bool easy_part(const AttnEvictParams& p, int n, int hk, int32_t* kept, int& M,
+                                          int& k) {
+  const int tid = threadIdx.x, step = blockDim.x, len = evict_len(p, n);
+  if (tid == 0 && hk == 0 && p.kv_lens[n] != len) set_status(p.status, GDN_DEV_BAD_LENGTH);
+  for (int i = min(len, p.keep) + tid; i < p.keep; i += step) kept[i] = -1;
+  if (len <= p.keep) {
+    for (int i = tid; i < len; i += step) kept[i] = i;
+    return true;
+  }
+  M = len - p.recent;
+  k = p.keep - p.recent;
+  for (int i = tid; i < p.recent; i += step) kept[k + i] = M + i;
+  return k == 0;
+}
+
+// E tokens a thread, kT threads.
+template <int E, int kT>
+__global__ void __launch_bounds__(kT) select_kernel(const AttnEvictParams p, bool wide) {
+  __shared__ uint32_t counts[2][32], list[kList], listed, found[2];
+  const int n = blockIdx.x / p.Hk, hk = blockIdx.x - n * p.Hk;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  pdl_wait();
+  pdl_release();
+  int32_t* kept = p.kept + (size_t)blockIdx.x * p.keep;
+  int M, k;
+  if (easy_part(p, n, hk, kept, M, k)) return;
+  if (tid == 0) listed = 0;
+  // This thread's tokens [i0, i0 + E); 0 stands for what is past the end (no weight's bits are 0).
+  const int i0 = tid * E;
+  uint32_t u[E];
+#pragma unroll
+  for (int c = 0; c < E; c += 8) {  // 8 tokens are in one page
+    const int i = i0 + c;
+    int page = -1;
+    if (i < M) page = p.table[(size_t)n * p.max_pages + (i >> p.page_shift)];
+    const float* w = p.weights + ((((int64_t)page * p.Hk + hk) << p.page_shift) + (i & (p.page - 1)));
+    float x[8];
+    if (page < 0 || page >= p.n_pages) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = 0.f;
+    } else if (wide) {
+      *reinterpret_cast<float4*>(x) = reinterpret_cast<const float4*>(w)[0];
+      *reinterpret_cast<float4*>(x + 4) = reinterpret_cast<const float4*>(w)[1];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = w[e];
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) u[c + e] = i + e < M ? order_bits(x[e]) : 0;
+  }
+  // Sum of a value over the CTA.
+  auto total = [&](uint32_t x, int buf) -> uint32_t {
+    x = __reduce_add_sync(0xffffffffu, x);
+    if (lane == 0) counts[buf][warp] = x;
+    __syncthreads();
+    return __reduce_add_sync(0xffffffffu, lane < kT / 32 ? counts[buf][lane] : 0);
+  };
+  // The k-th largest value lies in [top, top + 2^bit); `above` values lie above that, `reach` from
+  // top on.
+  uint32_t top = 0, above = 0, reach = M;
+  int bit = 32;
+  while (bit > 0 && reach != (uint32_t)k && reach - above > kList) {
+    const uint32_t next = top + (1u << --bit);
+    uint32_t c = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e) c += u[e] >= next;
+    c = total(c, bit & 1);
+    if (c >= (uint32_t)k) {
+      top = next;
+      reach = c;
+    } else {
+      above = c;
+    }
+  }
+  if (bit > 0 && reach != (uint32_t)k) {
+    // Few are left: one warp goes on with them, without barriers.
+    __syncthreads();
+    const uint32_t last = top + ((bit < 32 ? 1u << bit : 0u) - 1);
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (u[e] >= top && u[e] <= last && u[e] != 0) list[atomicAdd(&listed, 1u)] = u[e];
+    __syncthreads();
+    if (warp == 0) {
+      uint32_t x[kList / 32];
+#pragma unroll
+      for (int i = 0; i < kList / 32; ++i) x[i] = i * 32 + lane < (int)listed ? list[i * 32 + lane] : 0;
+      while (bit > 0 && reach != (uint32_t)k) {
+        const uint32_t next = top + (1u << --bit);
+        uint32_t c = 0;
+#pragma unroll
+        for (int i = 0; i < kList / 32; ++i) c += x[i] >= next;
+        c = above + __reduce_add_sync(0xffffffffu, c);
+        if (c >= (uint32_t)k) {
+          top = next;
+          reach = c;
+        }
+      }
+      if (lane == 0) {
+        found[0] = top;
+        found[1] = reach;
+      }
+    }
+    __syncthreads();
+    top = found[0];
+    reach = found[1];
+  }
+  const bool exact = reach == (uint32_t)k;  // k values reach it
+  // Where exactly k values reach it, all of them stay; else the larger ones and the first equal ones.
+  uint32_t more = 0, same = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    more += exact ? u[e] >= top : u[e] > top;
+    same += !exact && u[e] == top;
+  }
+  // Those of the threads before this one.
+  uint32_t m_inc = more, s_inc = same;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t a = __shfl_up_sync(0xffffffffu, m_inc, o), b = __shfl_up_sync(0xffffffffu, s_inc, o);
+    if (lane >= o) {
+      m_inc += a;
+      s_inc += b;
+    }
+  }
+  __syncthreads();
+  if (lane == 31) {
+    counts[0][warp] = m_inc;
+    counts[1][warp] = s_inc;
+  }
+  __syncthreads();
+  const uint32_t mw = lane < kT / 32 ? counts[0][lane] : 0, sw = lane < kT / 32 ? counts[1][lane] : 0;
+  const uint32_t want = k - __reduce_add_sync(0xffffffffu, mw);  // of the equal ones
+  uint32_t m_at = m_inc - more + __reduce_add_sync(0xffffffffu, lane < warp ? mw : 0);
+  uint32_t s_at = s_inc - same + __reduce_add_sync(0xffffffffu, lane < warp ? sw : 0);
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const bool is_more = exact ? u[e] >= top : u[e] > top, is_same = !exact && u[e] == top;
+    if (is_more || (is_same && s_at < want)) kept[m_at + min(s_at, want)] = i0 + e;
+    m_at += is_more;
+    s_at += is_same;
+  }
+}
+
+__global__ void __launch_bounds__(kSelect) select_long_kernel(const AttnEvictParams p) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t found[2];
   __shared__ uint32_t sums[2][kSelect / 32];
   const int n = blockIdx.x / p.Hk, hk = blockIdx.x - n * p.Hk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
-  const int len = evict_len(p, n);
-  if (tid == 0 && hk == 0 && p.kv_lens[n] != len) set_status(p.status, GDN_DEV_BAD_LENGTH);
   int32_t* kept = p.kept + (size_t)blockIdx.x * p.keep;
-  const int stay = min(len, p.keep);
-  for (int i = stay + tid; i < p.keep; i += kSelect) kept[i] = -1;
-  if (len <= p.keep) {
-    for (int i = tid; i < len; i += kSelect) kept[i] = i;
-    return;
-  }
-  const int M = len - p.recent, k = p.keep - p.recent;
-  for (int i = tid; i < p.recent; i += kSelect) kept[k + i] = M + i;
-  if (k == 0) return;
+  int M, k;
+  if (easy_part(p, n, hk, kept, M, k)) return;
   auto bits = [&](int i) -> uint32_t {
     const int page = p.table[(size_t)n * p.max_pages + (i >> p.page_shift)];
     if (page < 0 || page >= p.n_pages) return order_bits(0.f);
@@ -104,8 +247,6 @@ __global__ void __launch_bounds__(kSelect) select_kernel(const AttnEvictParams p
     __syncthreads();
   }
 }
-
-// `out` above counts the larger ones only; the equal ones that stay come in by s_taken.
 
 template <int kRow, bool k8>
 __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const AttnEvictParams p) {
@@ -188,8 +329,18 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const AttnEvictPa
 }  // namespace
 
 bool launch_attn_evict(const AttnEvictParams& p, cudaStream_t s) {
-  if (launch_pdl(select_kernel, dim3((unsigned)(p.N * p.Hk)), dim3(kSelect), 0, s, p) != cudaSuccess)
-    return false;
+  // The smallest form that the table's rows fit: registers are read once, and more CTAs fit an SM.
+  const dim3 rows((unsigned)(p.N * p.Hk));
+  const int64_t most = (int64_t)p.max_pages * p.page;
+  const bool wide = ((uintptr_t)p.weights & 15) == 0;
+  const cudaError_t e =
+      most <= 2048    ? launch_pdl(select_kernel<8, 256>, rows, dim3(256), 0, s, p, wide)
+      : most <= 4096  ? launch_pdl(select_kernel<8, 512>, rows, dim3(512), 0, s, p, wide)
+      : most <= 8192  ? launch_pdl(select_kernel<8, 1024>, rows, dim3(1024), 0, s, p, wide)
+      : most <= 16384 ? launch_pdl(select_kernel<16, 1024>, rows, dim3(1024), 0, s, p, wide)
+      : most <= 32768 ? launch_pdl(select_kernel<32, 1024>, rows, dim3(1024), 0, s, p, wide)
+                      : launch_pdl(select_long_kernel, rows, dim3(kSelect), 0, s, p);
+  if (e != cudaSuccess) return false;
   const int64_t items = (int64_t)p.N * p.Hk * ((p.keep + kBlock8 - 1) / kBlock8) * 2;
   const dim3 grid((unsigned)((items + kMoveWarps - 1) / kMoveWarps)), block(kMoveWarps * 32);
   const auto kernel = p.ks ? (p.D == 128 ? move_kernel<128, true> : move_kernel<64, true>)

@@ -690,6 +690,13 @@ def test_evict_many_and_long(bits):
     run_evict([9000, 5, 4097], 2, 64, 64, 1000, 100, bits)
 
 
+@pytest.mark.parametrize("longest", [2048, 4096, 8192, 16384, 32768, 40000])
+def test_evict_row_lengths(longest):
+    """Each size of the selection, full and nearly empty; weights of many equal values."""
+    run_evict([longest, 9, longest - 1, longest // 2 + 3], 1, 64, 256, longest // 3, 17, seed=longest)
+    run_evict([longest - 5], 2, 64, 16, 50, 0, 8, change=lambda w: (w * 3).round())
+
+
 @pytest.mark.parametrize("what", ["equal", "zeros", "negative", "nan", "inf", "close", "denormal"])
 def test_evict_choices(what):
     def change(w):
