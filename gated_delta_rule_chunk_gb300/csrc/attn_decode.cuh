@@ -318,17 +318,44 @@ combine_kernel(const AttnParams p, const DecodeParts w) {
 }
 
 // The weight that each key gets: 2^(score - lse2) over the R rows of its pair, from the scores
-// that decode_kernel left (a few bytes a key beside its K and V). Each warp takes an equal part
-// of the units, two keys a lane.
+// that the decode kernel left (a few bytes a key beside its K and V). Each warp takes an equal part
+// of the list of 64-key pieces, two keys a lane. Bound: latency, a chain of lookups (unit numbers,
+// page, scores, denominators, weights) for a few pieces a warp; so the next piece's loads are issued
+// before this one's are used.
+constexpr int kRowsAtOnce = 8;  // loaded side by side
 template <int kUnit>
-__global__ void __launch_bounds__(256) weights_kernel(const AttnParams p, const DecodeParts w) {
+__global__ void __launch_bounds__(256, 3) weights_kernel(const AttnParams p, const DecodeParts w) {
+  constexpr int kPieces = kUnit / 64;
   const int lane = threadIdx.x & 31, R = p.nq * p.G;
   pdl_wait();
-  const int U = w.first[p.N], W = gridDim.x * 8, me = blockIdx.x * 8 + (threadIdx.x >> 5);
-  int u = (int)((int64_t)me * U / W);
-  const int u1 = (int)((int64_t)(me + 1) * U / W);
-  int n = -1, at = 0, end = 0, c = 0, len = 0;  // the sequence of unit u and its units [at, end)
-  for (; u < u1; ++u) {
+  const int64_t U = (int64_t)w.first[p.N] * kPieces, W = (int64_t)gridDim.x * 8;
+  const int64_t me = blockIdx.x * 8 + (threadIdx.x >> 5);
+  const int64_t z0 = me * U / W, z1 = (me + 1) * U / W;
+  int n = -1, at = 0, end = 0, c = 1, len = 0;  // the sequence of the last piece looked up, its units [at, end)
+  struct Piece {
+    const float *x, *lse;  // this lane's first score, the pair's first row's denominator
+    int n, hk, key, len, page;
+    bool live;
+    float2 y[kRowsAtOnce];
+    float l[kRowsAtOnce];
+  };
+  auto rows = [&](Piece& a, int r0, int& i, int& g) {
+#pragma unroll
+    for (int r = 0; r < kRowsAtOnce; ++r) {
+      a.y[r] = make_float2(-INFINITY, -INFINITY);
+      a.l[r] = 0.f;
+      if (a.live && r0 + r < R) {
+        a.y[r] = __ldcs(reinterpret_cast<const float2*>(a.x + (size_t)(r0 + r) * w.keys));
+        a.l[r] = a.lse[(size_t)i * p.H + g];
+        if (++g == p.G) {
+          g = 0;
+          ++i;
+        }
+      }
+    }
+  };
+  auto begin = [&](Piece& a, int64_t z) {
+    const int u = (int)(z / kPieces);
     if (u >= end) {
       for (int n0 = n + 1; n0 < p.N; n0 += 32) {  // the first sequence that ends after u
         const uint32_t hit = __ballot_sync(0xffffffffu, n0 + lane < p.N && w.first[n0 + lane + 1] > u);
@@ -343,32 +370,50 @@ __global__ void __launch_bounds__(256) weights_kernel(const AttnParams p, const 
       len = seq_len(p, n);
     }
     const int hk = (u - at) / c, chunk = (u - at) - hk * c - kPair<kUnit>;
+    a.n = n;
+    a.hk = hk;
+    a.len = len;
+    a.key = chunk * kUnit + (int)(z % kPieces) * 64 + 2 * lane;
+    a.live = chunk >= 0 && a.key < len;
+    a.page = -1;
+    if (a.live) a.page = p.table[(size_t)n * p.max_pages + (a.key >> p.page_shift)];
+    a.x = w.scores + (size_t)(n * p.Hk + hk) * R * w.keys + a.key;
+    a.lse = w.lse2 + (size_t)n * p.nq * p.H + hk * p.G;
+    int i = 0, g = 0;
+    rows(a, 0, i, g);
+  };
+  auto finish = [&](Piece& a) {
+    float2 sum = make_float2(0.f, 0.f);
+    int i = kRowsAtOnce / p.G, g = kRowsAtOnce % p.G;  // of the rows not yet loaded
+    for (int r0 = 0; r0 < R; r0 += kRowsAtOnce) {
+      if (r0 > 0) rows(a, r0, i, g);
 #pragma unroll
-    for (int key = chunk * kUnit + 2 * lane, z = 0; z < kUnit / 64; ++z, key += 64) {
-      if (chunk < 0 || key >= len) continue;
-      const int page = p.table[(size_t)n * p.max_pages + (key >> p.page_shift)];
-      const float* x = w.scores + (size_t)(n * p.Hk + hk) * R * w.keys + key;
-      const float* lse = w.lse2 + (size_t)n * p.nq * p.H + hk * p.G;
-      float2 sum = make_float2(0.f, 0.f);
-      int r = 0;
-      for (int i = 0; i < p.nq; ++i)
-        for (int g = 0; g < p.G; ++g, ++r) {
-          const float2 y = *reinterpret_cast<const float2*>(x + (size_t)r * w.keys);
-          const float l = lse[(size_t)i * p.H + g];
-          // (a row that sees no key: -inf - -inf)
-          sum.x += y.x == -INFINITY ? 0.f : ex2(y.x - l);
-          sum.y += y.y == -INFINITY ? 0.f : ex2(y.y - l);
-        }
-      if (page < 0 || page >= p.n_pages) continue;
-      float* to = p.weights + ((((size_t)page * p.Hk + hk) << p.page_shift) + (key & (p.page - 1)));
-      const int fresh = len - p.nq;  // from here on keys are the call's own
-      if (key >= fresh) to[0] = sum.x;
-      else atomicAdd(to, sum.x);
-      if (key + 1 < len) {
-        if (key + 1 >= fresh) to[1] = sum.y;
-        else atomicAdd(to + 1, sum.y);
+      for (int r = 0; r < kRowsAtOnce; ++r) {
+        // (a row that sees no key: -inf - -inf)
+        sum.x += a.y[r].x == -INFINITY ? 0.f : ex2(a.y[r].x - a.l[r]);
+        sum.y += a.y[r].y == -INFINITY ? 0.f : ex2(a.y[r].y - a.l[r]);
       }
     }
+    if (a.page < 0 || a.page >= p.n_pages) return;
+    float* to = p.weights + ((((size_t)a.page * p.Hk + a.hk) << p.page_shift) + (a.key & (p.page - 1)));
+    const int fresh = a.len - p.nq;  // from here on keys are the call's own
+    if (a.key >= fresh) to[0] = sum.x;
+    else atomicAdd(to, sum.x);
+    if (a.key + 1 < a.len) {
+      if (a.key + 1 >= fresh) to[1] = sum.y;
+      else atomicAdd(to + 1, sum.y);
+    }
+  };
+  if (z0 >= z1) return;
+  Piece a, b;
+  begin(a, z0);
+  for (int64_t z = z0;;) {
+    if (z + 1 < z1) begin(b, z + 1);
+    finish(a);
+    if (++z >= z1) break;
+    if (z + 1 < z1) begin(a, z + 1);
+    finish(b);
+    if (++z >= z1) break;
   }
 }
 
@@ -420,7 +465,7 @@ bool launch_rest(const AttnParams& p, const DecodeParts& w, cudaStream_t s) {
                  s, p, w) != cudaSuccess)
     return false;
   if (!kScores) return true;
-  return launch_pdl(weights_kernel<kUnit>, dim3(2 * num_sms()), dim3(256), 0, s, p, w) == cudaSuccess;
+  return launch_pdl(weights_kernel<kUnit>, dim3(3 * num_sms()), dim3(256), 0, s, p, w) == cudaSuccess;
 }
 
 // Where the parts are in the workspace.
