@@ -9,12 +9,15 @@
 
 namespace gdn {
 
-// Two elements (low byte first), rounded to nearest even; infinities and NaN become NaN. The
-// scale keeps finite values within 448.
+// Two finite elements of at most 448 in size (low byte first), rounded to nearest even.
+__device__ __forceinline__ uint32_t finite_to_e4m3x2(float a, float b) {
+  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+}
+// The same for any elements: infinities and NaN become NaN.
 __device__ __forceinline__ uint32_t to_e4m3x2(float a, float b) {
   a = fabsf(a) <= 3.402823466e38f ? a : NAN;
   b = fabsf(b) <= 3.402823466e38f ? b : NAN;
-  return __nv_cvt_float2_to_fp8x2(make_float2(a, b), __NV_SATFINITE, __NV_E4M3);
+  return finite_to_e4m3x2(a, b);
 }
 
 // Four bytes as two pairs of fp16 values (exact). (Through cuda_fp8.h's types the halves of a

@@ -9,10 +9,13 @@
 // become subnormal.
 //
 // A warp takes one (block, key head, k or v): all of its rows (4 KB in bf16 at D = 128) are loaded
-// side by side, their maximum is a few shuffles away, and the rounded rows are stored from the
-// registers; a block that holds earlier tokens reads its scale meanwhile, and those tokens' rows
-// only where the scale grows. A warp finds its block from the rows of the call: the first row of
-// each block stands for it.
+// side by side and kept as they are (32 registers a lane), their maximum is a few shuffles away,
+// and the rounded rows are stored from the registers; a block that holds earlier tokens reads its
+// scale meanwhile, and those tokens' rows only where the scale grows. The first row of each block
+// stands for it: a warp looks through `span` consecutive rows of the call for such rows, 16 for
+// prompts, where that is one or two blocks, and one for steps. Bound: the loads that depend on one
+// another (cu_seqlens, kv_lens, then the rows and the page), so the search for a sequence looks at
+// 32 entries at a time.
 #include "attn_common.cuh"
 #include "e4m3.cuh"
 
@@ -23,8 +26,61 @@ namespace {
 constexpr int kWarps = 4;
 constexpr uint32_t kLargest = 0x7F7FFFFFu;  // bits of the largest finite number
 
+// Sequence n of row t and its rows [b, e); n = -1 outside every sequence. By a whole warp.
+__device__ __forceinline__ int warp_find_seq(const AttnAppend8Params& p, int t, int& b, int& e) {
+  if (!p.cu) {
+    b = 0;
+    e = p.T;
+    return 0;
+  }
+  const int lane = threadIdx.x & 31;
+  // In a step the sequence is the row's number; looked at beside the first part of the search.
+  const int guess = min(t, p.N - 1);
+  const int gb = p.cu[guess], ge = p.cu[guess + 1];
+  int lo = 0, count = p.N + 1;  // the last entry <= t is one of [lo, lo + count)
+  while (true) {
+    const int step = (count + 31) / 32, at = lo + min(lane * step, count - 1);
+    const uint32_t below = __ballot_sync(0xffffffffu, lane * step < count && p.cu[at] <= t);
+    if (gb <= t && t < ge) {
+      b = gb;
+      e = ge;
+      return guess;
+    }
+    if (below == 0) return -1;
+    const int j = 31 - __clz(below);
+    lo += j * step;
+    count = min(step, count - j * step);
+    if (count == 1) break;
+  }
+  if (lo >= p.N) return -1;
+  b = p.cu[lo];
+  e = p.cu[lo + 1];
+  return b <= t && t < e && b >= 0 && e <= p.T ? lo : -1;
+}
+
+// 8 elements of a row as they were loaded.
+template <bool kBf16>
+struct Run {
+  uint32_t w[kBf16 ? 4 : 8];
+  __device__ __forceinline__ void load(const void* x, size_t at) {
+    const uint4* v = reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at * (kBf16 ? 2 : 4));
+    *reinterpret_cast<uint4*>(w) = __ldcs(v);
+    if constexpr (!kBf16) *reinterpret_cast<uint4*>(w + 4) = __ldcs(v + 1);
+  }
+  __device__ __forceinline__ void zero() {
+#pragma unroll
+    for (uint32_t& x : w) x = 0;
+  }
+  // bits of element i in 32 bits
+  __device__ __forceinline__ uint32_t bits(int i) const {
+    if constexpr (kBf16) return i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16;
+    else return w[i];
+  }
+};
+
 template <int D, bool kBf16>
-__global__ void __launch_bounds__(kWarps * 32) append8_kernel(const AttnAppend8Params p) {
+__global__ void __launch_bounds__(kWarps * 32, kBf16 ? 7 : 5)
+append8_kernel(const AttnAppend8Params p) {
   constexpr int L = D / 8, kAtOnce = 32 / L, kPasses = kBlock8 / kAtOnce;
   const uint32_t item = blockIdx.x * kWarps + (threadIdx.x >> 5);
   const int lane = threadIdx.x & 31;
@@ -38,54 +94,44 @@ __global__ void __launch_bounds__(kWarps * 32) append8_kernel(const AttnAppend8P
         set_status(p.status, GDN_DEV_BAD_CU_SEQLENS);
   if ((uint64_t)group * p.span >= (uint64_t)p.T) return;
 
-  // The rows of this group that are the first of a block, one lane a row.
-  const int t = (int)(group * p.span) + lane;
-  int n = -1, b = 0, e = 0;
-  int64_t pos = 0;
-  if (lane < p.span && t < p.T) n = find_seq(p.cu, p.N, p.T, t, b, e);
-  if (n >= 0) pos = p.kv_lens ? (int64_t)p.kv_lens[n] - (e - t) : t - b;
-  uint32_t firsts = __ballot_sync(0xffffffffu, n >= 0 && (t == b || (pos & (kBlock8 - 1)) == 0));
-
   const void* x = is_v ? p.v : p.k;
   uint8_t* cache = is_v ? p.vc : p.kc;
   float* scales = is_v ? p.vs : p.ks;
   const int r0 = lane / L, col = (lane % L) * 8;
-  while (firsts) {
-    const int src = __ffs(firsts) - 1;
-    firsts &= firsts - 1;
-    const int t0 = __shfl_sync(0xffffffffu, t, src), n0 = __shfl_sync(0xffffffffu, n, src);
-    const int b0 = __shfl_sync(0xffffffffu, b, src), e0 = __shfl_sync(0xffffffffu, e, src);
-    const int64_t at = __shfl_sync(0xffffffffu, pos, src);
+  int t = (int)(group * p.span), b = 0, e = 0;
+  const int t_end = min(t + p.span, p.T);
+  // The group's rows are on their way while its sequence and place are looked up, a line a lane.
+  constexpr int kLine = 128 / (kBf16 ? 2 : 4), kLines = D / kLine;  // of a row
+  for (int i = lane; i < (t_end - t) * kLines; i += 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(static_cast<const char*>(x) +
+        (((size_t)(t + i / kLines) * p.Hk + hk) * D + i % kLines * kLine) * (kBf16 ? 2 : 4)));
+  int n = warp_find_seq(p, t, b, e);
+  while (t < t_end) {
+    if (n < 0 || t >= e) {
+      if (n < 0) {  // (only with cu) before the first sequence, or behind the last
+        if (t >= p.cu[p.N]) return;
+        t = max(t + 1, min(p.cu[0], t_end));
+      }
+      if (t < t_end) n = warp_find_seq(p, t, b, e);
+      continue;
+    }
+    const int64_t at = p.kv_lens ? (int64_t)p.kv_lens[n] - (e - t) : t - b;
+    const int in_block = (int)(at & (kBlock8 - 1));
+    const int rows = min(kBlock8 - in_block, e - t), t0 = t;
+    t += rows;
+    if (t0 != b && in_block != 0) continue;  // another warp's block
     if (at < 0 || (at >> p.page_shift) >= p.max_pages) {
       if (lane == 0) set_status(p.status, GDN_DEV_BAD_LENGTH);
       continue;
     }
-    const int in_block = (int)(at & (kBlock8 - 1));
-    const int rows = min(kBlock8 - in_block, e0 - t0);
-    const int held = t0 == b0 ? in_block : 0;
-    const int page = p.table[(size_t)n0 * p.max_pages + (at >> p.page_shift)];
-
-    float y[kPasses][8];
+    const int held = in_block;  // earlier tokens in the block
+    const int page = p.table[(size_t)n * p.max_pages + (at >> p.page_shift)];
+    Run<kBf16> y[kPasses];
 #pragma unroll
     for (int i = 0; i < kPasses; ++i) {
       const int r = i * kAtOnce + r0;
-#pragma unroll
-      for (int j = 0; j < 8; ++j) y[i][j] = 0.f;
-      if (r >= rows) continue;
-      const size_t from = ((size_t)(t0 + r) * p.Hk + hk) * D + col;
-      if constexpr (kBf16) {
-        const uint4 w = *reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(x) + from);
-        const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[i][2 * j] = __uint_as_float(u[j] << 16);
-          y[i][2 * j + 1] = __uint_as_float(u[j] & 0xFFFF0000u);
-        }
-      } else {
-        const float4* w = reinterpret_cast<const float4*>(static_cast<const float*>(x) + from);
-        *reinterpret_cast<float4*>(y[i]) = w[0];
-        *reinterpret_cast<float4*>(y[i] + 4) = w[1];
-      }
+      if (r < rows) y[i].load(x, ((size_t)(t0 + r) * p.Hk + hk) * D + col);
+      else y[i].zero();
     }
     if (page < 0 || page >= p.n_pages) {
       if (lane == 0) set_status(p.status, GDN_DEV_BAD_PAGE_TABLE);
@@ -95,15 +141,38 @@ __global__ void __launch_bounds__(kWarps * 32) append8_kernel(const AttnAppend8P
     const size_t block = row / kBlock8;
     float old = 0.f;
     if (held) old = scales[block];
-    uint32_t top = 0;  // the largest finite |x|; its bits are in the order of the values
+    uint32_t top = 0;  // the largest |x|; its bits are in the order of the values
+    if constexpr (kBf16) {
+      uint32_t two = 0;  // of even and odd elements
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i)
+      for (int i = 0; i < kPasses; ++i)
 #pragma unroll
-      for (int j = 0; j < 8; ++j) {
-        const uint32_t a = __float_as_uint(y[i][j]) & 0x7FFFFFFFu;
-        top = max(top, a <= kLargest ? a : 0u);
-      }
+        for (int j = 0; j < 4; ++j) two = __vmaxu2(two, y[i].w[j] & 0x7FFF7FFFu);
+      top = max(two << 16, two & 0xFFFF0000u);
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPasses; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, y[i].w[j] & 0x7FFFFFFFu);
+    }
     top = __reduce_max_sync(0xffffffffu, top);
+    // What is seldom (infinities, NaN, a scale that is no power of two) goes through the rows once
+    // more, from memory, so that the code for it stays small.
+    const bool finite = top <= kLargest;
+    if (!finite) {
+      top = 0;  // of the finite ones
+#pragma unroll 1
+      for (int r = r0; r < rows; r += kAtOnce) {
+        Run<kBf16> z;
+        z.load(x, ((size_t)(t0 + r) * p.Hk + hk) * D + col);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const uint32_t a = z.bits(j) & 0x7FFFFFFFu;
+          top = max(top, a <= kLargest ? a : 0u);
+        }
+      }
+      top = __reduce_max_sync(0xffffffffu, top);
+    }
     // 448 = 1.75 * 2^8
     const int ex = max((int)(top >> 23) - 127 - 8 + ((top & 0x7FFFFFu) > 0x600000u), -100);
     const float need = __uint_as_float((uint32_t)(ex + 127) << 23);
@@ -111,17 +180,29 @@ __global__ void __launch_bounds__(kWarps * 32) append8_kernel(const AttnAppend8P
     const bool power = (__float_as_uint(s) & 0x7FFFFFu) == 0;
     const float inv = 1.0f / s;  // exact for a power of two
     uint8_t* dst = cache + row * D + col;
+    if (finite && power) {
 #pragma unroll
-    for (int i = 0; i < kPasses; ++i) {
-      const int r = i * kAtOnce + r0;
-      if (r >= rows) continue;
-      uint32_t z[4];
+      for (int i = 0; i < kPasses; ++i) {
+        const int r = i * kAtOnce + r0;
+        uint32_t z[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = y[i][2 * j], c = y[i][2 * j + 1];
-        z[j] = power ? to_e4m3x2(a * inv, c * inv) : to_e4m3x2(a / s, c / s);
+        for (int j = 0; j < 4; ++j)
+          z[j] = finite_to_e4m3x2(__uint_as_float(y[i].bits(2 * j)) * inv,
+                                  __uint_as_float(y[i].bits(2 * j + 1)) * inv);
+        if (r < rows)
+          *reinterpret_cast<uint2*>(dst + (size_t)r * D) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
       }
-      *reinterpret_cast<uint2*>(dst + (size_t)r * D) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+    } else {
+#pragma unroll 1
+      for (int r = r0; r < rows; r += kAtOnce) {
+        Run<kBf16> v;
+        v.load(x, ((size_t)(t0 + r) * p.Hk + hk) * D + col);
+        uint32_t z[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          z[j] = to_e4m3x2(__uint_as_float(v.bits(2 * j)) / s, __uint_as_float(v.bits(2 * j + 1)) / s);
+        *reinterpret_cast<uint2*>(dst + (size_t)r * D) = make_uint2(z[0] | z[1] << 16, z[2] | z[3] << 16);
+      }
     }
     if (s != old || !held) {
       if (lane == 0) scales[block] = s;
