@@ -136,69 +136,77 @@ __device__ __forceinline__ bool find_units(const AttnParams& p, const DecodePart
 }
 
 // The end of a pair's part: its key groups' results merged in shared memory and finished, or handed
-// over in place `place`. stats() writes the reference and denominator of the warp's rows to ml
-// [WK][16 WM]; put(buf, q, m) writes columns 32 q .. 32 q + 31 of their sums, against the references
-// m of all groups (m(row)), to buf [WK][16 WM][32], the 8-column pieces swapped by row (piece e at
-// e ^ (row & 3)), so that a warp's eight rows do not share banks. merge: kBufs such buffers.
+// over in place `place`. A warp has TM rows. stats() writes the reference and denominator of the
+// warp's rows to ml [WK][TM WM]; put(buf, q, m) writes columns kCols q .. kCols (q + 1) - 1 of their sums,
+// against the references m of all groups (m(row)), to buf [WK][TM WM][kCols], the 8-column pieces of 32
+// columns swapped by row (piece e at e ^ (row & 3)), so that a warp's eight rows do not share banks.
+// merge: kBufs such buffers.
 constexpr int kMergeBytes = kWarps * 16 * 32 * 4;
-template <int D, int WM, bool kScores, int kBufs, typename Stats, typename Put>
+template <int D, int WM, int TM, int kCols, bool kScores, int kBufs, typename Stats, typename Put>
 __device__ __forceinline__ void finish_part(const AttnParams& p, const DecodeParts& w, float* merge,
                                             float2* ml, Stats stats, Put put, int n, int hk,
                                             bool whole, int place) {
-  constexpr int WK = kWarps / WM;
+  constexpr int WK = kWarps / WM, kQuads = kCols / 4;  // threads of a row
+  constexpr int kTurns = TM * WM * kQuads / (kWarps * 32);
   const int tid = threadIdx.x, R = p.nq * p.G;
   stats();
   __syncthreads();
   auto most = [&](int row) {
     float m = -INFINITY;
 #pragma unroll
-    for (int k = 0; k < WK; ++k) m = fmaxf(m, ml[k * 16 * WM + row].x);
+    for (int k = 0; k < WK; ++k) m = fmaxf(m, ml[k * TM * WM + row].x);
     return m;
   };
-  // 32 columns at a time through the buffers, one barrier a round: a buffer is written again two
-  // rounds later, past a barrier that its readers have reached (one buffer: past one of its own).
+  // This thread's rows: z * 128 / kQuads + tid / kQuads.
+  float m[kTurns], d[kTurns];
 #pragma unroll
-  for (int q = 0; q < D / 32; ++q) {
-    float* buf = merge + (kBufs == 2 ? q & 1 : 0) * (kWarps * 16 * 32);
+  for (int z = 0; z < kTurns; ++z) {
+    const int r = (z * kWarps * 32 + tid) / kQuads;
+    m[z] = most(r);
+    d[z] = 0.f;
+#pragma unroll
+    for (int k = 0; k < WK; ++k) {
+      const float2 y = ml[k * TM * WM + r];
+      d[z] += m[z] == -INFINITY ? y.y : y.y * ex2(y.x - m[z]);
+    }
+  }
+  // The buffers in turn, one barrier a round: a buffer is written again two rounds later, past a
+  // barrier that its readers have reached (one buffer: past one of its own).
+#pragma unroll
+  for (int q = 0; q < D / kCols; ++q) {
+    float* buf = merge + (kBufs == 2 ? q & 1 : 0) * (WK * TM * WM * kCols);
     if (kBufs == 1 && q > 0) __syncthreads();
     put(buf, q, most);
     __syncthreads();
 #pragma unroll
-    for (int z = 0; z < WM; ++z) {
-      const int x = z * 128 + tid, r = x >> 3, col = (x & 7) * 4;
+    for (int z = 0; z < kTurns; ++z) {
+      const int r = (z * kWarps * 32 + tid) / kQuads, col = tid % kQuads * 4;
+      if (r >= R) continue;
       float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-      float m = -INFINITY, d = 0.f;
 #pragma unroll
       for (int k = 0; k < WK; ++k) {
-        const float4 y = *reinterpret_cast<const float4*>(buf + (k * 16 * WM + r) * 32 +
+        const float4 y = *reinterpret_cast<const float4*>(buf + (k * TM * WM + r) * kCols +
                                                             (col ^ ((r & 3) * 8)));
         acc.x += y.x; acc.y += y.y; acc.z += y.z; acc.w += y.w;
-        m = fmaxf(m, ml[k * 16 * WM + r].x);
       }
-#pragma unroll
-      for (int k = 0; k < WK; ++k) {
-        const float2 y = ml[k * 16 * WM + r];
-        d += m == -INFINITY ? y.y : y.y * ex2(y.x - m);
-      }
-      if (r >= R) continue;
       if (whole && p.shared == 0) {
-        const float inv = d == 0.f ? 0.f : 1.f / d;
+        const float inv = d[z] == 0.f ? 0.f : 1.f / d[z];
         const size_t at = (size_t)(n * p.nq + r / p.G) * p.H + hk * p.G + r % p.G;
         if (p.out_bf16)
-          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D + q * 32 + col) =
+          *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.out) + at * D + q * kCols + col) =
               make_uint2(pack_bf16(acc.x * inv, acc.y * inv), pack_bf16(acc.z * inv, acc.w * inv));
         else
-          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D + q * 32 + col) =
+          *reinterpret_cast<float4*>(static_cast<float*>(p.out) + at * D + q * kCols + col) =
               make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if ((p.lse || kScores) && q == 0 && col == 0) {
-          const float lse2 = d == 0.f ? -INFINITY : m + log2f(d);
+          const float lse2 = d[z] == 0.f ? -INFINITY : m[z] + log2f(d[z]);
           if (p.lse) p.lse[at] = lse2 * 0.69314718055994530942f;
           if (kScores) w.lse2[at] = lse2;
         }
       } else {
         const size_t at = (size_t)(whole ? n * p.Hk + hk : place) * R + r;
-        *reinterpret_cast<float4*>((whole ? w.own : w.part) + at * D + q * 32 + col) = acc;
-        if (q == 0 && col == 0) (whole ? w.own_ml : w.part_ml)[at] = make_float2(m, d);
+        *reinterpret_cast<float4*>((whole ? w.own : w.part) + at * D + q * kCols + col) = acc;
+        if (q == 0 && col == 0) (whole ? w.own_ml : w.part_ml)[at] = make_float2(m[z], d[z]);
       }
     }
   }

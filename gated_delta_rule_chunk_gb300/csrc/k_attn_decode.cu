@@ -270,7 +270,7 @@ decode_kernel(const AttnParams p, const DecodeParts w) {
     const bool whole = seg_chunk == cur.kOwn && was.chunk == was.chunks - 1;
     float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
     float f[2];
-    finish_part<D, WM, kScores, 2>(
+    finish_part<D, WM, 16, 32, kScores, 2>(
         p, w, reinterpret_cast<float*>(smem + S::kMerge), ml,
         [&] {
 #pragma unroll

@@ -34,7 +34,7 @@ constexpr int kBlk = 32;    // keys of a warp's block
 constexpr int kUnit = kWarps * kBlk;
 constexpr float kApart = 40.f;  // how far the denominators' reference may fall behind
 
-template <int D>
+template <int D, int RN>
 struct Smem8 {
   static constexpr int kHalf = kBlk * D;     // a K or V block
   static constexpr int kStage = 2 * kHalf;
@@ -42,7 +42,7 @@ struct Smem8 {
   static constexpr int kScales = kWarps * kStages * kStage;                // float4 a stage
   static constexpr int kMerge = kScales + kWarps * kStages * 16;
   static constexpr int kMl = kMerge + kMergeBytes;
-  static constexpr int kBars = kMl + kWarps * 16 * 8;
+  static constexpr int kBars = kMl + kWarps * RN * 8 * 8;
   static constexpr int kBytes = kBars + (kWarps * kStages + 1) * 8 + 1024;  // + alignment
 };
 
@@ -80,8 +80,8 @@ template <int D, int RN, int WM, bool kScores>
 __global__ void __launch_bounds__(kWarps * 32, kDecode8Ctas)
 decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v) {
-  using S = Smem8<D>;
-  constexpr int kSt = S::kStages, E = D / 16;
+  using S = Smem8<D, RN>;
+  constexpr int kSt = S::kStages, E = D / 16, TM = 8 * RN;
   extern __shared__ char raw_smem[];
   char* smem = raw_smem + (-smem_u32(raw_smem) & 1023u);
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -160,8 +160,8 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
 
   const float c = p.scale * 1.44269504088896340736f;
   const int g = lane >> 2, cq = (lane & 3) * 2;
-  const int row0 = mt * 16 + cq;  // this thread's rows in the sums: row0 + 8 n + x
-  uint32_t qf[RN][E][2];          // row mt * 16 + 8 n + g
+  const int row0 = mt * TM + cq;  // this thread's rows in the sums: row0 + 8 n + x
+  uint32_t qf[RN][E][2];          // row mt * TM + 8 n + g
   float qc[RN][2];                // what a row's products are multiplied with
   float o[RN][E][4];              // columns 16 e + 2 g + (i >> 1), row x = i & 1
   float refv[RN][2], ref[RN][2], l[RN][2];  // ref and l: of this thread's keys alone
@@ -177,7 +177,7 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
   auto load_q = [&] {
 #pragma unroll
     for (int n = 0; n < RN; ++n) {
-      const int r = mt * 16 + 8 * n + g;
+      const int r = mt * TM + 8 * n + g;
       const __nv_bfloat16* q =
           p.q + ((size_t)(cur.n * p.nq + r / p.G) * p.H + cur.hk * p.G + r % p.G) * D + 2 * cq;
       uint32_t top = 0;
@@ -341,18 +341,26 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
           pf[n][h][1] = transpose_8x8(pack_f16(y[2], y[3]));
         }
       }
-      bool bad = false;  // a value that a weight of 0 would not remove
+      // A value that a weight of 0 would not remove: in any key of the halves that are used (the
+      // second one may not have been loaded), and in one that some row sees.
+      const int halves = key0 + kBlock8 < cur.len ? 2 : 1;
+      bool bad = false, seen = false;
       if (part) {
-        for (int i = lane; i < S::kHalf / 16; i += 32) {
+#pragma unroll 4
+        for (int i = lane; i < halves * (S::kHalf / 32); i += 32) {
           const uint4 x = *reinterpret_cast<const uint4*>(smem + (vb - smem_u32(smem)) + i * 16);
-          bad |= (nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w)) != 0;
+          const bool nan = (nan_bytes(x.x) | nan_bytes(x.y) | nan_bytes(x.z) | nan_bytes(x.w)) != 0;
+          bad |= nan;
+          seen |= nan && key0 + i / (D / 16) < cur.len;
         }
         bad = __any_sync(0xffffffffu, bad);
+        seen = __any_sync(0xffffffffu, seen);
       }
       // Pairs of elements of 8 keys come transposed as one matrix: the even elements are the
       // operand's first 8 rows, the odd ones its last 8.
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int h = 0; h < 2; ++h) {
+        if (h >= halves) break;
 #pragma unroll
         for (int e = 0; e < E; e += 2) {
           uint32_t f[4];
@@ -371,9 +379,10 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
             for (int n = 0; n < RN; ++n) mma_f16(o[n][e + z], a, pf[n][h][0], pf[n][h][1]);
           }
         }
-      if (bad) {  // NaN to the rows that see it, whatever its weight
+      }
+      if (seen) {  // NaN to the rows that see it, whatever its weight
 #pragma unroll 1
-        for (int j = 0; j < kBlk; ++j) {
+        for (int j = 0; j < kBlk && key0 + j < cur.len; ++j) {
 #pragma unroll
           for (int e = 0; e < E; ++e) {
             const uint32_t nan = nan_bytes(*reinterpret_cast<const uint16_t*>(
@@ -399,24 +408,22 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
     if (cur.u < u1) load_q();  // the next pair's queries arrive meanwhile
     const bool whole = seg_chunk == cur.kOwn && was.chunk == was.chunks - 1;
     float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
-    finish_part<D, WM, kScores, 1>(
+    constexpr int kCols = RN == 1 ? 64 : 32;
+    finish_part<D, WM, TM, kCols, kScores, 1>(
         p, w, reinterpret_cast<float*>(smem + S::kMerge), ml,
         [&] {
 #pragma unroll
-          for (int n = 0; n < 2; ++n)
+          for (int n = 0; n < RN; ++n)
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
-              float m = -INFINITY, y = 0.f;
-              if (n < RN) {
-                m = ref[n % RN][x];
+              float m = ref[n][x];
 #pragma unroll
-                for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
-                y = l[n % RN][x];
-                if (ref[n % RN][x] != -INFINITY) y *= ex2(ref[n % RN][x] - m);
+              for (int z = 4; z < 32; z <<= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, z));
+              float y = l[n][x];
+              if (ref[n][x] != -INFINITY) y *= ex2(ref[n][x] - m);
 #pragma unroll
-                for (int z = 4; z < 32; z <<= 1) y += __shfl_xor_sync(0xffffffffu, y, z);
-              }
-              if (g == 0) ml[kg * 16 * WM + row0 + 8 * n + x] = make_float2(m, y);
+              for (int z = 4; z < 32; z <<= 1) y += __shfl_xor_sync(0xffffffffu, y, z);
+              if (g == 0) ml[kg * TM * WM + row0 + 8 * n + x] = make_float2(m, y);
             }
         },
         [&](float* buf, int q, auto most) {
@@ -429,9 +436,9 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
               // in two factors: a scale may take their product past fp32 where the sum is not
               const float f = m == -INFINITY ? 0.f : ex2(0.5f * (refv[n][x] - m));
 #pragma unroll
-              for (int e = 0; e < 2; ++e) {
-                const float* y = o[n][2 * q + e];
-                *reinterpret_cast<float2*>(buf + (kg * 16 * WM + row) * 32 +
+              for (int e = 0; e < kCols / 16; ++e) {
+                const float* y = o[n][kCols / 16 * q + e];
+                *reinterpret_cast<float2*>(buf + (kg * TM * WM + row) * kCols +
                                            ((e * 16 + g * 2) ^ ((row & 3) * 8))) =
                     make_float2(y[x] * f * f, y[2 + x] * f * f);
               }
@@ -459,6 +466,7 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   p.shared = 0;
   // no more CTAs than units there can be
   const int64_t most = (int64_t)p.N * p.Hk * ((keys + kUnit - 1) / kUnit);
+  const int R = p.nq * p.G;
   w.grid = (int)(most < L.grid ? (most > 0 ? most : 1) : L.grid);
   if (kScores) {
     w.lse2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.lse2);
@@ -473,16 +481,17 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   CUtensorMap tm_k, tm_v;
   if (!encode_u8_tmap(&tm_k, p.k, 3, dim, str, box) || !encode_u8_tmap(&tm_v, p.v, 3, dim, str, box))
     return false;
-  const int R = p.nq * p.G;
-  const auto kernel = R <= 8    ? decode8_kernel<D, 1, 1, kScores>
-                      : R <= 16 ? decode8_kernel<D, 2, 1, kScores>
-                      : R <= 32 ? decode8_kernel<D, 2, 2, kScores>
-                                : decode8_kernel<D, 2, 4, kScores>;
-  constexpr int smem = Smem8<D>::kBytes;
-  ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
-  return launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w, tm_k, tm_v) ==
-             cudaSuccess &&
-         launch_rest<D, kUnit, kScores>(p, w, s);
+  auto go = [&](auto kernel, int smem) {
+    ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
+    return launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w, tm_k, tm_v) == cudaSuccess;
+  };
+  // (More than 16 rows: several warps with 16 each, which convert the same keys. One warp with 32
+  // rows has too few registers for its sums: 96 sequences of 407 to 814 keys, 32 rows, 30 us and 52.)
+  const bool ok = R <= 8    ? go(decode8_kernel<D, 1, 1, kScores>, Smem8<D, 1>::kBytes)
+                  : R <= 16 ? go(decode8_kernel<D, 2, 1, kScores>, Smem8<D, 2>::kBytes)
+                  : R <= 32 ? go(decode8_kernel<D, 2, 2, kScores>, Smem8<D, 2>::kBytes)
+                            : go(decode8_kernel<D, 2, 4, kScores>, Smem8<D, 2>::kBytes);
+  return ok && launch_rest<D, kUnit, kScores>(p, w, s);
 }
 
 }  // namespace
