@@ -486,7 +486,8 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
     return launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w, tm_k, tm_v) == cudaSuccess;
   };
   // (More than 16 rows: several warps with 16 each, which convert the same keys. One warp with 32
-  // rows has too few registers for its sums: 96 sequences of 407 to 814 keys, 32 rows, 30 us and 52.)
+  // rows has too few registers for its sums: 96 sequences, 32 rows, 30 us and 52 with 407 to 814 keys
+  // of head size 128, 86 and 162 with 4000 to 8000 of 64.)
   const bool ok = R <= 8    ? go(decode8_kernel<D, 1, 1, kScores>, Smem8<D, 1>::kBytes)
                   : R <= 16 ? go(decode8_kernel<D, 2, 1, kScores>, Smem8<D, 2>::kBytes)
                   : R <= 32 ? go(decode8_kernel<D, 2, 2, kScores>, Smem8<D, 2>::kBytes)
