@@ -3,12 +3,16 @@
 // The choice is per sequence and key head: the k = keep - recent largest weights among the first
 // len - recent tokens, of equal ones those of lower index. A CTA holds the weights in registers, as
 // integers of the same order, and finds the k-th largest bit by bit from the top: a bit is set where
-// at least k values reach the number with it. A round is a comparison a value and one barrier (about
-// 150 cycles), and the rounds end early once exactly k values reach the number. A thread's values
-// are consecutive tokens, so that one scan over the threads gives the places in the result: larger
-// values stay, and of those equal to the k-th the first that are still wanted. Bound: the rounds,
-// a few microseconds; a histogram of 8 bits a pass took ten times as long, as weights share their
-// exponents and most of a warp's additions went to one counter.
+// at least k values reach the number with it, from the first bit in which the values differ on. A
+// round is a comparison a value and one barrier, and the rounds end early once exactly k values
+// reach the number. A lane holds few consecutive tokens and the next lane the next ones, so that
+// the places in the result, from scans over a warp's lanes, are close together where they are
+// written at once: larger values stay, and of those equal to the k-th the first that are still
+// wanted. Bound: latency, of the loads (page, then weights), the rounds and the writes, a few
+// microseconds each (one sequence of 16383 in 8 bits, four heads, the whole call: 16 consecutive
+// tokens a lane 17.4 us, 4 and the rounds' first bit from the ends 16.4). A histogram of 8 bits a
+// pass took ten times as long as the rounds, as weights share their exponents and most of a
+// warp's additions went to one counter.
 // Rows longer than the registers of a CTA hold (kThreads * 32 tokens) are read again each round, 8
 // bits a round, in select_long_kernel.
 //
@@ -55,8 +59,8 @@ __device__ __forceinline__ bool easy_part(const AttnEvictParams& p, int n, int h
 
 // E tokens a thread, kT threads.
 template <int E, int kT>
-__global__ void __launch_bounds__(kT) select_kernel(const AttnEvictParams p, bool wide) {
-  __shared__ uint32_t counts[2][32], list[kList], listed, found[2];
+__global__ void __launch_bounds__(kT, E == 32 ? 1 : (E == 8 ? 1536 : 1024) / kT) select_kernel(const AttnEvictParams p, bool wide) {
+  __shared__ uint32_t counts[2][32], ends[2][32], list[kList], listed, found[2];
   const int n = blockIdx.x / p.Hk, hk = blockIdx.x - n * p.Hk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   pdl_wait();
@@ -65,28 +69,40 @@ __global__ void __launch_bounds__(kT) select_kernel(const AttnEvictParams p, boo
   int M, k;
   if (easy_part(p, n, hk, kept, M, k)) return;
   if (tid == 0) listed = 0;
-  // This thread's tokens [i0, i0 + E); 0 stands for what is past the end (no weight's bits are 0).
-  const int i0 = tid * E;
+  // (8 values: 8 consecutive ones, one lookup; 64 sequences of up to 4096 80.0 us, with 4 80.7.)
+  // This thread's tokens: V from i0 + 32 V c on, for each c; 0 stands for what is past the end (no
+  // weight's bits are 0). Pages are looked up side by side, then weights.
+  constexpr int V = E == 8 ? 8 : 4, C = E / V;
+  const int i0 = warp * E * 32 + lane * V;
   uint32_t u[E];
+  int page[C];
+  float4 x[E / 4];
 #pragma unroll
-  for (int c = 0; c < E; c += 8) {  // 8 tokens are in one page
-    const int i = i0 + c;
-    int page = -1;
-    if (i < M) page = p.table[(size_t)n * p.max_pages + (i >> p.page_shift)];
-    const float* w = p.weights + ((((int64_t)page * p.Hk + hk) << p.page_shift) + (i & (p.page - 1)));
-    float x[8];
-    if (page < 0 || page >= p.n_pages) {
+  for (int c = 0; c < C; ++c) {
+    const int i = i0 + c * 32 * V;
+    page[c] = -1;
+    if (i < M) page[c] = p.table[(size_t)n * p.max_pages + (i >> p.page_shift)];
+  }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = 0.f;
-    } else if (wide) {
-      *reinterpret_cast<float4*>(x) = reinterpret_cast<const float4*>(w)[0];
-      *reinterpret_cast<float4*>(x + 4) = reinterpret_cast<const float4*>(w)[1];
-    } else {
+  for (int c = 0; c < C; ++c) {
+    const float* w = p.weights + ((((int64_t)page[c] * p.Hk + hk) << p.page_shift) +
+                                  ((i0 + c * 32 * V) & (p.page - 1)));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = w[e];
+    for (int e = 0; e < V / 4; ++e) {
+      x[c * V / 4 + e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (page[c] >= 0 && page[c] < p.n_pages) {
+        if (wide) x[c * V / 4 + e] = reinterpret_cast<const float4*>(w)[e];
+        else x[c * V / 4 + e] = make_float4(w[4 * e], w[4 * e + 1], w[4 * e + 2], w[4 * e + 3]);
+      }
     }
+  }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) u[c + e] = i + e < M ? order_bits(x[e]) : 0;
+  for (int e = 0; e < E; e += 4) {
+    const int i = i0 + e / V * 32 * V + e % V;
+    u[e] = i < M ? order_bits(x[e / 4].x) : 0;
+    u[e + 1] = i + 1 < M ? order_bits(x[e / 4].y) : 0;
+    u[e + 2] = i + 2 < M ? order_bits(x[e / 4].z) : 0;
+    u[e + 3] = i + 3 < M ? order_bits(x[e / 4].w) : 0;
   }
   // Sum of a value over the CTA.
   auto total = [&](uint32_t x, int buf) -> uint32_t {
@@ -97,8 +113,24 @@ __global__ void __launch_bounds__(kT) select_kernel(const AttnEvictParams p, boo
   };
   // The k-th largest value lies in [top, top + 2^bit); `above` values lie above that, `reach` from
   // top on.
-  uint32_t top = 0, above = 0, reach = M;
-  int bit = 32;
+  uint32_t above = 0, reach = M, least = ~0u, most = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    most = max(most, u[e]);
+    least = min(least, u[e] - 1);  // (past the end: the largest)
+  }
+  most = __reduce_max_sync(0xffffffffu, most);
+  least = __reduce_min_sync(0xffffffffu, least);
+  if (lane == 0) {
+    ends[0][warp] = most;
+    ends[1][warp] = least;
+  }
+  __syncthreads();
+  most = __reduce_max_sync(0xffffffffu, lane < kT / 32 ? ends[0][lane] : 0);
+  least = __reduce_min_sync(0xffffffffu, lane < kT / 32 ? ends[1][lane] : ~0u) + 1;
+  // The bits above the first one in which the ends differ are known.
+  int bit = 32 - __clz(most ^ least);
+  uint32_t top = bit < 32 ? most >> bit << bit : 0;
   while (bit > 0 && reach != (uint32_t)k && reach - above > kList) {
     const uint32_t next = top + (1u << --bit);
     uint32_t c = 0;
@@ -146,38 +178,63 @@ __global__ void __launch_bounds__(kT) select_kernel(const AttnEvictParams p, boo
   }
   const bool exact = reach == (uint32_t)k;  // k values reach it
   // Where exactly k values reach it, all of them stay; else the larger ones and the first equal ones.
-  uint32_t more = 0, same = 0;
+  // Places by scans over the lanes of a warp, of four c's at once: a byte each, 128 at most (one c: up
+  // to 256, in all bits).
+  constexpr int Q = (C + 3) / 4;
+  constexpr uint32_t kField = C == 1 ? ~0u : 255;
+  uint32_t more[Q] = {}, same[Q] = {}, m_inc[Q], s_inc[Q], m_all[Q], s_all[Q], m_sum = 0, s_sum = 0;
 #pragma unroll
   for (int e = 0; e < E; ++e) {
-    more += exact ? u[e] >= top : u[e] > top;
-    same += !exact && u[e] == top;
+    const uint32_t one = 1u << (e / V % 4 * 8);
+    more[e / V / 4] += (exact ? u[e] >= top : u[e] > top) ? one : 0;
+    same[e / V / 4] += !exact && u[e] == top ? one : 0;
   }
-  // Those of the threads before this one.
-  uint32_t m_inc = more, s_inc = same;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint32_t a = __shfl_up_sync(0xffffffffu, m_inc, o), b = __shfl_up_sync(0xffffffffu, s_inc, o);
-    if (lane >= o) {
-      m_inc += a;
-      s_inc += b;
+  for (int q = 0; q < Q; ++q) {
+    m_inc[q] = more[q];
+    s_inc[q] = same[q];
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t a = __shfl_up_sync(0xffffffffu, m_inc[q], o);
+      const uint32_t b = __shfl_up_sync(0xffffffffu, s_inc[q], o);
+      if (lane >= o) {
+        m_inc[q] += a;
+        s_inc[q] += b;
+      }
+    }
+    m_all[q] = __shfl_sync(0xffffffffu, m_inc[q], 31);
+    s_all[q] = __shfl_sync(0xffffffffu, s_inc[q], 31);
+#pragma unroll
+    for (int b = 0; b < (C == 1 ? 8 : 32); b += 8) {
+      m_sum += m_all[q] >> b & kField;
+      s_sum += s_all[q] >> b & kField;
     }
   }
   __syncthreads();
-  if (lane == 31) {
-    counts[0][warp] = m_inc;
-    counts[1][warp] = s_inc;
+  if (lane == 0) {
+    counts[0][warp] = m_sum;
+    counts[1][warp] = s_sum;
   }
   __syncthreads();
   const uint32_t mw = lane < kT / 32 ? counts[0][lane] : 0, sw = lane < kT / 32 ? counts[1][lane] : 0;
   const uint32_t want = k - __reduce_add_sync(0xffffffffu, mw);  // of the equal ones
-  uint32_t m_at = m_inc - more + __reduce_add_sync(0xffffffffu, lane < warp ? mw : 0);
-  uint32_t s_at = s_inc - same + __reduce_add_sync(0xffffffffu, lane < warp ? sw : 0);
+  uint32_t m_base = __reduce_add_sync(0xffffffffu, lane < warp ? mw : 0);
+  uint32_t s_base = __reduce_add_sync(0xffffffffu, lane < warp ? sw : 0);
 #pragma unroll
-  for (int e = 0; e < E; ++e) {
-    const bool is_more = exact ? u[e] >= top : u[e] > top, is_same = !exact && u[e] == top;
-    if (is_more || (is_same && s_at < want)) kept[m_at + min(s_at, want)] = i0 + e;
-    m_at += is_more;
-    s_at += is_same;
+  for (int c = 0; c < C; ++c) {
+    const int q = c / 4, b = c % 4 * 8;
+    uint32_t m_at = m_base + (m_inc[q] >> b & kField) - (more[q] >> b & kField);
+    uint32_t s_at = s_base + (s_inc[q] >> b & kField) - (same[q] >> b & kField);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      const uint32_t x = u[c * V + e];
+      const bool is_more = exact ? x >= top : x > top, is_same = !exact && x == top;
+      if (is_more || (is_same && s_at < want)) kept[m_at + min(s_at, want)] = i0 + c * 32 * V + e;
+      m_at += is_more;
+      s_at += is_same;
+    }
+    m_base += m_all[q] >> b & kField;
+    s_base += s_all[q] >> b & kField;
   }
 }
 
@@ -329,14 +386,17 @@ __global__ void __launch_bounds__(kMoveWarps * 32) move_kernel(const AttnEvictPa
 }  // namespace
 
 bool launch_attn_evict(const AttnEvictParams& p, cudaStream_t s) {
-  // The smallest form that the table's rows fit: registers are read once, and more CTAs fit an SM.
+  // The smallest form that the table's rows fit: registers are read once, and more CTAs fit an SM. 16
+  // values a thread where that makes a row 512 threads (32 sequences of 8000 cut to 256 in 8 bits 22.3
+  // us, 8 values and 1024 threads 25.2), 8 below (64 sequences of up to 4096 cut to 1024 80.0 us, 16
+  // values and 256 threads 80.8; two of 2000 cut to 256 10.2 us, 16 and 128 threads 10.5).
   const dim3 rows((unsigned)(p.N * p.Hk));
   const int64_t most = (int64_t)p.max_pages * p.page;
   const bool wide = ((uintptr_t)p.weights & 15) == 0;
   const cudaError_t e =
       most <= 2048    ? launch_pdl(select_kernel<8, 256>, rows, dim3(256), 0, s, p, wide)
       : most <= 4096  ? launch_pdl(select_kernel<8, 512>, rows, dim3(512), 0, s, p, wide)
-      : most <= 8192  ? launch_pdl(select_kernel<8, 1024>, rows, dim3(1024), 0, s, p, wide)
+      : most <= 8192  ? launch_pdl(select_kernel<16, 512>, rows, dim3(512), 0, s, p, wide)
       : most <= 16384 ? launch_pdl(select_kernel<16, 1024>, rows, dim3(1024), 0, s, p, wide)
       : most <= 32768 ? launch_pdl(select_kernel<32, 1024>, rows, dim3(1024), 0, s, p, wide)
                       : launch_pdl(select_long_kernel, rows, dim3(kSelect), 0, s, p);
