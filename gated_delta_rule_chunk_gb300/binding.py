@@ -715,6 +715,7 @@ def gdn_test_attn_tiles(tiles: int) -> None:
 
 
 def gdn_test_attn_timeout(polls: int, item: int = 0) -> None:
-    """Testing hook: with polls > 0 the tensor-core attention kernel waits that many polls, before
-    a CTA's `item`-th work item, for an event that never happens (GDN_DEV_TIMEOUT); 0 turns it off."""
+    """Testing hook: with polls > 0 the kernels of gdn_attn_prefill, gdn_attn_prefill_weights, decode
+    over an 8-bit cache and a common prefix's pass wait that many polls, before a CTA's `item`-th
+    work item, for an event that never happens (GDN_DEV_TIMEOUT); 0 turns it off."""
     load_library().gdn_test_attn_timeout(int(polls), int(item))

@@ -395,6 +395,7 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
       from_start = true;
       if (ends) at.next_item(p);
     }
+    tmem_ld_wait();  // (who gave up may have columns on the way)
   } else if (steps > 0 && warp == 16) {
     // ---------------------------------------------------------------- loads
     if (lane == 0) {

@@ -279,10 +279,11 @@ void gdn_test_attn_prefix(int32_t always);
 void gdn_test_attn_tiles(int32_t tiles);
 
 /*
- * Testing hook. Every on-chip wait of gdn_attn_prefill and of a common prefix's own pass is
- * bounded. With polls > 0, that is the bound in the calls that follow, and what issues the
- * products waits, before a CTA's work item number `item`, for an event that never happens: the
- * wait runs out, GDN_DEV_TIMEOUT is in the status word, every warp leaves, the results of that
+ * Testing hook. Every on-chip wait of gdn_attn_prefill, of gdn_attn_prefill_weights, of decode
+ * over an 8-bit cache and of a common prefix's own pass is bounded. With polls > 0, that is the
+ * bound in the calls that follow, and what issues the products waits, before a CTA's work item
+ * number `item` (of gdn_attn_prefill_weights: row tile of a head; of an 8-bit cache: 128 keys of
+ * a key head), for an event that never happens: the wait runs out, GDN_DEV_TIMEOUT is in the status word, every warp leaves, the results of that
  * call are invalid, and copies and products in flight are still waited for (at the full bound)
  * before the kernel ends, so the device stays usable. 0 (the default) turns it off.
  */

@@ -1025,6 +1025,58 @@ def test_two_graphs_with_workspaces_of_their_own():
             assert all(torch.equal(a, b) for a, b in zip(snapshot(state), want))
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("call", ["decode8", "decode8_rows", "decode8_weights", "prompt"])
+@pytest.mark.parametrize("item", [0, 1, 2])
+def test_a_wait_that_runs_out_is_reported_and_leaves_the_next_call_right(call, D, item):
+    """The testing hook has a wait before a CTA's first, second or third work item run out: the call
+    returns with GDN_DEV_TIMEOUT, and with the hook off the same call on the same buffers gives
+    its results again."""
+    g = torch.Generator().manual_seed(52)
+    status = new_status()
+    if call == "prompt":
+        q, k = (randn(g, 5000, h, D).cuda() for h in (8, 2))
+        cu = i32([0, 2000, 2001, 5000])
+        table = torch.arange(3 * 24, dtype=torch.int32, device="cuda").reshape(3, 24)
+        lse = torch.full((5000, 8), 6.0, device="cuda")
+        size = B.gdn_attn_prefill_weights_workspace_size(B.make_attn_desc(
+            5000, 3, 8, 2, D, page_size=128, n_pages=72, max_pages=24))
+        work = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+        def run():
+            w = torch.zeros(72, 2, 128, device="cuda")
+            B.gdn_attn_prefill_weights(q, k, lse, w, table, cu, workspace=work, status=status)
+            return (w,)
+    else:
+        N, Hk, nq = 200, 4, 5 if call == "decode8_rows" else 1
+        kb, ks = random_cache8(g, N * 8, Hk, 128, D)
+        vb, vs = random_cache8(g, N * 8, Hk, 128, D)
+        kb, vb, ks, vs = kb.cuda().view(F8), vb.cuda().view(F8), ks.cuda(), vs.cuda()
+        table = torch.randperm(N * 8, generator=g).to(torch.int32).reshape(N, 8).cuda()
+        kv = torch.randint(600, 1025, (N,), generator=g).to(torch.int32).cuda()
+        q = randn(g, N, nq, 5 * Hk, D).cuda()
+        kinds = dict(with_weights=call == "decode8_weights")
+        size = B.gdn_attn_decode_cache_workspace_size(B.make_attn_desc(
+            N * nq, N, 5 * Hk, Hk, D, page_size=128, n_pages=N * 8, max_pages=8), **kinds)
+        work = torch.empty(size, dtype=torch.uint8, device="cuda")
+
+        def run():
+            w = torch.zeros(N * 8, Hk, 128, device="cuda") if call == "decode8_weights" else None
+            out = B.gdn_attn_decode(q, kb, vb, table, kv, k_scale=ks, v_scale=vs, weights=w, workspace=work,
+                                    status=status)
+            return (out,) if w is None else (out, w)
+    want = run()
+    assert status.item() == 0
+    try:
+        B.gdn_test_attn_timeout(256, item)
+        run()
+        assert status.item() & 8
+    finally:
+        B.gdn_test_attn_timeout(0)
+    got = run()
+    assert status.item() == 0 and all(torch.equal(a, b) for a, b in zip(got, want))
+
+
 def test_no_tokens():
     e = lambda *s, t=BF: torch.empty(*s, dtype=t, device="cuda")
     k8, ks = e(2, 1, 16, 64, t=F8), e(2, 1, 1, t=F32)
