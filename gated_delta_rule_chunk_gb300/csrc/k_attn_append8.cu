@@ -26,7 +26,8 @@ namespace {
 constexpr int kWarps = 4;
 constexpr uint32_t kLargest = 0x7F7FFFFFu;  // bits of the largest finite number
 
-// Sequence n of row t and its rows [b, e); n = -1 outside every sequence. By a whole warp.
+// Sequence n of row t and its rows [b, e), which are rows of the call; n = -1 outside every sequence
+// and in one that passes the call's rows. By a whole warp.
 __device__ __forceinline__ int warp_find_seq(const AttnAppend8Params& p, int t, int& b, int& e) {
   if (!p.cu) {
     b = 0;
@@ -41,7 +42,7 @@ __device__ __forceinline__ int warp_find_seq(const AttnAppend8Params& p, int t, 
   while (true) {
     const int step = (count + 31) / 32, at = lo + min(lane * step, count - 1);
     const uint32_t below = __ballot_sync(0xffffffffu, lane * step < count && p.cu[at] <= t);
-    if (gb <= t && t < ge) {
+    if (gb >= 0 && gb <= t && t < ge && ge <= p.T) {
       b = gb;
       e = ge;
       return guess;

@@ -202,6 +202,30 @@ def test_append_places_that_do_not_exist():
     assert status.item() & 1
 
 
+@pytest.mark.parametrize("cu", [[0, 40, 90], [0, 61], [-3, 20, 90, 60], [0, 2, 2 ** 31 - 1]])
+def test_append_sequences_that_pass_the_rows(cu):
+    """What lies behind k and v (NaN here) does not reach the cache."""
+    g = torch.Generator().manual_seed(6)
+    N, T, Hk, D = len(cu) - 1, 60, 2, 64
+    kb, ks = random_cache8(g, 8 * N, Hk, 16, D)
+    x = torch.full((T + 40, Hk, D), float("nan"), dtype=BF)
+    x[:T] = randn(g, T, Hk, D)
+    table = torch.arange(8 * N, dtype=torch.int32).reshape(N, 8)
+    for dtype in (BF, F32):
+        k = x.to(dtype).cuda()[:T]
+        dev = [kb.cuda(), kb.cuda(), ks.cuda(), ks.cuda()]
+        status = new_status()
+        B.gdn_attn_append8(k, k, dev[0].view(F8), dev[1].view(F8), dev[2], dev[3], table.cuda(), cu_seqlens=i32(cu),
+                           status=status)
+        assert status.item() & 1
+        for b, s in ((dev[0], dev[2]), (dev[1], dev[3])):
+            assert np.isfinite(C.VALUES[as_bytes(b)]).all() and torch.isfinite(s).all()
+        if 0 <= cu[1] <= T and cu[0] == 0:
+            want, s = C.append8(np64(x[:cu[1]]), kb.numpy(), ks.numpy(), table.numpy()[:1])
+            assert C.same_bytes(as_bytes(dev[0])[:8], want[:8]).all()
+            assert np.array_equal(dev[2].cpu().numpy()[:8], s[:8])
+
+
 # ---------------------------------------------------------------- decode
 def close(out, lse, ref, mag, ref_lse, floor=0.0):
     o = np64(out).reshape(ref.shape)
