@@ -679,7 +679,8 @@ def gdn_attn_prefill_weights(q: torch.Tensor, k: torch.Tensor, lse: torch.Tensor
     [T, Hk, D] bf16 and lse fp32 [T, H] of gdn_attn_prefill; weights fp32 [n_pages, Hk, page_size]
     is set, at the places that page_table int32 [N, max_pages] gives the prompts' tokens (the first
     of their sequences), to the sum of their softmax weights over all rows (window = 0) or the last
-    `window` rows of each prompt, and over the query heads of the group."""
+    `window` rows of each prompt, and over the query heads of the group. A positive scale below
+    2^-100 is refused."""
     (_attn_module or _attn()).prefill_weights(
         q, k, lse, weights, page_table, cu_seqlens, window, scale, workspace, status,
         None if stream is None else stream.cuda_stream)

@@ -289,6 +289,7 @@ int gdn_attn_prefill_weights(const gdn_attn_desc* desc, const void* q, const voi
   if (d.T == 0) return clear_status(d.status, stream) ? GDN_OK : GDN_ERR_LAUNCH_FAILED;
   if (!q || !k || !lse || !page_table || !weights || !d.workspace) return GDN_ERR_NULL_ARG;
   if (d.page_size == 0 || (!cu_seqlens && d.N != 1) || window < 0) return GDN_ERR_BAD_SHAPE;
+  if (scale > 0.f && scale < 0x1p-100f) return GDN_ERR_UNSUPPORTED;  // lse / scale is formed
   if (!aligned(q, 16) || !aligned(k, 16)) return GDN_ERR_MISALIGNED;
   const void* ptrs4[] = {lse, cu_seqlens, page_table, weights, d.status};
   for (const void* p : ptrs4)

@@ -69,16 +69,17 @@ enum {
  *   max_pages    columns of page_table
  *   rot_dim      rotated elements at the start of each head: 0 or a multiple of 16, <= D
  *   max_pos      rows of rope
- *   in_dtype     gdn_dtype of x (front), q, k, v and the cache (prefill and decode:
- *                GDN_BF16 only)
+ *   in_dtype     gdn_dtype of x (front), k, v (append), q, k, v and a cache not in 8 bits
+ *                (prefill, decode and weights: GDN_BF16 only)
  *   out_dtype    gdn_dtype of q, k, v and the cache (front), out (prefill, decode)
  *   flags        GDN_ATTN_* bits
  *   norm_eps     eps of the norms; <= 0 selects 1e-6
  *   status       one int32 of device memory, cleared by the call and then ORed with
  *                gdn_dev_status bits, or NULL
  *   workspace    device scratch of gdn_attn_workspace_size(desc) bytes for
- *                gdn_attn_decode, 256-byte aligned; it must not be used by another call
- *                that may run at the same time (the other two calls need none)
+ *                gdn_attn_decode, of their own functions' for gdn_attn_decode_cache and
+ *                gdn_attn_prefill_weights, 256-byte aligned; it must not be used by another
+ *                call that may run at the same time (the other calls need none)
  */
 typedef struct gdn_attn_desc {
   int32_t T;
@@ -140,7 +141,7 @@ int gdn_attn_front(const gdn_attn_desc* desc, const void* x, const float* q_weig
  * (behind images, after an eviction).
  *   positions    [n_axes, T] int32, n_axes 1 to 8
  *   rope_axes    [rot_dim / 2] uint8: pair i turns by the table's row positions[rope_axes[i], t];
- *                NULL: all by the first
+ *                NULL: all by the first. 4-byte aligned
  * The token's place in the cache stays kv_lens[n] - len_n + t. A position outside [0, max_pos)
  * uses the table's nearest row (GDN_DEV_BAD_LENGTH), an axis outside [0, n_axes) the last axis
  * (GDN_DEV_BAD_LENGTH). rot_dim must not be 0. Everything else as for gdn_attn_front.
@@ -229,6 +230,7 @@ size_t gdn_attn_decode_cache_workspace_size(const gdn_attn_desc* desc, int32_t w
  * each prompt, which are the first tokens of their sequences.
  *   q [T, H, D], k [T, Hk, D]  bf16;  lse [T, H] fp32 as gdn_attn_prefill returns it
  *   window       0: all rows; w > 0: the last w rows of each prompt only
+ *   scale        as for gdn_attn_prefill; a positive one below 2^-100 is refused
  * cu_seqlens as for gdn_attn_prefill. A key with no place in the cache is left out
  * (GDN_DEV_BAD_LENGTH, GDN_DEV_BAD_PAGE_TABLE). A page of two sequences: undefined values there.
  * The workspace is gdn_attn_prefill_weights_workspace_size bytes.

@@ -183,6 +183,7 @@ PROMPT = dict(q=16, k=16, lse=16, cu=16, table=16, window=0, scale=0.0, weights=
     *[({n: None}, {}, -1) for n in ("q", "k", "lse", "table", "weights")], (dict(cu=None), {}, -2),
     (dict(window=-1), {}, -2), ({}, dict(page_size=0), -2), ({}, dict(in_dtype=torch.float32), -3),
     (dict(q=8), {}, -4), (dict(k=24), {}, -4), (dict(lse=18), {}, -4), (dict(weights=17), {}, -4),
+    (dict(scale=2.0 ** -101), {}, -3), (dict(scale=1e-45), {}, -3),
 ])
 def test_prefill_weights_refuses(lib, change, kw, want):
     a = {n: x if n in ("window", "scale") else ptr(x) for n, x in {**PROMPT, **change}.items()}

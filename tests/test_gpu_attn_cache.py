@@ -526,7 +526,7 @@ def test_decode8_cache_past_32_bit_offsets():
 
 
 # ---------------------------------------------------------------- a prompt's weights
-def run_prompt(lens, H, Hk, D, page=16, window=0, seed=0, lead=0, tail=0, mul=1.0, scale=None, cu=None):
+def run_prompt(lens, H, Hk, D, page=16, window=0, seed=0, lead=0, tail=0, mul=1.0, scale=None, slack=0.0):
     g = torch.Generator().manual_seed(seed)
     T = lead + sum(lens) + tail
     q, k = randn(g, T, H, D, mul=mul), randn(g, T, Hk, D)
@@ -540,7 +540,7 @@ def run_prompt(lens, H, Hk, D, page=16, window=0, seed=0, lead=0, tail=0, mul=1.
                                window=window, scale=scale, status=status)
     assert status.item() == 0
     want = C.prefill_weights(np64(q), np64(k), np64(lse), w.numpy(), table.numpy(), cu.numpy(), window, scale)
-    rel = weight_slack(q, np64(k), D, scale or D ** -0.5)
+    rel = weight_slack(q, np64(k), D, scale or D ** -0.5) + slack
     got = np64(w_dev)
     bad = ~(np.abs(got - want) <= rel * want + 1e-9)
     assert not bad.any(), (np.argwhere(bad)[:5], got[bad][:5], want[bad][:5], rel)
@@ -577,6 +577,15 @@ def test_prompt_score_ranges(mul):
 def test_prompt_scale_and_pages():
     run_prompt([200], 4, 1, 128, scale=0.3)
     run_prompt([300, 20], 4, 1, 64, page=256)
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -100, 1e-6, 20.0])
+def test_prompt_scales_far_from_the_usual(scale):
+    """lse / scale is formed: 1 / scale and the quotient rounded (a half step of 2^-24 each), its three
+    parts in bf16 (2^-25), the sum of it and the product (2^-23, as it may be cut), scale * log2(e)
+    and that times the sum (2^-24 each): 6.5 * 2^-24 |lse| at most, |lse| <= log(150) + 0.01 where
+    scores are nothing beside it."""
+    run_prompt([150, 20], 4, 2, 64, scale=scale, slack=6.5 * 2.0 ** -24 * 5.03)
 
 
 def test_prompt_many_sequences():
