@@ -41,7 +41,7 @@ struct Smem8 {
   static constexpr int kStages = D == 128 ? 2 : 4;
   static constexpr int kScales = kWarps * kStages * kStage;                // float4 a stage
   static constexpr int kMerge = kScales + kWarps * kStages * 16;
-  static constexpr int kMl = kMerge + kMergeBytes;
+  static constexpr int kMl = kMerge + (RN == 3 ? 3 : 1) * kMergeBytes;
   static constexpr int kBars = kMl + kWarps * RN * 8 * 8;
   static constexpr int kBytes = kBars + (kWarps * kStages + 1) * 8 + 1024;  // + alignment
 };
@@ -77,7 +77,7 @@ __device__ __forceinline__ void load_rows(uint32_t dst, const CUtensorMap* tm, i
 
 // RN tiles of 8 query rows a warp, WM warps for a pair's rows.
 template <int D, int RN, int WM, bool kScores>
-__global__ void __launch_bounds__(kWarps * 32, kDecode8Ctas)
+__global__ void __launch_bounds__(kWarps * 32, RN == 3 ? 2 : kDecode8Ctas)
 decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ CUtensorMap tm_k,
                const __grid_constant__ CUtensorMap tm_v) {
   using S = Smem8<D, RN>;
@@ -408,7 +408,7 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
     if (cur.u < u1) load_q();  // the next pair's queries arrive meanwhile
     const bool whole = seg_chunk == cur.kOwn && was.chunk == was.chunks - 1;
     float2* ml = reinterpret_cast<float2*>(smem + S::kMl);
-    constexpr int kCols = RN == 1 ? 64 : 32;
+    constexpr int kCols = RN == 2 ? 32 : 64;
     finish_part<D, WM, TM, kCols, kScores, 1>(
         p, w, reinterpret_cast<float*>(smem + S::kMerge), ml,
         [&] {
@@ -467,7 +467,9 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
   // no more CTAs than units there can be
   const int64_t most = (int64_t)p.N * p.Hk * ((keys + kUnit - 1) / kUnit);
   const int R = p.nq * p.G;
-  w.grid = (int)(most < L.grid ? (most > 0 ? most : 1) : L.grid);
+  const bool by24 = (R > 16 && R <= 24) || (R > 32 && R <= 48);  // rows a warp, see below
+  const int full = by24 ? L.grid / kDecode8Ctas * 2 : L.grid;
+  w.grid = (int)(most < full ? (most > 0 ? most : 1) : full);
   if (kScores) {
     w.lse2 = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.lse2);
     w.scores = reinterpret_cast<float*>(static_cast<char*>(workspace) + L.scores);
@@ -485,12 +487,17 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
     ensure_smem_limit(reinterpret_cast<const void*>(kernel), smem);
     return launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w, tm_k, tm_v) == cudaSuccess;
   };
-  // (More than 16 rows: several warps with 16 each, which convert the same keys. One warp with 32
+  // (More than 16 rows: warps with 24 each where that leaves fewer rows empty, with the registers of
+  // two CTAs an SM in place of three: 64 sequences of 2000 to 4000 keys, head size 128, 24 rows 77.9 us,
+  // as two warps with 16 87.1; 40 rows 120.5 and 144.7; one of 8000 keys, 40 rows, 20.6 and 23.0, but
+  // 17.9 and 16.9 at head size 64. Else several with 16, which convert the same keys. One warp with 32
   // rows has too few registers for its sums: 96 sequences, 32 rows, 30 us and 52 with 407 to 814 keys
   // of head size 128, 86 and 162 with 4000 to 8000 of 64.)
   const bool ok = R <= 8    ? go(decode8_kernel<D, 1, 1, kScores>, Smem8<D, 1>::kBytes)
                   : R <= 16 ? go(decode8_kernel<D, 2, 1, kScores>, Smem8<D, 2>::kBytes)
+                  : by24 && R <= 24 ? go(decode8_kernel<D, 3, 1, kScores>, Smem8<D, 3>::kBytes)
                   : R <= 32 ? go(decode8_kernel<D, 2, 2, kScores>, Smem8<D, 2>::kBytes)
+                  : by24    ? go(decode8_kernel<D, 3, 2, kScores>, Smem8<D, 3>::kBytes)
                             : go(decode8_kernel<D, 2, 4, kScores>, Smem8<D, 2>::kBytes);
   return ok && launch_rest<D, kUnit, kScores>(p, w, s);
 }

@@ -329,6 +329,15 @@ def test_decode_several_tokens(nq, G, bits, weights):
     run_decode([nq, nq + 1, 100, nq + 15, 257], 2 * G, 2, 64, 32, nq=nq, bits=bits, weights=weights, seed=nq)
 
 
+@pytest.mark.parametrize("rows", [17, 24, 25, 32, 33, 40, 48, 49])
+@pytest.mark.parametrize("D", [64, 128])
+def test_decode8_rows_of_a_key_head(rows, D):
+    """Either side of each change of the warps' tiles, with one token and with several."""
+    run_decode([300, 17, 0, 1000], rows, 1, D, 32, weights=True, seed=rows)
+    nq = next(n for n in (8, 7, 5, 3, 1) if rows % n == 0)
+    run_decode([300, 2, 129, 700], rows // nq * 2, 2, D, 16, nq=nq, seed=rows)
+
+
 @FORMS
 def test_decode_fewer_keys_than_rows_and_none(bits, weights):
     run_decode([0, 5, 2, 0, 1, 33], 2, 1, 64, 16, nq=4, bits=bits, weights=weights)
