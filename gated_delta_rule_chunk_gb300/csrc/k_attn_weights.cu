@@ -22,7 +22,14 @@
 // Columns that a key does not count (rows before it or before the window, past the sequence's end)
 // are selected away in the tiles that have any; a row there may hold anything.
 //
-// Bound: the products and the exponentials alike, 1,076 and 1,024 cycles a step.
+// Bound: a step's operands and exponentials take 1,152 cycles of shared memory (both operands of
+// an N = 128 product come from there) and 1,024 of the unit, and what passes between warps is on the
+// way from one to the other: 1,700 cycles a step measured. In front and behind stand the lookup of a
+// CTA's part, its first tiles and the sums' merge, 9 us for any call. 4096 tokens, 16 heads 36.4 us
+// (0.94 PFLOP/s of the pairs seen), 8 ragged prompts 75.6. Branches of masked tiles between the loads and
+// the exponentials of unmasked ones cost 1 us of the first, 64-bit divisions and a binary search in
+// the lookups 2. No gain: barriers of their own for the two tiles, three Q tiles, two warps that
+// issue, all of a thread's columns loaded first.
 #include "attn_tc.cuh"
 
 namespace gdn {
@@ -83,6 +90,27 @@ struct WeightsParts {
   float* part;     // [2 * grid][256] an item's sums in a CTA: of its first item, of its last
 };
 
+// a / b of numbers that seldom need 64 bits, whose division takes several times as long.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+  if (((a | b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
+
+// The last i in [0, count) with holds(i), which is true up to some i (and at 0); by a whole warp.
+template <typename F>
+__device__ __forceinline__ int last_of(int count, F holds) {
+  const int lane = threadIdx.x & 31;
+  int lo = 0;
+  while (count > 1) {
+    const int step = (count + 31) / 32;
+    const bool yes = lane * step < count && (lane == 0 || holds(lo + lane * step));
+    const int j = 31 - __clz(__ballot_sync(0xffffffffu, yes));
+    lo += j * step;
+    count = min(step, count - j * step);
+  }
+  return lo;
+}
+
 // Steps of a sequence: nt row tiles, of which the window begins in tile w.
 struct Shape {
   int len, row0, nt, w;
@@ -99,15 +127,9 @@ struct Shape {
     return (int64_t)k0 * (nt - w) + (int64_t)(pair - k0) * (nt - pair + 1 - k0);
   }
   __device__ int pairs() const { return (nt + 1) / 2; }
-  // the pair that step u (of one key head, all its query heads) is in
+  // the pair that step u (of one key head, all its query heads) is in; by a whole warp
   __device__ int pair_of(int64_t u, int G) const {
-    int lo = 0, hi = pairs() - 1;
-    while (lo < hi) {
-      const int m = (lo + hi + 1) >> 1;
-      if (before(m) * G <= u) lo = m;
-      else hi = m - 1;
-    }
-    return lo;
+    return last_of(pairs(), [&](int m) { return before(m) * G <= u; });
   }
 };
 
@@ -199,8 +221,8 @@ __device__ __forceinline__ uint32_t find_steps(const AttnWeightsParams& p, const
       if (scribe && lane == 0) w.first[p.N] = after;
       const int64_t grid = min((int64_t)gridDim.x, after);
       if ((int64_t)blockIdx.x >= grid) return 0;
-      u0 = after * blockIdx.x / grid;
-      steps = (uint32_t)(after * (blockIdx.x + 1) / grid - u0);
+      u0 = quotient(after * blockIdx.x, grid);
+      steps = (uint32_t)(quotient(after * (blockIdx.x + 1), grid) - u0);
     }
     if (!count || (last && p.N <= 32)) {
       const uint32_t hit = __ballot_sync(0xffffffffu, c > 0 && u0 >= first && u0 < first + c);
@@ -220,12 +242,13 @@ __device__ __forceinline__ uint32_t find_steps(const AttnWeightsParams& p, const
   at.next = p.cu ? at.bound(p, at.n + 2) : p.T;
   at.shape = Shape(p, at.end - at.base);
   const int64_t head = at.shape.before(at.shape.pairs()) * p.G;
-  at.hk = (int)(r / head);
+  at.hk = (int)quotient(r, head);
   r -= at.hk * head;
   at.pair = at.shape.pair_of(r, p.G);
   r -= at.shape.before(at.pair) * p.G;
-  at.rt = at.shape.first_row_tile(at.pair) + (int)(r / p.G);
-  at.g = (int)(r % p.G);
+  const int tile = (int)quotient(r, p.G);
+  at.rt = at.shape.first_row_tile(at.pair) + tile;
+  at.g = (int)(r - (int64_t)tile * p.G);
   return steps;
 }
 
@@ -316,16 +339,16 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
         const int r0 = at.rt * kTile + half * 64;
         const int lo = max(key, q.row0) - r0, hi = at.rt >= kt && kt < q.nt ? q.len - r0 : INT_MIN;
         const int lo0 = max(key - lane, q.row0) - r0, lo1 = max(key - lane + 31, q.row0) - r0;
-        auto chunk = [&](const float (&y)[16], int c0) {
-          if (c0 + 16 <= lo0 || c0 >= hi) return;
-          if (c0 >= lo1 && c0 + 16 <= hi) {
+        auto all = [&](const float (&y)[16]) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-              const float2 x = mul2(make_float2(y[2 * i], y[2 * i + 1]), c2);
-              acc[i & 1] = add2(acc[i & 1], make_float2(ex2(x.x), ex2(x.y)));
-            }
-            return;
+          for (int i = 0; i < 8; ++i) {
+            const float2 x = mul2(make_float2(y[2 * i], y[2 * i + 1]), c2);
+            acc[i & 1] = add2(acc[i & 1], make_float2(ex2(x.x), ex2(x.y)));
           }
+        };
+        auto some = [&](const float (&y)[16], int c0) {
+          if (c0 + 16 <= lo0 || c0 >= hi) return;
+          if (c0 >= lo1 && c0 + 16 <= hi) return all(y);
           const uint32_t counts =
               (lo <= c0 ? 0xffffu : lo >= c0 + 16 ? 0u : 0xffffu << (lo - c0)) &
               (hi >= c0 + 16 ? 0xffffu : (1u << (hi - c0)) - 1);
@@ -337,7 +360,7 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
           }
         };
         const uint32_t todo = min((uint32_t)(p.G - at.g), left), end = s + todo;
-        for (; s < end; ++s) {
+        auto step = [&](auto chunk) {
           const uint32_t b = s & 1;
           if (!loaded) {
             wait(&B.s_full[b], s >> 1);
@@ -363,7 +386,12 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
             tmem_ld16(t + (b ^ 1) * 128, v[0]);
           }
           chunk(v[1], 48);
-        }
+        };
+        // (all columns count: no branches between a step's loads and its exponentials)
+        if (lo1 <= 0 && hi >= 64)
+          for (; s < end; ++s) step([&](const float (&y)[16], int) { all(y); });
+        else
+          for (; s < end; ++s) step(some);
         sum += (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
         left -= todo;
         at.g += (int)todo;
@@ -535,25 +563,29 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
 // if it began there.
 __global__ void __launch_bounds__(256) reduce_kernel(const AttnWeightsParams p, const WeightsParts w) {
   pdl_wait();
+  pdl_release();
   const int64_t U = w.first[p.N], grid = min((int64_t)gridDim.x + 1, U);
   const int64_t cta = blockIdx.x;
   if (cta + 1 >= grid) return;
-  const int64_t u0 = U * cta / grid, cut = U * (cta + 1) / grid;
-  int lo = 0, hi = p.N - 1;  // the last sequence that begins at or before the cut
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (w.first[m] <= cut) lo = m;
-    else hi = m - 1;
-  }
-  const int n = lo;
+  const int64_t u0 = quotient(U * cta, grid), cut = quotient(U * (cta + 1), grid);
+  // the last sequence that begins at or before the cut
+  const int n = last_of(p.N, [&](int m) { return w.first[m] <= cut; });
   const Shape s(p, w.seq[n].y);
   const int64_t head = s.before(s.pairs()) * p.G, r = cut - w.first[n];
-  const int hk = (int)(r / head), pair = s.pair_of(r - hk * head, p.G);
+  const int hk = (int)quotient(r, head), pair = s.pair_of(r - hk * head, p.G);
   const int64_t first = w.first[n] + hk * head + s.before(pair) * p.G;
   const int64_t last = w.first[n] + hk * head + s.before(pair + 1) * p.G;
   if (first >= cut || first < u0) return;
+  // The CTAs up to the one with the item's last step (U i / grid < last), eight parts at a time.
+  const int64_t end = quotient(last * grid - 1, U);
   float sum = w.part[(2 * cta + (first == u0 ? 0 : 1)) * 256 + threadIdx.x];
-  for (int64_t i = cta + 1; U * i / grid < last; ++i) sum += w.part[2 * i * 256 + threadIdx.x];
+  for (int64_t i = cta + 1; i <= end; i += 8) {
+    float x[8];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[k] = i + k <= end ? w.part[2 * (i + k) * 256 + threadIdx.x] : 0.f;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) sum += x[k];
+  }
   const int key = pair * 256 + threadIdx.x;
   if (key >= s.len) return;
   if (float* to = weight_at(p, n, hk, key)) *to = sum;
