@@ -21,7 +21,7 @@
 // summed in fp32 before that.
 //
 // Measured (GB300): 64 sequences of up to 8192 keys 148.5 to 153 us (6.8 TB/s), one of 8191 keys
-// 10.1 us, 64 behind 16384 shared keys 53 to 58 us.
+// 10.1 to 10.7 us, 64 behind 16384 shared keys 53 to 58 us; with weights, 64 of up to 4096 keys 88 us.
 #include "attn_decode.cuh"
 
 namespace gdn {

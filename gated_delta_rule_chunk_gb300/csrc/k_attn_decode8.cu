@@ -22,7 +22,9 @@
 // fp16 ones, 104. The blocks come by TMA, two copies issued by one lane, laid out for ldmatrix by the
 // tensor map's swizzle. Rows of a block past the sequence's end come along: their scores are masked,
 // and their values, which a weight of 0 would not remove where they are NaN, are made 0 in the
-// registers.
+// registers (the second half of a block that is past the end is not looked at: its page is not loaded).
+// Measured (GB300): 64 sequences of up to 8192 keys 89 us (6.0 TB/s, the second kernel included), one
+// of 8191 keys 10.7 us, two of 20 and 40 keys 6.5 us.
 #include "attn_decode.cuh"
 #include "e4m3.cuh"
 

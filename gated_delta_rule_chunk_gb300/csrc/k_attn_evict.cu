@@ -17,7 +17,8 @@
 // bits a round, in select_long_kernel.
 //
 // The copies are rows of 64 to 256 bytes from anywhere to consecutive places. A warp takes 16
-// places of K or of V, all rows loaded side by side.
+// places of K or of V, all rows loaded side by side. Measured (GB300): 64 sequences of up to 4096
+// tokens cut to 1024, bf16, 80 us (5.6 TB/s), of which the copies alone take 65.
 #include "attn_common.cuh"
 #include "e4m3.cuh"
 
