@@ -25,8 +25,8 @@
 // Bound: a step's operands and exponentials take 1,152 cycles of shared memory (both operands of
 // an N = 128 product come from there) and 1,024 of the unit, and what passes between warps is on the
 // way from one to the other: 1,700 cycles a step measured. In front and behind stand the lookup of a
-// CTA's part, its first tiles and the sums' merge, 9 us for any call. 4096 tokens, 16 heads 36.4 us
-// (0.94 PFLOP/s of the pairs seen), 8 ragged prompts 75.6. Branches of masked tiles between the loads and
+// CTA's part, its first tiles and the sums' merge, 9 us for any call. 4096 tokens, 16 heads 37.1 us
+// (0.93 PFLOP/s of the pairs seen), 8 ragged prompts 77.2. Branches of masked tiles between the loads and
 // the exponentials of unmasked ones cost 1 us of the first, 64-bit divisions and a binary search in
 // the lookups 2. No gain: barriers of their own for the two tiles, three Q tiles, two warps that
 // issue, all of a thread's columns loaded first.
@@ -563,7 +563,6 @@ weights_tc_kernel(const AttnWeightsParams p, const WeightsParts parts,
 // if it began there.
 __global__ void __launch_bounds__(256) reduce_kernel(const AttnWeightsParams p, const WeightsParts w) {
   pdl_wait();
-  pdl_release();
   const int64_t U = w.first[p.N], grid = min((int64_t)gridDim.x + 1, U);
   const int64_t cta = blockIdx.x;
   if (cta + 1 >= grid) return;
