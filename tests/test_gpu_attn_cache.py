@@ -739,6 +739,13 @@ def test_evict_row_lengths(longest):
     run_evict([longest - 5], 2, 64, 16, 50, 0, 8, change=lambda w: (w * 3).round())
 
 
+@pytest.mark.parametrize("longest", [2048, 4096, 8192, 16384, 32768])
+def test_evict_rows_that_stay_nearly_whole(longest):
+    """Every lane of a warp keeps all of its tokens, in one go or up to the first equal ones."""
+    run_evict([longest, longest - 1], 1, 64, 256, longest - 3, 1, seed=longest)
+    run_evict([longest], 1, 64, 256, longest - 40, 0, 8, change=torch.ones_like)
+
+
 @pytest.mark.parametrize("what", ["equal", "zeros", "negative", "nan", "inf", "close", "denormal"])
 def test_evict_choices(what):
     def change(w):
