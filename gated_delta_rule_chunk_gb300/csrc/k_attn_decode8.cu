@@ -322,6 +322,9 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
             }
           }
       }
+      // A value scale that is not finite, in a half that some row may not see: its weight there is 0
+      // and not that scale's (-inf + NaN, -inf + inf). A branch, as seldom taken.
+      const bool odd = part && !(fmaxf(lv[0], lv[1]) < INFINITY && lv[0] == lv[0] && lv[1] == lv[1]);
       uint32_t pf[RN][2][2];  // the weights as the MMAs' operand: [half][8 keys]
 #pragma unroll
       for (int n = 0; n < RN; ++n) {
@@ -338,6 +341,12 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
           for (int i = 0; i < 4; ++i) {
             l[n][i & 1] += ex2(s[n][h][i] - r[i & 1]);
             y[i] = ex2(s[n][h][i] + (lv[h] - v[i & 1]));
+          }
+          if (odd) {
+            asm volatile("");
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (s[n][h][i] == -INFINITY) y[i] = 0.f;
           }
           pf[n][h][0] = transpose_8x8(pack_f16(y[0], y[1]));
           pf[n][h][1] = transpose_8x8(pack_f16(y[2], y[3]));

@@ -1215,3 +1215,39 @@ def test_a_conversation(bits):
         g1 = w.cpu().numpy()
         fin = ~np.isnan(want)
         assert np.allclose(g1[fin], want[fin], rtol=1e-4, atol=1e-6)
+
+
+# ---------------------------------------------------------------- what single calls got wrong
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("G", [1, 5, 7, 10, 15, 20])  # each number of row tiles and warps for 3 tokens
+@pytest.mark.parametrize("length", [18, 34])  # the block behind is a half of 32 keys, or 32 of its own
+def test_decode8_scales_of_later_tokens_have_no_influence(length, G, D):
+    """Row i does not see the tokens behind it, nor the scales of a block that holds only such
+    tokens: with a scale there that is no number, or infinite, row 0's output stays as it is."""
+    g = torch.Generator().manual_seed(length + G)
+    H, nq = 2 * G, 3
+    kb, ks = random_cache8(g, 3, 2, 16, D)
+    vb, vs = random_cache8(g, 3, 2, 16, D)
+    q = randn(g, 1, nq, H, D)
+    table, last = i32([[2, 0, 1]]), [2, 0, 1][length // 16]
+
+    def run(weights=None):
+        return B.gdn_attn_decode(q.cuda(), kb.cuda().view(F8), vb.cuda().view(F8), table, i32([length]),
+                                 k_scale=ks.cuda(), v_scale=vs.cuda(), out_dtype=F32, return_lse=True,
+                                 weights=weights)
+    keep = ks[last].clone()
+    want, want_lse = run()
+    assert want.isfinite().all()
+    w = torch.zeros(3, 2, 16, device="cuda")
+    run(w)
+    for bad in (float("nan"), float("inf")):
+        vs[last] = bad
+        got, lse = run()
+        assert torch.equal(got[:, 0], want[:, 0]) and torch.equal(lse, want_lse)
+        assert not got[:, 1:].isfinite().any()  # (rows that see it)
+        w2 = torch.zeros_like(w)
+        assert torch.equal(run(w2)[0][:, 0], want[:, 0]) and torch.equal(w2, w)
+        ks[last] = bad
+        got, lse = run()
+        assert torch.equal(got[:, 0], want[:, 0]) and torch.equal(lse[:, 0], want_lse[:, 0])
+        ks[last] = keep
