@@ -13,8 +13,8 @@
 // tokens a lane 17.4 us, 4 and the rounds' first bit from the ends 16.4). A histogram of 8 bits a
 // pass took ten times as long as the rounds, as weights share their exponents and most of a
 // warp's additions went to one counter.
-// Rows longer than the registers of a CTA hold (kThreads * 32 tokens) are read again each round, 8
-// bits a round, in select_long_kernel.
+// Rows longer than the registers of a CTA hold (kSelect * 32 tokens) are read again each round, 8
+// bits a round (select_long_row).
 //
 // The copies are rows of 64 to 256 bytes from anywhere to consecutive places. A warp takes 16
 // places of K or of V, all rows loaded side by side. Measured (GB300): 64 sequences of up to 4096
@@ -58,17 +58,12 @@ __device__ __forceinline__ bool easy_part(const AttnEvictParams& p, int n, int h
   return k == 0;
 }
 
-// E tokens a thread, kT threads.
+// The k largest of the first M weights of a row, which kT threads hold, E each.
 template <int E, int kT>
-__global__ void __launch_bounds__(kT, E == 32 ? 1 : (E == 8 ? 1536 : 1024) / kT) select_kernel(const AttnEvictParams p, bool wide) {
+__device__ __forceinline__ void select_row(const AttnEvictParams& p, int n, int hk, int32_t* kept, int M,
+                                           int k, bool wide) {
   __shared__ uint32_t counts[2][32], ends[2][32], list[kList], listed, found[2];
-  const int n = blockIdx.x / p.Hk, hk = blockIdx.x - n * p.Hk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  pdl_release();
-  int32_t* kept = p.kept + (size_t)blockIdx.x * p.keep;
-  int M, k;
-  if (easy_part(p, n, hk, kept, M, k)) return;
   if (tid == 0) listed = 0;
   // (8 values: 8 consecutive ones, one lookup; 64 sequences of up to 4096 80.0 us, with 4 80.7.)
   // This thread's tokens: V from i0 + 32 V c on, for each c; 0 stands for what is past the end (no
@@ -239,16 +234,24 @@ __global__ void __launch_bounds__(kT, E == 32 ? 1 : (E == 8 ? 1536 : 1024) / kT)
   }
 }
 
-__global__ void __launch_bounds__(kSelect) select_long_kernel(const AttnEvictParams p) {
+template <int E, int kT>
+__global__ void __launch_bounds__(kT, E == 32 ? 1 : (E == 8 ? 1536 : 1024) / kT)
+select_kernel(const AttnEvictParams p, bool wide) {
+  const int n = blockIdx.x / p.Hk, hk = blockIdx.x - n * p.Hk;
+  pdl_wait();
+  pdl_release();
+  int32_t* kept = p.kept + (size_t)blockIdx.x * p.keep;
+  int M, k;
+  if (!easy_part(p, n, hk, kept, M, k)) select_row<E, kT>(p, n, hk, kept, M, k, wide);
+}
+
+// The same for a row of any length, whose weights are read again each round.
+__device__ __forceinline__ void select_long_row(const AttnEvictParams& p, int n, int hk, int32_t* kept, int M,
+                                                int k) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t found[2];
   __shared__ uint32_t sums[2][kSelect / 32];
-  const int n = blockIdx.x / p.Hk, hk = blockIdx.x - n * p.Hk;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  pdl_wait();
-  int32_t* kept = p.kept + (size_t)blockIdx.x * p.keep;
-  int M, k;
-  if (easy_part(p, n, hk, kept, M, k)) return;
   auto bits = [&](int i) -> uint32_t {
     const int page = p.table[(size_t)n * p.max_pages + (i >> p.page_shift)];
     if (page < 0 || page >= p.n_pages) return order_bits(0.f);
@@ -304,6 +307,23 @@ __global__ void __launch_bounds__(kSelect) select_long_kernel(const AttnEvictPar
     equal += s_all;
     __syncthreads();
   }
+}
+
+// For a table wider than registers hold: what a row takes goes by its own length, which the host does
+// not know. (With a table of 131072 tokens: 64 sequences of up to 600 cut to 256 33.5 us, all of them by
+// select_long_row 49.5; 64 of up to 4096 cut to 1024 91.2 and 125.6; one of 16383 16.8 and 63.6; two of
+// 30000 28.7 and 104.8. Two of 50000 to 100000 take 270.)
+__global__ void __launch_bounds__(kSelect) select_any_kernel(const AttnEvictParams p, bool wide) {
+  const int n = blockIdx.x / p.Hk, hk = blockIdx.x - n * p.Hk;
+  pdl_wait();
+  pdl_release();
+  int32_t* kept = p.kept + (size_t)blockIdx.x * p.keep;
+  int M, k;
+  if (easy_part(p, n, hk, kept, M, k)) return;
+  if (M <= 8 * kSelect) select_row<8, kSelect>(p, n, hk, kept, M, k, wide);
+  else if (M <= 16 * kSelect) select_row<16, kSelect>(p, n, hk, kept, M, k, wide);
+  else if (M <= 32 * kSelect) select_row<32, kSelect>(p, n, hk, kept, M, k, wide);
+  else select_long_row(p, n, hk, kept, M, k);
 }
 
 template <int kRow, bool k8>
@@ -400,7 +420,7 @@ bool launch_attn_evict(const AttnEvictParams& p, cudaStream_t s) {
       : most <= 8192  ? launch_pdl(select_kernel<16, 512>, rows, dim3(512), 0, s, p, wide)
       : most <= 16384 ? launch_pdl(select_kernel<16, 1024>, rows, dim3(1024), 0, s, p, wide)
       : most <= 32768 ? launch_pdl(select_kernel<32, 1024>, rows, dim3(1024), 0, s, p, wide)
-                      : launch_pdl(select_long_kernel, rows, dim3(kSelect), 0, s, p);
+                      : launch_pdl(select_any_kernel, rows, dim3(kSelect), 0, s, p, wide);
   if (e != cudaSuccess) return false;
   const int64_t items = (int64_t)p.N * p.Hk * ((p.keep + kBlock8 - 1) / kBlock8) * 2;
   const dim3 grid((unsigned)((items + kMoveWarps - 1) / kMoveWarps)), block(kMoveWarps * 32);

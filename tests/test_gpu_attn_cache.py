@@ -1251,3 +1251,33 @@ def test_decode8_scales_of_later_tokens_have_no_influence(length, G, D):
         got, lse = run()
         assert torch.equal(got[:, 0], want[:, 0]) and torch.equal(lse[:, 0], want_lse[:, 0])
         ks[last] = keep
+
+
+def evict_called_with(monkeypatch, columns=0, skew=0):
+    """The calls that follow get page tables of at least `columns` columns, and weights that begin
+    `skew` floats past a 16-byte boundary."""
+    real = B.gdn_attn_evict
+
+    def call(k, v, w, table, *rest, **kw):
+        wide = torch.full((table.shape[0], max(columns, table.shape[1])), -1, dtype=torch.int32, device="cuda")
+        wide[:, :table.shape[1]] = table
+        room = torch.empty(w.numel() + 4, device="cuda")
+        there = room[skew:skew + w.numel()].view(w.shape)
+        assert room.data_ptr() % 16 == 0
+        there.copy_(w)
+        out = real(k, v, there, wide, *rest, **kw)
+        w.copy_(there)
+        return out
+    monkeypatch.setattr(B, "gdn_attn_evict", call)
+
+
+def test_evict_rows_of_any_length_in_a_wide_table(monkeypatch):
+    """What a row takes goes by its own length: either side of each change, in one call."""
+    evict_called_with(monkeypatch, columns=200)  # of 256 tokens
+    for recent in (0, 17):
+        run_evict([300, 0, 8192 + recent, 8193 + recent, 32768 + recent, 32769 + recent, 250, 251], 1, 64, 256, 250,
+                  recent, seed=recent)
+    run_evict([40000, 9, 33000], 2, 64, 256, 9000, 100, 8, change=lambda w: (w * 3).round())
+    run_evict([8000, 32000], 1, 64, 256, 7990, 0, change=torch.ones_like)
+    evict_called_with(monkeypatch, columns=2049)  # of 16 tokens
+    run_evict([700, 100, 513, 9000], 2, 64, 16, 90, 7)
