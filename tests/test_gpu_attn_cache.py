@@ -1281,3 +1281,42 @@ def test_evict_rows_of_any_length_in_a_wide_table(monkeypatch):
     run_evict([8000, 32000], 1, 64, 256, 7990, 0, change=torch.ones_like)
     evict_called_with(monkeypatch, columns=2049)  # of 16 tokens
     run_evict([700, 100, 513, 9000], 2, 64, 16, 90, 7)
+
+
+@pytest.mark.parametrize("skew", [1, 2, 3])
+def test_evict_weights_that_begin_anywhere(monkeypatch, skew):
+    """Weights are 4-byte aligned; from a 16-byte boundary on they are read four at a time, else singly."""
+    evict_called_with(monkeypatch, skew=skew)
+    for longest in (2048, 4096, 8192, 16384, 32768):
+        run_evict([longest, 9, longest - 1, longest // 2 + 3], 1, 64, 256, longest // 3, 17, seed=longest)
+    run_evict([700, 100, 513], 2, 64, 16, 90, 7, 8)
+    evict_called_with(monkeypatch, columns=200, skew=skew)
+    run_evict([8000, 9000, 17000, 33000, 40], 1, 64, 256, 50, 7)
+
+
+@pytest.mark.parametrize("bits", [8, 16])
+def test_weights_that_begin_anywhere(monkeypatch, bits):
+    """As above, of a decode step and of a prompt."""
+    decode, prompt = B.gdn_attn_decode, B.gdn_attn_prefill_weights
+
+    def skewed(w):
+        room = torch.empty(w.numel() + 4, device="cuda")
+        there = room[1:1 + w.numel()].view(w.shape)
+        there.copy_(w)
+        return there
+
+    def step(*a, weights=None, **kw):
+        there = skewed(weights)
+        out = decode(*a, weights=there, **kw)
+        weights.copy_(there)
+        return out
+
+    def whole(q, k, lse, weights, *a, **kw):
+        there = skewed(weights)
+        prompt(q, k, lse, there, *a, **kw)
+        weights.copy_(there)
+    monkeypatch.setattr(B, "gdn_attn_decode", step)
+    monkeypatch.setattr(B, "gdn_attn_prefill_weights", whole)
+    run_decode([70, 1, 150], 6, 2, 64, 16, bits=bits, weights=True)
+    run_decode([5, 33, 100], 4, 2, 128, 32, nq=4, bits=bits, weights=True)
+    run_prompt([300, 20], 4, 2, 128)
