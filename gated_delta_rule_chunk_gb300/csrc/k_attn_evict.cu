@@ -83,6 +83,7 @@ __device__ __forceinline__ void select_row(const AttnEvictParams& p, int n, int 
   for (int c = 0; c < C; ++c) {
     const float* w = p.weights + ((((int64_t)page[c] * p.Hk + hk) << p.page_shift) +
                                   ((i0 + c * 32 * V) & (p.page - 1)));
+    if (i0 + c * 32 * V < M && (page[c] < 0 || page[c] >= p.n_pages)) set_status(p.status, GDN_DEV_BAD_PAGE_TABLE);
 #pragma unroll
     for (int e = 0; e < V / 4; ++e) {
       x[c * V / 4 + e] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -254,7 +255,10 @@ __device__ __forceinline__ void select_long_row(const AttnEvictParams& p, int n,
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   auto bits = [&](int i) -> uint32_t {
     const int page = p.table[(size_t)n * p.max_pages + (i >> p.page_shift)];
-    if (page < 0 || page >= p.n_pages) return order_bits(0.f);
+    if (page < 0 || page >= p.n_pages) {
+      set_status(p.status, GDN_DEV_BAD_PAGE_TABLE);
+      return order_bits(0.f);
+    }
     return order_bits(p.weights[(((size_t)page * p.Hk + hk) << p.page_shift) + (i & (p.page - 1))]);
   };
   uint32_t prefix = 0, want = k;  // want: of the values that agree with prefix

@@ -257,8 +257,9 @@ size_t gdn_attn_prefill_weights_workspace_size(const gdn_attn_desc* desc);
  *   kept         [N, Hk, keep] int32, the places that the tokens had; -1 past new_lens[n]
  * Tokens differ from head to head, so a place holds several tokens; rotary positions are in the
  * keys already. T, H and dtypes of desc are not looked at beyond gdn_attn_check_desc. Keys and
- * values of a page outside [0, n_pages) are zeros of weight 0, and what would go to such a page
- * goes nowhere (GDN_DEV_BAD_PAGE_TABLE).
+ * values of a page outside [0, n_pages) are zeros of weight 0 (GDN_DEV_BAD_PAGE_TABLE where a weight
+ * of the page is looked at or a token of it stays), and what would go to such a page goes nowhere
+ * (GDN_DEV_BAD_PAGE_TABLE).
  */
 int gdn_attn_evict(const gdn_attn_desc* desc, void* k_cache, void* v_cache, float* k_scale,
                    float* v_scale, float* weights, const int32_t* page_table,

@@ -1320,3 +1320,21 @@ def test_weights_that_begin_anywhere(monkeypatch, bits):
     run_decode([70, 1, 150], 6, 2, 64, 16, bits=bits, weights=True)
     run_decode([5, 33, 100], 4, 2, 128, 32, nq=4, bits=bits, weights=True)
     run_prompt([300, 20], 4, 2, 128)
+
+
+@pytest.mark.parametrize("longest", [600, 3000, 8000, 16000, 32000, 40000])
+def test_evict_pages_that_do_not_exist_are_reported_where_nothing_of_them_stays(longest):
+    page, keep, recent = 256, 20, 4
+    cols = -(-longest // page)
+    for bad in (-1, cols + 1):
+        table = torch.arange(cols, dtype=torch.int32)[None].cuda()
+        k = torch.ones(cols + 1, 1, page, 64, dtype=BF, device="cuda")
+        w = torch.rand(cols + 1, 1, page, device="cuda") + 1
+        w[cols - 2] += 2  # the tokens that stay are of this page, the last ones of the last
+        status = new_status()
+        run = lambda: B.gdn_attn_evict(k, k, w, table, i32([longest]), i32([[cols]]), keep, recent, status=status)
+        want = run()[1]
+        assert status.item() == 0
+        table[0, 0] = bad
+        got = run()[1]
+        assert status.item() == 64 and torch.equal(got, want)
