@@ -488,16 +488,19 @@ PyObject* evict(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const int32_t *ptable = static_cast<int32_t*>(address(&table, "page_table", kI32, {N, table.size(1)})),
                 *pkv = static_cast<int32_t*>(address(&kv, "kv_lens", kI32, {N})),
                 *pnew = static_cast<int32_t*>(address(&fresh, "new_table", kI32, {N, fresh.size(1)}));
-  const int32_t recent = i32(number(a[7]));
+  const int32_t keep32 = i32(keep), recent = i32(number(a[7])), new_max = i32(fresh.size(1));
+  // (before `kept` is allocated, whose size goes by `keep`)
+  int rc = f_check(&d);
+  if (rc == GDN_OK && (recent < 0 || recent > keep || keep > (int64_t)new_max * page)) rc = GDN_ERR_BAD_SHAPE;
+  if (rc != GDN_OK) fail(rc, "gdn_attn_evict");
   address(tensor(a[10], "new_lens"), "new_lens", kI32, {N});
   address(tensor(a[11], "kept"), "kept", kI32, {N, Hk, keep});
   const Place place(a[13], kc);
   at::Tensor lens = made(a[10], "new_lens", {N}, kI32, kc, place),
              kept = made(a[11], "kept", {N, Hk, keep}, kI32, kc, place);
   place.order();
-  const int rc = f_evict(&d, pk, pv, pks, pvs, pw, ptable, pkv, pnew, i32(fresh.size(1)), i32(keep),
-                         recent, static_cast<int32_t*>(lens.data_ptr()),
-                         static_cast<int32_t*>(kept.data_ptr()), place.stream);
+  rc = f_evict(&d, pk, pv, pks, pvs, pw, ptable, pkv, pnew, new_max, keep32, recent,
+               static_cast<int32_t*>(lens.data_ptr()), static_cast<int32_t*>(kept.data_ptr()), place.stream);
   if (rc != GDN_OK) fail(rc, "gdn_attn_evict");
   PyObject* r = PyTuple_New(2);
   if (!r) throw python_error();

@@ -312,3 +312,16 @@ def test_binding_refuses_other_arguments():
     shapes, rest = cases()["evict"]
     with pytest.raises(ValueError, match="keep"):
         B.gdn_attn_evict(**tensors(shapes), keep=0)
+
+
+@pytest.mark.parametrize("change, error, text", [
+    (dict(keep=33), B.GdnError, "gdn_attn_evict"), (dict(keep=1 << 30), B.GdnError, "gdn_attn_evict"),
+    (dict(keep=1 << 40), ValueError, "32 bits"), (dict(recent=21), B.GdnError, "gdn_attn_evict"),
+    (dict(recent=-1), B.GdnError, "gdn_attn_evict"),
+])
+def test_evict_refuses_a_budget_before_it_allocates(lib, change, error, text):
+    """`kept` goes by the budget: one that the new pages do not hold is refused, not asked for."""
+    shapes, _ = cases()["evict"]
+    given = {n: x for n, x in shapes.items() if n not in ("new_lens", "kept")}
+    with pytest.raises(error, match=text):
+        B.gdn_attn_evict(**tensors(given), **{**dict(keep=20), **change})
