@@ -347,6 +347,10 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   const float *pks = static_cast<float*>(address(ks, "k_scale", kF32, {pages, Hk, page / 16})),
               *pvs = static_cast<float*>(address(vs, "v_scale", kF32, {pages, Hk, page / 16}));
   float* pw = static_cast<float*>(address(weights, "weights", kF32, {pages, Hk, page}));
+  const int32_t shared = i32(number(a[5]));
+  const float scale = (float)real(a[6]);
+  // (before the workspace is allocated, which holds the scores of all keys)
+  if (weights && shared > 0) fail(GDN_ERR_UNSUPPORTED, "gdn_attn_decode");
   const Place place(a[13], q);
   at::Tensor out = made(a[8], "out", q.sizes(), to, q, place), lse, work;
   const at::IntArrayRef rows = q.sizes().slice(0, q.dim() - 1);
@@ -364,8 +368,6 @@ PyObject* decode(PyObject*, PyObject* const* a, Py_ssize_t n) {
   place.order();
   void* po = address(&out, "out", to, q.sizes());
   float* pl = static_cast<float*>(address(want_lse ? &lse : nullptr, "lse", kF32, rows));
-  const int32_t shared = i32(number(a[5]));
-  const float scale = (float)real(a[6]);
   const int rc = ks || vs || weights
                      ? f_decode_cache(&d, pq, pk, pv, pks, pvs, ptable, pkv, shared, scale, po, pl, pw,
                                       place.stream)

@@ -325,3 +325,14 @@ def test_evict_refuses_a_budget_before_it_allocates(lib, change, error, text):
     given = {n: x for n, x in shapes.items() if n not in ("new_lens", "kept")}
     with pytest.raises(error, match=text):
         B.gdn_attn_evict(**tensors(given), **{**dict(keep=20), **change})
+
+
+def test_decode_refuses_weights_behind_a_prefix_before_it_allocates(lib):
+    """The workspace holds the scores of all keys: not asked for by a call that is refused."""
+    shapes, _ = cases()["decode"]
+    a = tensors({n: x for n, x in shapes.items() if n not in ("k_scale", "v_scale")} |
+                {n: (shapes[n][0], torch.bfloat16) for n in ("k_cache", "v_cache")})
+    with pytest.raises(B.GdnError, match="gdn_attn_decode"):
+        B.gdn_attn_decode(**a, shared_len=32)
+    with pytest.raises(B.GdnError, match="gdn_attn_decode"):
+        B.gdn_attn_decode(**tensors(shapes), shared_len=32)
