@@ -1338,3 +1338,43 @@ def test_evict_pages_that_do_not_exist_are_reported_where_nothing_of_them_stays(
         table[0, 0] = bad
         got = run()[1]
         assert status.item() == 64 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("nq, G", [(1, 4), (3, 2), (4, 8), (8, 8)])  # one, two and four row tiles
+def test_decode_with_weights_keeps_sixteen_bits_of_them(nq, G, D):
+    """Over a bf16 cache, 32-bit outputs. Each weight goes into the product in two bf16 parts, off by
+    2^-16 of it at most; scores and exp add weight_slack's part (that amount for the weight, as much for
+    its denominator), sums in 32 bits of at most 64 products a part and their merge 2^-18. The weights
+    rounded to bf16 alone (2^-9 each) would pass it."""
+    g = torch.Generator().manual_seed(nq + D)
+    H, page, lens = 2 * G, 16, [nq + 2, 9, 33, 64]
+    N = len(lens)
+    q = randn(g, N, nq, H, D, mul=0.2)
+    table, n_pages, _ = pages_for(g, [-(-n // page) for n in lens], 1)
+    k, v = randn(g, n_pages, 2, page, D), randn(g, n_pages, 2, page, D)
+    w = torch.zeros(n_pages, 2, page, device="cuda")
+    out = B.gdn_attn_decode(q.cuda(), k.cuda(), v.cuda(), table.cuda(), i32(lens), out_dtype=F32, weights=w)
+    ref, mag, _ = A.decode(np64(q), np64(k), np64(v), table.numpy(), lens)
+    tol = 2.0 ** -16 + 2.0 ** -18 + 2 * weight_slack(q, np64(k), D, D ** -0.5)
+    assert tol < 2.0 ** -11
+    assert (np.abs(np64(out) - ref) <= tol * mag + 1e-9).all()
+
+
+@pytest.mark.parametrize("nq", [1, 3])
+def test_decode_with_weights_over_infinite_values(nq):
+    """An infinite value is infinite for the rows that see it, whatever the bits of its weight (equal
+    scores here: weights of 1, which leave no rest), and nothing for the others."""
+    g = torch.Generator().manual_seed(3)
+    k, v = torch.zeros(2, 1, 16, 64, dtype=BF), randn(g, 2, 1, 16, 64)
+    table, w = i32([[1, 0]]), torch.zeros(2, 1, 16, device="cuda")
+    q = randn(g, 1, nq, 2, 64)
+    for scores in (0.0, 1.0):
+        k[:] = scores * randn(g, 2, 1, 16, 64)
+        x = v.clone()
+        x[1, 0, 3, 5], x[1, 0, 9, 6], x[0, 0, 3, 7] = float("inf"), float("-inf"), float("inf")
+        out = B.gdn_attn_decode(q.cuda(), k.cuda(), x.cuda(), table, i32([20]), out_dtype=F32, weights=w)
+        assert (out[..., 5] == float("inf")).all() and (out[..., 6] == float("-inf")).all()
+        assert (out[0, -1, :, 7] == float("inf")).all() and out[0, :-1, :, 7].isfinite().all()
+        rest = [c for c in range(64) if c not in (5, 6, 7)]
+        assert out[..., rest].isfinite().all()
