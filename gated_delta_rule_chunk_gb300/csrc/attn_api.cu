@@ -342,7 +342,7 @@ int gdn_attn_evict(const gdn_attn_desc* desc, void* k_cache, void* v_cache, floa
   p.N = d.N; p.Hk = d.Hk; p.D = d.D;
   p.page = d.page_size; p.page_shift = log2_of(d.page_size);
   p.n_pages = d.n_pages; p.max_pages = d.max_pages; p.new_max = new_max_pages;
-  p.keep = keep; p.recent = recent; p.row = d.D * (k_scale ? 1 : 2);
+  p.keep = keep; p.recent = recent;
   p.kc = static_cast<char*>(k_cache); p.vc = static_cast<char*>(v_cache);
   p.ks = k_scale; p.vs = v_scale; p.weights = weights;
   p.table = page_table; p.kv_lens = kv_lens; p.new_table = new_table;

@@ -1,5 +1,4 @@
-// Shared definitions of the softmax-attention kernels (include/gdn_attn.h): launch
-// parameters and the sequence lookup.
+// Shared definitions of the softmax-attention kernels (include/gdn_attn.h): launch parameters.
 #pragma once
 
 #include "../../include/gdn_attn.h"
@@ -60,7 +59,6 @@ struct AttnWeightsParams {
 
 struct AttnEvictParams {
   int N, Hk, D, page, page_shift, n_pages, max_pages, new_max, keep, recent;
-  int row;                  // bytes of a key
   char* kc;
   char* vc;
   float* ks;                // or null: bf16
@@ -128,30 +126,6 @@ __device__ __forceinline__ int seq_len(const AttnParams& p, int n) {
 }
 __device__ __forceinline__ int keys_seen(const AttnParams& p, int n, int i) {
   return max(seq_len(p, n) - p.nq + i + 1, 0);
-}
-
-// Sequence n of token t and its [cu[n], cu[n + 1]); n = -1 outside every sequence. The guess
-// n = t is right in a decode step (one token each), where it saves the search's loads.
-__device__ __forceinline__ int find_seq(const int32_t* cu, int N, int T, int t, int& b, int& e) {
-  if (!cu) {
-    b = 0;
-    e = T;
-    return 0;
-  }
-  int n = min(t, N - 1);
-  b = cu[n];
-  e = cu[n + 1];
-  if (b <= t && t < e) return n;
-  int lo = 0, hi = N;  // the last entry <= t lies in [lo, hi]
-  while (lo < hi) {
-    const int m = (lo + hi + 1) >> 1;
-    if (cu[m] <= t) lo = m;
-    else hi = m - 1;
-  }
-  if (lo >= N) return -1;
-  b = cu[lo];
-  e = cu[lo + 1];
-  return b <= t && t < e && b >= 0 && e <= T ? lo : -1;
 }
 
 // One lane's D / 32 output columns of row `row` (a [rows, D] array).

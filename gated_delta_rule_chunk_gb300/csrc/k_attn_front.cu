@@ -50,6 +50,30 @@ __device__ __forceinline__ void store4(void* x, size_t at, const float* y) {
   }
 }
 
+// Sequence n of token t and its [cu[n], cu[n + 1]); n = -1 outside every sequence. The guess
+// n = t is right in a decode step (one token each), where it saves the search's loads.
+__device__ __forceinline__ int find_seq(const int32_t* cu, int N, int T, int t, int& b, int& e) {
+  if (!cu) {
+    b = 0;
+    e = T;
+    return 0;
+  }
+  int n = min(t, N - 1);
+  b = cu[n];
+  e = cu[n + 1];
+  if (b <= t && t < e) return n;
+  int lo = 0, hi = N;  // the last entry <= t lies in [lo, hi]
+  while (lo < hi) {
+    const int m = (lo + hi + 1) >> 1;
+    if (cu[m] <= t) lo = m;
+    else hi = m - 1;
+  }
+  if (lo >= N) return -1;
+  b = cu[lo];
+  e = cu[lo + 1];
+  return b <= t && t < e && b >= 0 && e <= T ? lo : -1;
+}
+
 // 1 / sqrt(x): rsqrtf is good to 2 ulp, one Newton step brings it to rounding (not from 0, the
 // result for infinity, which the step would make NaN).
 __device__ __forceinline__ float inv_sqrt(float x) {

@@ -37,7 +37,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], u
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// Barrier over `count` threads (a multiple of 32) with hardware barrier `id` (1..15).
 // The transpose of an 8 x 8 matrix of 16-bit elements: lane l holds row l / 4, elements 2 (l % 4) and
 // the next, before and after.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
@@ -45,6 +44,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;\n" : "=r"(y) : "r"(x));
   return y;
 }
+
+// Barrier over `count` threads (a multiple of 32) with hardware barrier `id` (1..15).
 __device__ __forceinline__ void named_sync(int id, int count) {
   asm volatile("bar.sync %0, %1;\n" ::"r"(id), "r"(count) : "memory");
 }
