@@ -645,8 +645,10 @@ def gdn_attn_decode(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     With k_scale and v_scale (fp32 [n_pages, Hk, page_size / 16]) the caches are in 8 bits
     (torch.float8_e4m3fn, see gdn_attn_append8). With `weights` (fp32 [n_pages, Hk, page_size])
     each key's softmax weights, summed over the call's rows and its group's query heads, are added
-    there; the call's own tokens are set to theirs (shared_len must be 0 then). A workspace is
-    gdn_attn_decode_cache_workspace_size bytes with either."""
+    there; the call's own tokens are set to theirs (shared_len must be 0 then). What rows of tokens
+    that are rejected afterwards gave to older keys stays there. A workspace is
+    gdn_attn_decode_cache_workspace_size bytes with either; with weights that is some 4 bytes a query
+    row, head and token of the page table's width."""
     return (_attn_module or _attn()).decode(
         q, k_cache, v_cache, page_table, kv_lens, shared_len, scale, out_dtype, out, return_lse,
         lse, workspace, status, None if stream is None else stream.cuda_stream, k_scale, v_scale,

@@ -331,8 +331,8 @@ combine_kernel(const AttnParams p, const DecodeParts w) {
 // page, scores, weights) for a few pieces a warp, so the next piece's loads are issued before this
 // one's are used; and the instructions of a piece: the rows' denominators are one load, handed out by
 // shuffles, and a place in the list comes from the one before it. 64 sequences of up to 4096 keys,
-// bf16: 87.7 us with weights, 79.5 without (a load for each row's denominator, divisions for each
-// place: 92.2); 8 x 4 tokens in 8 bits 23.5 and 17.2.
+// bf16: 87.5 us with weights, 79.5 without (a load for each row's denominator, divisions for each
+// place: 5 us more); 8 x 4 tokens in 8 bits 23.6 and 17.4.
 // kRows rows are loaded side by side.
 template <int kUnit, int kRows>
 __global__ void __launch_bounds__(256, 3) weights_kernel(const AttnParams p, const DecodeParts w) {

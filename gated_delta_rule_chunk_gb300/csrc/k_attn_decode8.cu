@@ -174,7 +174,7 @@ decode8_kernel(const AttnParams p, const DecodeParts w, const __grid_constant__ 
     for (int x = 0; x < 2; ++x) lim_off[n][x] = p.nq - 1 - min((row0 + 8 * n + x) / p.G, p.nq - 1);
   // This warp's rows of the queries of the pair at `cur`, in fp16: times a power of two, by the
   // row's largest element, that puts it below 2^15; elements are then exact down to 2^-29 of it, and
-  // below that off by 2^-40 of it at most. Row k of the MMAs' operand is element 4 (k / 2) + k % 2 of
+  // below that off by 2^-40 of it at most (in rows whose largest is below 2^-86, off by 2^-125). Row k of the MMAs' operand is element 4 (k / 2) + k % 2 of
   // 16, row 8 + k the one 2 further on: so a lane's 4 bytes of a key are two of its operands.
   auto load_q = [&] {
 #pragma unroll
@@ -499,9 +499,12 @@ bool launch(AttnParams p, void* workspace, cudaStream_t s) {
     return launch_pdl(kernel, dim3(w.grid), dim3(kWarps * 32), smem, s, p, w, tm_k, tm_v) == cudaSuccess;
   };
   // (More than 16 rows: warps with 24 each where that leaves fewer rows empty, with the registers of
-  // two CTAs an SM in place of three: 64 sequences of 2000 to 4000 keys, head size 128, 24 rows 77.9 us,
-  // as two warps with 16 87.1; 40 rows 120.5 and 144.7; one of 8000 keys, 40 rows, 20.6 and 23.0, but
-  // 17.9 and 16.9 at head size 64. Else several with 16, which convert the same keys. One warp with 32
+  // two CTAs an SM in place of three; else several with 16, which convert the same keys. 24 a warp and
+  // 16, us, 64 sequences of 2000 to 4000 keys, 8 key heads: head size 128, 24 rows 147.4 and 164.0, 40 rows
+  // 234.5 and 281.6; head size 64, 24 rows 108.0 and 115.3, 40 rows 177.2 and 197.2. Four of 4000 to 8000,
+  // 4 key heads, head size 64, 40 rows: 22.7 and 23.9. One of 8000: head size 128, 40 rows 20.8 and 23.3;
+  // head size 64, 24 rows 12.7 and 13.4, but 33 to 48 rows 17.6 to 17.9 and 16.5 to 17.4, the rule's one
+  // point on the wrong side: which batches come next to it the host cannot see. One warp with 32
   // rows has too few registers for its sums: 96 sequences, 32 rows, 30 us and 52 with 407 to 814 keys
   // of head size 128, 86 and 162 with 4000 to 8000 of 64.)
   const bool ok = R <= 8    ? go(decode8_kernel<D, 1, 1, kScores>, Smem8<D, 1>::kBytes)

@@ -15,9 +15,10 @@
 // prompts; latency (cu_seqlens -> kv_lens -> page table and rotary row -> store, x loaded
 // meanwhile) for a decode step. Measured (GB300): 8 prompts to 2048 in 32 bits 27.3 us (6.2 TB/s),
 // 4096 tokens in bf16 with dense and cached k and v 12.1 us (3.9 TB/s: 8-byte accesses and their
-// latency at 16 warps an SM), one token 2.3 us; with positions of three axes 13.4 and, 64 tokens, 3.2
-// us (one more dependent read; cos and sin of a block's tokens looked up once, through shared memory,
-// 14.2 and a microsecond more for 64 tokens).
+// latency at 16 warps an SM), one token 2.3 us; with positions of three axes 13.5 (both with x and the
+// cache in L2 from the call before; from HBM 16.0) and, 64 tokens, 3.2 us (one more dependent read; cos
+// and sin of a block's tokens looked up once, through shared memory, 14.2 and a microsecond more for 64
+// tokens).
 #include "attn_common.cuh"
 
 namespace gdn {

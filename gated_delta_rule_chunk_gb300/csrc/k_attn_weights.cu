@@ -22,13 +22,14 @@
 // Columns that a key does not count (rows before it or before the window, past the sequence's end)
 // are selected away in the tiles that have any; a row there may hold anything.
 //
-// Bound: a step's operands and exponentials take 1,152 cycles of shared memory (both operands of
-// an N = 128 product come from there) and 1,024 of the unit, and what passes between warps is on the
-// way from one to the other: 1,700 cycles a step measured. In front and behind stand the lookup of a
-// CTA's part, its first tiles and the sums' merge, 9 us for any call. 4096 tokens, 16 heads 37.1 us
-// (0.93 PFLOP/s of the pairs seen), 8 ragged prompts 77.2. Branches of masked tiles between the loads and
-// the exponentials of unmasked ones cost 1 us of the first, 64-bit divisions and a binary search in
-// the lookups 2. No gain: barriers of their own for the two tiles, three Q tiles, two warps that
+// Bound: a step's operands take 1,152 cycles of shared memory (both of an N = 128 product come from
+// there) and the Q tile that TMA writes there 256 more, its exponentials 1,024 of their unit, and what
+// passes between warps is on the way from one to the other: 1,700 cycles a step measured. In front and
+// behind stand the lookup of a CTA's part, its first tiles and the sums' merge, 9 us for any call. 4096
+// tokens, 16 heads 37.1 us (0.93 PFLOP/s of the pairs seen), 8 ragged prompts 77.2; from the last 64 rows
+// of each alone 12.9 and 23.9; a prompt of 100 9.4. Branches of masked tiles between the loads and the
+// exponentials of unmasked ones cost 1 us of the first, 64-bit divisions and a binary search in the
+// lookups 2. No gain: barriers of their own for the two tiles, three Q tiles, two warps that
 // issue, all of a thread's columns loaded first.
 #include "attn_tc.cuh"
 
